@@ -1,4 +1,5 @@
-"""ctypes binding of libmxgemm.so: the C ABI of include/mxgemm.h, same names.
+"""ctypes binding of libmxgemm.so: the C ABI of include/mxgemm.h and
+include/mxdecode.h, same names.
 
 Argument marshalling only: every step of the hot path runs in the HIP
 library. Device buffers may be passed as torch tensors (their data_ptr is
@@ -18,6 +19,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 # sanitizer build of the ABI tests); the default is the in-tree build.
 LIB_PATH = os.environ.get("MXG_LIBRARY") or os.path.join(_PKG, "lib", "libmxgemm.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mxgemm.h")
+DECODE_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mxdecode.h")
 
 OK = 0
 EINVAL = -1
@@ -42,6 +44,15 @@ NOALLOC_PAIR_BYTES = 4 << 20
 WS_EPOCH, WS_ERROR = 0, 2
 ERR_COLLECT_SPIN = 0x1
 ERR_SPLITK_SPIN = 0x2
+
+ROUTE_SOFTMAX, ROUTE_SIGMOID = 0, 1
+F32, BF16 = 0, 1
+ROUTE_MAX_EXPERTS = 1024
+ROUTE_MAX_GROUPS = 64
+ROUTE_MAX_TOP_K = 32
+MOE_MAX_EXPERTS = 1024
+MOE_MAX_PAIRS = 1024
+LORA_MAX_RANK = 128
 
 
 class MxgError(Exception):
@@ -73,6 +84,30 @@ class mxg_mailbox(ctypes.Structure):
         ("capacity_bytes", ctypes.c_int64),
         ("spin_limit", ctypes.c_uint32),
         ("reserved", ctypes.c_uint32),
+    ]
+
+
+class mxmoe_router(ctypes.Structure):
+    _fields_ = [
+        ("experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_best", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class mxg_lora(ctypes.Structure):
+    _fields_ = [
+        ("a", ctypes.c_void_p),
+        ("b", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("ids", ctypes.c_void_p),
+        ("adapters", ctypes.c_int32),
+        ("rank", ctypes.c_int32),
     ]
 
 
@@ -119,6 +154,17 @@ def _load() -> ctypes.CDLL:
         "mxg_graph_launch": (ctypes.c_int, [vp, vp]),
         "mxg_graph_destroy": (ctypes.c_int, [vp]),
         "mxg_strerror": (ctypes.c_char_p, [ctypes.c_int]),
+        "mxmoe_route": (ctypes.c_int, [ctypes.POINTER(mxmoe_router), vp, i32, i64, vp, i32, vp,
+                                       vp, vp]),
+        "mxmoe_packed_weight_bytes": (sz, [i32, i32, i32]),
+        "mxmoe_packed_scale_bytes": (sz, [i32, i32, i32]),
+        "mxmoe_pack_weight": (ctypes.c_int, [vp, vp, i32, i32, i32, vp, vp, vp]),
+        "mxmoe_workspace_bytes": (sz, [i32, i32, i32, i32]),
+        "mxmoe_experts": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp,
+                                         sz, vp, vp]),
+        "mxgemm_lora_scratch_bytes": (sz, [i32, i32]),
+        "mxgemm_lora": (ctypes.c_int, [mbp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, sz,
+                                       ctypes.POINTER(mxg_lora), vp, sz, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -130,9 +176,9 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 
 
-def header_functions() -> list[str]:
-    """Names of the functions include/mxgemm.h declares."""
-    with open(HEADER_PATH) as f:
+def header_functions(path: str = HEADER_PATH) -> list[str]:
+    """Names of the functions a header declares (include/mxgemm.h by default)."""
+    with open(path) as f:
         text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
     names = re.findall(r"^\s*(?:const\s+)?[A-Za-z_][\w\s\*]*?\b([a-z_][a-z0-9_]*)\s*\(", text,
                        flags=re.M)
@@ -379,3 +425,54 @@ def mxg_graph_destroy(exec_: int) -> None:
 
 def mxg_strerror(code: int) -> str:
     return strerror(code)
+
+
+# ---- include/mxdecode.h ----------------------------------------------------
+
+
+def mxmoe_route(router: mxmoe_router, logits, logits_type: int, row_stride: int, bias,
+                tokens: int, ids, weights, stream=None) -> None:
+    _check(_lib.mxmoe_route(ctypes.byref(router), _ptr(logits), logits_type, row_stride,
+                            _ptr(bias), tokens, _ptr(ids), _ptr(weights), _stream(stream)),
+           "mxmoe_route")
+
+
+def mxmoe_packed_weight_bytes(experts: int, n: int, k: int) -> int:
+    return int(_lib.mxmoe_packed_weight_bytes(experts, n, k))
+
+
+def mxmoe_packed_scale_bytes(experts: int, n: int, k: int) -> int:
+    return int(_lib.mxmoe_packed_scale_bytes(experts, n, k))
+
+
+def mxmoe_pack_weight(w, w_scale, experts: int, n: int, k: int, w_packed, ws_packed,
+                      stream=None) -> None:
+    _check(_lib.mxmoe_pack_weight(_ptr(w), _ptr(w_scale), experts, n, k, _ptr(w_packed),
+                                  _ptr(ws_packed), _stream(stream)), "mxmoe_pack_weight")
+
+
+def mxmoe_workspace_bytes(tokens: int, top_k: int, hidden: int, inter: int) -> int:
+    return int(_lib.mxmoe_workspace_bytes(tokens, top_k, hidden, inter))
+
+
+def mxmoe_experts(x, ids, weights, w13, w13_scale, w2, w2_scale, tokens: int, top_k: int,
+                  experts: int, hidden: int, inter: int, workspace, workspace_bytes: int, out,
+                  stream=None) -> None:
+    _check(_lib.mxmoe_experts(_ptr(x), _ptr(ids), _ptr(weights), _ptr(w13), _ptr(w13_scale),
+                              _ptr(w2), _ptr(w2_scale), tokens, top_k, experts, hidden, inter,
+                              _ptr(workspace), workspace_bytes, _ptr(out), _stream(stream)),
+           "mxmoe_experts")
+
+
+def mxgemm_lora_scratch_bytes(m: int, rank: int) -> int:
+    return int(_lib.mxgemm_lora_scratch_bytes(m, rank))
+
+
+def mxgemm_lora(mb, w, w_scale, x, x_scale, x_bf16, m: int, n: int, k: int, split_k: int,
+                workspace, workspace_bytes: int, lora: mxg_lora, scratch, scratch_bytes: int,
+                c_out=None, stream=None) -> None:
+    _check(_lib.mxgemm_lora(ctypes.byref(mb) if mb is not None else None, _ptr(w),
+                            _ptr(w_scale), _ptr(x), _ptr(x_scale), _ptr(x_bf16), m, n, k,
+                            split_k, _ptr(workspace), workspace_bytes, ctypes.byref(lora),
+                            _ptr(scratch), scratch_bytes, _ptr(c_out), _stream(stream)),
+           "mxgemm_lora")

@@ -80,7 +80,7 @@ def build(verbose: bool = False) -> str:
 
 
 # Host-side sanitizers for the C-ABI layer only (argument validation, size
-# arithmetic, descriptor handling): api.hip's host code is compiled with
+# arithmetic, descriptor handling): the api*.hip files' host code is compiled with
 # AddressSanitizer and UndefinedBehaviorSanitizer (-Xarch_host: the device
 # code is built as usual) and linked with the regular objects of the other
 # sources. Loading it needs the ASan runtime preloaded (HOST_ASAN_RUNTIME).
@@ -108,13 +108,14 @@ def build_host_sanitized(verbose: bool = False) -> str:
     objs = [os.path.join(BUILD, os.path.basename(s) + ".o") for s in srcs]
     if not all(os.path.exists(o) for o in objs):
         build(verbose)
-    api = os.path.join(CSRC, "api.hip")
-    san_obj = os.path.join(BUILD, "api.hostsan.o")
+    apis = [s for s in srcs if os.path.basename(s).startswith("api")]
+    san_objs = [os.path.join(BUILD, os.path.basename(s) + ".hostsan.o") for s in apis]
     flags = [f for f in HIPCC_FLAGS if f != "-O3"] + ["-O1", "-g"]
-    _run([hipcc, *flags, *HOST_SAN_FLAGS, "-c", api, "-o", san_obj])
-    others = [o for s, o in zip(srcs, objs) if os.path.basename(s) != "api.hip"]
+    for api, san_obj in zip(apis, san_objs):
+        _run([hipcc, *flags, *HOST_SAN_FLAGS, "-c", api, "-o", san_obj])
+    others = [o for s, o in zip(srcs, objs) if s not in apis]
     tmp = HOST_SAN_LIB + ".tmp"
-    _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *HOST_SAN_FLAGS, "-o", tmp, san_obj,
+    _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *HOST_SAN_FLAGS, "-o", tmp, *san_objs,
           *others])
     os.replace(tmp, HOST_SAN_LIB)
     if verbose:

@@ -129,7 +129,8 @@ int gemm_call(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scale,
               const uint8_t* x, const uint8_t* x_scale, const uint16_t* xb, int32_t m, int32_t n,
               int32_t k, int32_t split_k, void* workspace, size_t workspace_bytes,
               uint32_t epoch_bias, uint16_t* c_out, uint8_t* xq_out, uint8_t* xs_out,
-              void* stream, void* ev_start, void* ev_stop, const char* tile) {
+              void* stream, void* ev_start, void* ev_stop, const char* tile,
+              const LoraArgs* lora) {
   const int rc =
       gemm_validate(mb, w, w_scale, x, x_scale, xb, m, n, k, split_k, c_out, xq_out, xs_out);
   if (rc != MXG_OK) return rc;
@@ -143,7 +144,7 @@ int gemm_call(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scale,
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return MXG_EHIP;
   TileCfg cfg;
-  if (!choose_tile(m, n, k, split_k, tile, &cfg)) return MXG_EUNSUPPORTED;
+  if (!choose_tile(m, n, k, split_k, tile, &cfg, lora != nullptr)) return MXG_EUNSUPPORTED;
 
   GemmArgs a;
   a.w = w;
@@ -173,6 +174,7 @@ int gemm_call(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scale,
   a.split_k = split_k;
   a.spin_limit = spin_limit(mb);
   a.epoch_bias = epoch_bias;
+  a.lora = lora ? *lora : LoraArgs{};
   return hip_code(launch_gemm_publish(a, cfg, static_cast<hipStream_t>(stream),
                                       static_cast<hipEvent_t>(ev_start),
                                       static_cast<hipEvent_t>(ev_stop)));

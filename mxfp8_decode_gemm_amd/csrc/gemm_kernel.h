@@ -70,37 +70,12 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/mxgemm.h"
+#include "mx_device.h"
 #include "mxgemm_internal.h"
 #include "quant_device.h"
 
 namespace mxg {
 namespace {
-
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
-typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
-
-// 2^(s-127) as an FP32 multiplier: the biased exponent s in the exponent
-// field; s == 0 is the subnormal 2^-127.
-__device__ __forceinline__ float e8m0_to_f32(uint32_t s) {
-  // 2^-127 (an FP32 subnormal, kept: the library is built with FP32
-  // denormals on) times 2^s, one instruction; s = 255 gives +inf.
-  return __builtin_amdgcn_ldexpf(__uint_as_float(0x00400000u), (int)s);
-}
-
-// Eight e4m3fn bytes (two dwords, lowest byte first) times a power-of-two
-// scale, as eight BF16 values. v_cvt_scalef32_pk_bf16_fp8 converts two bytes
-// of a dword per instruction; an e4m3 value times 2^k is exact in BF16 for
-// every scale the workloads use, and the instruction rounds to nearest even.
-__device__ __forceinline__ v8bf fp8x8_to_bf16(uint32_t w0, uint32_t w1, float scale) {
-  const v2bf p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, false);
-  const v2bf p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, true);
-  const v2bf p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, false);
-  const v2bf p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, true);
-  return v8bf{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-}
 
 // LDS header: [0] generation, [1] epoch, [2] the workspace's error word as
 // read at the call's start, [4 + w] worker wave w's range flags (bit 0: an x
@@ -130,54 +105,6 @@ __device__ __forceinline__ bool scale_byte_out(uint32_t s) {
 __device__ __forceinline__ bool scale_word_out(uint32_t w) {
   return scale_byte_out(w & 0xFFu) || scale_byte_out((w >> 8) & 0xFFu) ||
          scale_byte_out((w >> 16) & 0xFFu) || scale_byte_out(w >> 24);
-}
-
-// Raw buffer descriptors (gfx9 family): the fourth word of a plain byte
-// buffer, an offset no descriptor here reaches (1 GiB; offsets at or past a
-// buffer's size read as zeros), and the cache policy of a streaming load.
-constexpr int kBufferWord3 = 0x00020000;
-constexpr int kPastBuffer = 0x40000000;
-constexpr int kLoadNontemporal = 2;
-
-// A word that nothing writes while the kernel runs, read at a wave-uniform
-// address through the constant address space: a scalar load, counted apart
-// from the vector loads of the W stream, so a wait for it never waits for
-// the stream (the dispatch's acquire makes earlier launches' stores visible).
-__device__ __forceinline__ uint32_t ld_uniform_u32(const uint32_t* p) {
-  return *(const __attribute__((address_space(4))) uint32_t*)(p);
-}
-// Lane i takes lane i + N of its 16-lane row (0 where that lies past the
-// row): a DPP move on the vector unit instead of an LDS permute.
-template <int N>
-__device__ __forceinline__ uint32_t row_down(uint32_t x) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x100 + N, 0xF, 0xF, true);
-}
-__device__ __forceinline__ uint32_t ld_agent_u32(const uint32_t* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void st_agent_u32(uint32_t* p, uint32_t v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ uint64_t ld_agent_u64(const uint64_t* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void st_agent_u64(uint64_t* p, uint64_t v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
-// BF16 bits of an FP32 value, round to nearest even (v_cvt_pk_bf16_f32).
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  const __bf16 a = (__bf16)lo;
-  const __bf16 b = (__bf16)hi;
-  return (uint32_t)__builtin_bit_cast(uint16_t, a) |
-         ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
-}
-
-// Each BF16 half equal to 0x8000 (negative zero) becomes 0x0000.
-__device__ __forceinline__ uint32_t clear_negative_zero(uint32_t w) {
-  const uint32_t lo = (w & 0xFFFFu) == 0x8000u ? 0u : (w & 0xFFFFu);
-  const uint32_t hi = (w >> 16) == 0x8000u ? 0u : (w & 0xFFFF0000u);
-  return lo | hi;
 }
 
 // Token row of index c in a slice of rows of d items each (c < 8 d: an
@@ -443,6 +370,28 @@ __device__ __attribute__((noinline)) bool stage_rest(const uint8_t* x, const uin
   return out;
 }
 
+// Column n of row t: sum over the rank of B[ids[t]][n][r] u[t][r] in FP32.
+__device__ __forceinline__ float lora_term(const LoraArgs& l, int t, int n, int N) {
+  const int i = l.ids[t];
+  if ((unsigned)i >= (unsigned)l.adapters) return 0.f;
+  const uint4* b = reinterpret_cast<const uint4*>(l.b + ((size_t)i * N + n) * l.rank);
+  const float4* u = reinterpret_cast<const float4*>(l.u + (size_t)t * l.rank);
+  float s = 0.f;
+  for (int r = 0; r < l.rank >> 3; ++r) {
+    const uint4 v = b[r];
+    const float4 u0 = u[2 * r], u1 = u[2 * r + 1];
+    s = fmaf(__uint_as_float(v.x << 16), u0.x, s);
+    s = fmaf(__uint_as_float(v.x & 0xFFFF0000u), u0.y, s);
+    s = fmaf(__uint_as_float(v.y << 16), u0.z, s);
+    s = fmaf(__uint_as_float(v.y & 0xFFFF0000u), u0.w, s);
+    s = fmaf(__uint_as_float(v.z << 16), u1.x, s);
+    s = fmaf(__uint_as_float(v.z & 0xFFFF0000u), u1.y, s);
+    s = fmaf(__uint_as_float(v.w << 16), u1.z, s);
+    s = fmaf(__uint_as_float(v.w & 0xFFFF0000u), u1.w, s);
+  }
+  return s;
+}
+
 // At least two waves per SIMD (<= 256 VGPRs): with split-K the grid must be
 // resident at once, and a second wave hides the other's conversion work.
 // With split-K one more wave, the control wave, runs beside the WN x WK
@@ -456,8 +405,10 @@ __device__ __attribute__((noinline)) bool stage_rest(const uint8_t* x, const uin
 // loads all go out before the W prologue).
 // X16: the staged slice holds exact BF16 values (XStage::dest16 layout), not
 // FP8 codes and scale bytes, and the main loop reads the B operand as is.
+// LORA: each row's adapter is added before the rounding (a.lora).
 // Without a mailbox (a.state null) the kernel is a plain GEMM into c_out.
-template <int RB, int WN, int WK, int D, int SK, bool QX, int XR = 1, bool X16 = false>
+template <int RB, int WN, int WK, int D, int SK, bool QX, int XR = 1, bool X16 = false,
+          bool LORA = false>
 __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
     __attribute__((amdgpu_waves_per_eu(2))) gemm_publish_kernel(GemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -1023,6 +974,9 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
           v = r;
         }
       }
+      if constexpr (LORA) {
+        if (live) v += lora_term(a.lora, t, row0 + row, N);
+      }
       // BF16 (nearest even) of this column, then the pack's eight halves
       // gathered into lane e = 0: raw store, negative-zero clear, publish.
       const __bf16 hb = (__bf16)v;
@@ -1068,19 +1022,28 @@ struct Variant {
   const void* fn_q;    // BF16 x, quantized in the activation stage
   const void* fn16;    // MXFP8 x, staged as BF16 (null: not built)
   const void* fn16_q;  // BF16 x, quantized and staged as BF16 (null: not built)
+  const void* lora[4]; // the same four with the adapter epilogue
 };
 
 #define MXG_FN(RB, WN, WK, D, SK, QX, XR, X16) \
   reinterpret_cast<const void*>(&gemm_publish_kernel<RB, WN, WK, D, SK, QX, XR, X16>)
+#define MXG_FNL(RB, WN, WK, D, SK, QX, XR, X16) \
+  reinterpret_cast<const void*>(&gemm_publish_kernel<RB, WN, WK, D, SK, QX, XR, X16, true>)
 #define MXG_V(RB, WN, WK, D, SK)                                                     \
   Variant{TileCfg{RB, WN, WK, D}, SK, MXG_FN(RB, WN, WK, D, SK, false, 1, false),    \
-          MXG_FN(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr}
+          MXG_FN(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr,               \
+          {MXG_FNL(RB, WN, WK, D, SK, false, 1, false),                              \
+           MXG_FNL(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr}}
 // Also built with x staged as BF16 (the tiles the chooser takes for the
 // workload shapes).
 #define MXG_V16(RB, WN, WK, D, SK)                                                   \
   Variant{TileCfg{RB, WN, WK, D}, SK, MXG_FN(RB, WN, WK, D, SK, false, 1, false),    \
           MXG_FN(RB, WN, WK, D, SK, true, 1, false),                                 \
-          MXG_FN(RB, WN, WK, D, SK, false, 1, true), MXG_FN(RB, WN, WK, D, SK, true, 1, true)}
+          MXG_FN(RB, WN, WK, D, SK, false, 1, true), MXG_FN(RB, WN, WK, D, SK, true, 1, true), \
+          {MXG_FNL(RB, WN, WK, D, SK, false, 1, false),                              \
+           MXG_FNL(RB, WN, WK, D, SK, true, 1, false),                               \
+           MXG_FNL(RB, WN, WK, D, SK, false, 1, true),                               \
+           MXG_FNL(RB, WN, WK, D, SK, true, 1, true)}}
 // The x stage with an 8-chunk first round (xr = 2: a slice of twice the
 // size staged before the first barrier without a second, out-of-line round);
 // BF16 x stages through XQuant either way.
@@ -1088,7 +1051,9 @@ struct Variant {
 // 1 us slower.
 #define MXG_V2(RB, WN, WK, D, SK)                                                    \
   Variant{TileCfg{RB, WN, WK, D, 2}, SK, MXG_FN(RB, WN, WK, D, SK, false, 2, false), \
-          MXG_FN(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr}
+          MXG_FN(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr,               \
+          {MXG_FNL(RB, WN, WK, D, SK, false, 2, false),                              \
+           MXG_FNL(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr}}
 #define MXG_VARIANT(RB, WN, WK, D) \
   MXG_V(RB, WN, WK, D, 1), MXG_V(RB, WN, WK, D, 2), MXG_V(RB, WN, WK, D, 4), \
       MXG_V(RB, WN, WK, D, 8)

@@ -95,7 +95,8 @@ __global__ void scale_summary_kernel(const uint8_t* wp, const uint8_t* wsp, int 
   if (lane == 0) summary[rb] = lo | (hi << 8);
 }
 
-const void* variant_fn(const Variant& v, bool bf16_x, bool x16) {
+const void* variant_fn(const Variant& v, bool bf16_x, bool x16, bool lora) {
+  if (lora) return v.lora[2 * (x16 ? 1 : 0) + (bf16_x ? 1 : 0)];
   return x16 ? (bf16_x ? v.fn16_q : v.fn16) : (bf16_x ? v.fn_q : v.fn);
 }
 
@@ -127,18 +128,18 @@ size_t gemm_lds_bytes(const TileCfg& c, int m, int k_slice) {
 bool tile_available(const TileCfg& c) { return find_variant(c, 1) != nullptr; }
 
 static bool choose_tile_uncached(int m, int n, int k, int split_k, const char* tile,
-                                 TileCfg* out);
+                                 TileCfg* out, bool lora);
 
 // The default choice depends only on the sizes and the device: remembered
 // per key (a memo of device queries, not state that changes a result). A
 // forced tile is not remembered.
-bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* out) {
-  if (tile) return choose_tile_uncached(m, n, k, split_k, tile, out);
+bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* out, bool lora) {
+  if (tile) return choose_tile_uncached(m, n, k, split_k, tile, out, lora);
   static std::mutex mu;
-  static std::map<std::tuple<int, int, int, int, int>, std::pair<bool, TileCfg>> cache;
+  static std::map<std::tuple<int, int, int, int, int, bool>, std::pair<bool, TileCfg>> cache;
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return false;
-  const auto key = std::make_tuple(dev, m, n, k, split_k);
+  const auto key = std::make_tuple(dev, m, n, k, split_k, lora);
   {
     std::lock_guard<std::mutex> g(mu);
     auto it = cache.find(key);
@@ -148,7 +149,7 @@ bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* ou
     }
   }
   TileCfg c{};
-  const bool ok = choose_tile_uncached(m, n, k, split_k, nullptr, &c);
+  const bool ok = choose_tile_uncached(m, n, k, split_k, nullptr, &c, lora);
   std::lock_guard<std::mutex> g(mu);
   cache[key] = std::make_pair(ok, c);
   *out = c;
@@ -156,7 +157,7 @@ bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* ou
 }
 
 static bool choose_tile_uncached(int m, int n, int k, int split_k, const char* tile,
-                                 TileCfg* out) {
+                                 TileCfg* out, bool lora) {
   const int ks = k / split_k;
   auto fits = [&](const TileCfg& c) {
     const Variant* v = find_variant(c, split_k);
@@ -165,7 +166,7 @@ static bool choose_tile_uncached(int m, int n, int k, int split_k, const char* t
     // The workgroups of one tile wait for each other: the grid must be
     // resident all at once.
     const long tiles = (n + tile_rows(c) - 1) / tile_rows(c);
-    const long resident = gemm_resident_blocks(c, split_k, gemm_lds_bytes(c, m, ks));
+    const long resident = gemm_resident_blocks(c, split_k, gemm_lds_bytes(c, m, ks), lora);
     return resident > 0 && tiles * split_k <= resident && tiles * split_k <= MXG_WS_MAX_GROUPS;
   };
   int cus = 256;
@@ -257,13 +258,15 @@ static bool choose_tile_uncached(int m, int n, int k, int split_k, const char* t
   return found;
 }
 
-long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes) {
+long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool lora) {
   static std::mutex mu;
   static std::map<std::tuple<int, int, int, int, int, size_t>, long> cache;
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return -1;
   const auto key = std::make_tuple(dev, c.rb, c.wn,
-                                   c.wk * 100 + c.depth + 10000 * c.xr + 100000 * c.x16, split_k,
+                                   c.wk * 100 + c.depth + 10000 * c.xr + 100000 * c.x16 +
+                                       (lora ? 1000000 : 0),
+                                   split_k,
                                    lds_bytes);
   {
     std::lock_guard<std::mutex> g(mu);
@@ -274,7 +277,7 @@ long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes) {
   if (!v) return -1;
   // Both activation forms of the variant: a shape gets one tile either way.
   int per_cu = 1 << 30, cus = 0;
-  for (const void* fn : {variant_fn(*v, false, c.x16), variant_fn(*v, true, c.x16)}) {
+  for (const void* fn : {variant_fn(*v, false, c.x16, lora), variant_fn(*v, true, c.x16, lora)}) {
     int n = 0;
     if (!fn) return -1;
     if (lds_bytes > 64 * 1024 &&
@@ -317,7 +320,7 @@ hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t 
   const size_t lds = gemm_lds_bytes(c, a.m, a.k / a.split_k);
   GemmArgs args = a;
   args.xcd_groups = a.split_k > 1 && tiles % 8 == 0 ? 1 : 0;
-  const void* fn = variant_fn(*v, a.xb != nullptr, c.x16);
+  const void* fn = variant_fn(*v, a.xb != nullptr, c.x16, a.lora.b != nullptr);
   if (!fn) return hipErrorInvalidValue;
   if (lds > 64 * 1024) {
     const hipError_t e =

@@ -1,0 +1,54 @@
+// Internal declarations of the per-row decode operators (routing, experts,
+// adapters). Not part of the C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/mxdecode.h"
+
+namespace mxg {
+
+struct RouteArgs {
+  mxmoe_router r;
+  const void* logits;
+  int64_t row_stride;
+  const float* bias;  // or null
+  int32_t tokens;
+  int32_t* ids;
+  float* weights;
+};
+
+hipError_t launch_route(const RouteArgs& a, int logits_type, hipStream_t s);
+
+struct ExpertArgs {
+  const uint16_t* x;       // [tokens, hidden] BF16
+  const int32_t* ids;      // [tokens * top_k]
+  const float* weights;    // [tokens * top_k]
+  const uint8_t *w13, *w13s, *w2, *w2s;  // packed
+  size_t w13_bytes, w13s_bytes, w2_bytes, w2s_bytes;  // of one expert
+  int32_t tokens, top_k, experts, hidden, inter;
+  uint16_t* h;             // workspace: [2][pairs][inter] BF16, high then low parts
+  float* y;                // workspace: [pairs][hidden]
+  uint16_t* out;           // [tokens, hidden] BF16
+};
+
+hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
+
+// u[t][r] = scale[i] * sum_k A[i][r][k] x[t][k], i = ids[t] (zeros without an
+// adapter), FP32. xb: BF16 x, or x and xs.
+struct ShrinkArgs {
+  const uint16_t* a;
+  const float* scale;
+  const int32_t* ids;
+  const uint16_t* xb;
+  const uint8_t* x;
+  const uint8_t* xs;
+  float* u;
+  int32_t adapters, rank, m, k;
+};
+
+hipError_t launch_shrink(const ShrinkArgs& a, hipStream_t s);
+
+}  // namespace mxg

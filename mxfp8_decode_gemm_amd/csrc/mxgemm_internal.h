@@ -10,6 +10,15 @@
 
 namespace mxg {
 
+// The adapters of mxgemm_lora as the GEMM's epilogue reads them:
+// C[t, n] += sum_r b[ids[t]][n][r] u[t][r], u holding the scaled A x.
+struct LoraArgs {
+  const uint16_t* b;   // [adapters, n, rank] BF16, or null
+  const float* u;      // [m, rank]
+  const int32_t* ids;  // [m]
+  int32_t adapters, rank;
+};
+
 // Everything one GEMM+publish launch needs, by value.
 struct GemmArgs {
   const uint8_t* w;   // packed W tiles (mxgemm_pack_weight)
@@ -35,6 +44,8 @@ struct GemmArgs {
   // EPOCH starts at 1), 1 for the library's zero-filled no-allocation
   // scratch (stored 0 means epoch 1). Epoch 0 is never live either way.
   uint32_t epoch_bias;
+  // The rows' adapters (mxgemm_lora): b null without them.
+  LoraArgs lora;
 };
 
 // A workgroup computes an output tile of n_tile = 16 * rb * wn rows for one
@@ -63,15 +74,17 @@ size_t gemm_lds_bytes(const TileCfg& c, int m, int k_slice);
 
 // The tile for a problem. tile null: the default choice; "fp8": the default
 // tile with x kept in FP8 in LDS; "rb,wn,wk,depth[,xr[,x16]]": exactly that
-// variant (fails when it does not fit). Returns false when no variant fits.
-bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* out);
+// variant (fails when it does not fit). lora: the kernels with the adapters in
+// their epilogue. Returns false when no variant fits.
+bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* out,
+                 bool lora = false);
 
 // Whether a variant is compiled in.
 bool tile_available(const TileCfg& c);
 
 // How many workgroups of this variant can be resident at once on the current
 // device (CUs x blocks per CU); negative on a HIP error.
-long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes);
+long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool lora = false);
 
 // ev_start/ev_stop (may be null) are recorded around the kernel itself.
 hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t s,
@@ -131,11 +144,12 @@ int gemm_validate(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scal
 
 // One GEMM launch after host validation (the body of mxgemm_publish and its
 // siblings). mb null: plain GEMM into c_out. xb non-null: BF16 x quantized in
-// the kernel. epoch_bias: see GemmArgs. Returns an MXG_* code.
+// the kernel. epoch_bias: see GemmArgs. lora: the rows' adapters, or null.
+// Returns an MXG_* code.
 int gemm_call(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scale, const uint8_t* x,
               const uint8_t* x_scale, const uint16_t* xb, int32_t m, int32_t n, int32_t k,
               int32_t split_k, void* workspace, size_t workspace_bytes, uint32_t epoch_bias,
               uint16_t* c_out, uint8_t* xq_out, uint8_t* xs_out, void* stream, void* ev_start,
-              void* ev_stop, const char* tile = nullptr);
+              void* ev_stop, const char* tile = nullptr, const LoraArgs* lora = nullptr);
 
 }  // namespace mxg

@@ -19,6 +19,8 @@ computes, in float64 / exact integer arithmetic:
 * ``mailbox``   -- the three-generation Lamport mailbox: publish, collect,
                    reset, generation advance, and the invariant checker; the
                    word publish and fused all-gather; the all-reduce collect.
+* ``decode``    -- the operators whose weights are chosen per row: expert
+                   routing, the chosen experts' products, low-rank adapters.
 * ``tolerance`` -- the BF16 acceptance bound used by every parity test.
 
 Page citations in this package name the four API pages by module:
@@ -28,6 +30,6 @@ Page citations in this package name the four API pages by module:
   "sync page"            = vllm.models.deepseek_v41.amd.mono.common.sync
 """
 
-from . import codecs, gemm, mailbox, quant, tolerance  # noqa: F401
+from . import codecs, decode, gemm, mailbox, quant, tolerance  # noqa: F401
 
-__all__ = ["codecs", "gemm", "mailbox", "quant", "tolerance"]
+__all__ = ["codecs", "decode", "gemm", "mailbox", "quant", "tolerance"]

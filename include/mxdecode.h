@@ -151,9 +151,16 @@ typedef struct mxg_lora {
   int32_t rank;         /* a multiple of 8, 8..MXG_LORA_MAX_RANK */
 } mxg_lora;
 
-/* Bytes of scratch mxgemm_lora needs beside the split-K workspace; 0 on bad
- * sizes. */
-size_t mxgemm_lora_scratch_bytes(int32_t m, int32_t rank);
+/* Bytes of scratch mxgemm_lora needs for n columns, beside the split-K
+ * workspace; 0 on bad sizes. The workgroups exchange A[i] x through it as
+ * (value, epoch) pairs, like the split-K partials in theirs. */
+size_t mxgemm_lora_scratch_bytes(int32_t n);
+
+/* Arm a scratch: once before first use, outside capture; it then serves calls
+ * of any size up to its own, in any order. scratch_bytes: at least
+ * mxgemm_lora_scratch_bytes(8), a multiple of 16. Errors: MXG_EINVAL,
+ * MXG_EALIGN, MXG_EHIP. */
+int mxgemm_lora_scratch_init(void* scratch, size_t scratch_bytes, void* stream);
 
 /* The projection of mxgemm_publish, mxgemm_publish_bf16 or mxgemm with a
  * low-rank adapter beside it, chosen per row:
@@ -162,15 +169,20 @@ size_t mxgemm_lora_scratch_bytes(int32_t m, int32_t rank);
  *
  * The shared product is theirs (with BF16 x: of the quantized activation);
  * the adapter takes BF16 x as it is, MXFP8 x as the values it stands for.
- * A[i] x and B[i] u are summed in FP32, u is held in FP32, and the two products
- * are added before the one rounding to BF16.
+ * Both products of the adapter accumulate in FP32, u = scale[i] A[i] x between
+ * them is held as the sum of two BF16 values (about 17 bits), and the result is
+ * added to the shared product before the one rounding to BF16.
  *
  *   mb       a mailbox to publish C into (then collect it, as after
  *            mxgemm_publish), or NULL for the plain product into c_out
  *   x, x_scale  MXFP8 x, or both NULL with x_bf16 given
  *   x_bf16   BF16 x, or NULL with x and x_scale given
- *   scratch  device, at least mxgemm_lora_scratch_bytes(), 16-B aligned; one
- *            call at a time per scratch. Holds nothing between calls
+ *   scratch  device, at least mxgemm_lora_scratch_bytes(n), 16-B aligned, armed
+ *            by mxgemm_lora_scratch_init; one call at a time per scratch.
+ *            Workgroup 0 gives up waiting for the others to start after
+ *            mb->spin_limit polls (MXG_DEFAULT_SPIN_LIMIT without mb) and sets
+ *            MXG_ERR_SPLITK_SPIN in the scratch's ERROR word (MXG_WS_ERROR):
+ *            later calls are right but slow until it is armed again
  *   c_out    device [m, n] BF16 as rounded; may be NULL with mb
  * Other arguments as mxgemm_publish. Errors: its errors, MXG_EINVAL for a bad
  * adapter argument, MXG_EWORKSPACE for a missing or small scratch. */

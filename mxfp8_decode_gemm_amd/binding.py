@@ -162,7 +162,8 @@ def _load() -> ctypes.CDLL:
         "mxmoe_workspace_bytes": (sz, [i32, i32, i32, i32]),
         "mxmoe_experts": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp,
                                          sz, vp, vp]),
-        "mxgemm_lora_scratch_bytes": (sz, [i32, i32]),
+        "mxgemm_lora_scratch_bytes": (sz, [i32]),
+        "mxgemm_lora_scratch_init": (ctypes.c_int, [vp, sz, vp]),
         "mxgemm_lora": (ctypes.c_int, [mbp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, sz,
                                        ctypes.POINTER(mxg_lora), vp, sz, vp, vp]),
     }
@@ -464,8 +465,13 @@ def mxmoe_experts(x, ids, weights, w13, w13_scale, w2, w2_scale, tokens: int, to
            "mxmoe_experts")
 
 
-def mxgemm_lora_scratch_bytes(m: int, rank: int) -> int:
-    return int(_lib.mxgemm_lora_scratch_bytes(m, rank))
+def mxgemm_lora_scratch_bytes(n: int) -> int:
+    return int(_lib.mxgemm_lora_scratch_bytes(n))
+
+
+def mxgemm_lora_scratch_init(scratch, scratch_bytes: int, stream=None) -> None:
+    _check(_lib.mxgemm_lora_scratch_init(_ptr(scratch), scratch_bytes, _stream(stream)),
+           "mxgemm_lora_scratch_init")
 
 
 def mxgemm_lora(mb, w, w_scale, x, x_scale, x_bf16, m: int, n: int, k: int, split_k: int,

@@ -144,7 +144,7 @@ int gemm_call(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scale,
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return MXG_EHIP;
   TileCfg cfg;
-  if (!choose_tile(m, n, k, split_k, tile, &cfg, lora != nullptr)) return MXG_EUNSUPPORTED;
+  if (!choose_tile(m, n, k, split_k, tile, &cfg, lora ? lora->rank : 0)) return MXG_EUNSUPPORTED;
 
   GemmArgs a;
   a.w = w;

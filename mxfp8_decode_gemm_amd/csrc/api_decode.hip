@@ -135,9 +135,25 @@ int mxmoe_experts(const uint16_t* x, const int32_t* ids, const float* weights,
   return hip_code(launch_experts(a, static_cast<hipStream_t>(stream)));
 }
 
-size_t mxgemm_lora_scratch_bytes(int32_t m, int32_t rank) {
-  if (m < 1 || m > MXG_MAX_ROWS || rank < 8 || rank > MXG_LORA_MAX_RANK || rank % 8) return 0;
-  return (size_t)m * rank * sizeof(float);
+namespace {
+// The scratch: header, one epoch word per workgroup, the pairs.
+size_t lora_flag_bytes(int32_t n) {
+  const size_t words = (size_t)(n + 15) / 16;  // tiles of at least 16 rows, or a split-K grid
+  return (words < MXG_WS_MAX_GROUPS ? MXG_WS_MAX_GROUPS : (words + 3) / 4 * 4) * 4;
+}
+}  // namespace
+
+size_t mxgemm_lora_scratch_bytes(int32_t n) {
+  if (n <= 0 || n % 8) return 0;
+  return MXG_WS_HEADER_BYTES + lora_flag_bytes(n) + kLoraMaxPairs * sizeof(uint64_t);
+}
+
+int mxgemm_lora_scratch_init(void* scratch, size_t scratch_bytes, void* stream) {
+  if (!scratch || scratch_bytes < mxgemm_lora_scratch_bytes(8) || scratch_bytes % 16)
+    return MXG_EINVAL;
+  if (!aligned16(scratch)) return MXG_EALIGN;
+  return hip_code(launch_workspace_init(static_cast<uint32_t*>(scratch), scratch_bytes,
+                                        static_cast<hipStream_t>(stream)));
 }
 
 int mxgemm_lora(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scale,
@@ -154,37 +170,19 @@ int mxgemm_lora(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scale,
   if (!aligned16(lora->a) || !aligned16(lora->b) || !aligned(lora->scale, 4) ||
       !aligned(lora->ids, 4))
     return MXG_EALIGN;
-  if (!scratch || scratch_bytes < mxgemm_lora_scratch_bytes(m, lora->rank)) return MXG_EWORKSPACE;
+  if (!scratch || scratch_bytes < mxgemm_lora_scratch_bytes(n)) return MXG_EWORKSPACE;
   if (!aligned16(scratch)) return MXG_EALIGN;
-  LoraArgs l;
+  uint8_t* s = static_cast<uint8_t*>(scratch);
+  LoraArgs l = {};
+  l.a = lora->a;
   l.b = lora->b;
-  l.u = static_cast<const float*>(scratch);
+  l.scale = lora->scale;
   l.ids = lora->ids;
   l.adapters = lora->adapters;
   l.rank = lora->rank;
-  // What the GEMM call would refuse is refused before the first launch.
-  if (split_k > 1) {
-    if (!workspace || workspace_bytes < mxgemm_workspace_bytes(m, n, k, split_k))
-      return MXG_EWORKSPACE;
-    if (!aligned16(workspace)) return MXG_EALIGN;
-  }
-  TileCfg cfg;
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) return MXG_EHIP;
-  if (!choose_tile(m, n, k, split_k, nullptr, &cfg, true)) return MXG_EUNSUPPORTED;
-  ShrinkArgs s;
-  s.a = lora->a;
-  s.scale = lora->scale;
-  s.ids = lora->ids;
-  s.xb = x_bf16;
-  s.x = x;
-  s.xs = x_scale;
-  s.u = static_cast<float*>(scratch);
-  s.adapters = lora->adapters;
-  s.rank = lora->rank;
-  s.m = m;
-  s.k = k;
-  if (launch_shrink(s, static_cast<hipStream_t>(stream)) != hipSuccess) return MXG_EHIP;
+  l.hdr = static_cast<uint32_t*>(scratch);
+  l.flags = reinterpret_cast<uint32_t*>(s + MXG_WS_HEADER_BYTES);
+  l.pairs = reinterpret_cast<uint64_t*>(s + MXG_WS_HEADER_BYTES + lora_flag_bytes(n));
   return gemm_call(mb, w, w_scale, x, x_scale, x_bf16, m, n, k, split_k, workspace,
                    workspace_bytes, 0, c_out, nullptr, nullptr, stream, nullptr, nullptr, nullptr,
                    &l);

@@ -370,26 +370,264 @@ __device__ __attribute__((noinline)) bool stage_rest(const uint8_t* x, const uin
   return out;
 }
 
-// Column n of row t: sum over the rank of B[ids[t]][n][r] u[t][r] in FP32.
-__device__ __forceinline__ float lora_term(const LoraArgs& l, int t, int n, int N) {
-  const int i = l.ids[t];
-  if ((unsigned)i >= (unsigned)l.adapters) return 0.f;
-  const uint4* b = reinterpret_cast<const uint4*>(l.b + ((size_t)i * N + n) * l.rank);
-  const float4* u = reinterpret_cast<const float4*>(l.u + (size_t)t * l.rank);
-  float s = 0.f;
-  for (int r = 0; r < l.rank >> 3; ++r) {
-    const uint4 v = b[r];
-    const float4 u0 = u[2 * r], u1 = u[2 * r + 1];
-    s = fmaf(__uint_as_float(v.x << 16), u0.x, s);
-    s = fmaf(__uint_as_float(v.x & 0xFFFF0000u), u0.y, s);
-    s = fmaf(__uint_as_float(v.y << 16), u0.z, s);
-    s = fmaf(__uint_as_float(v.y & 0xFFFF0000u), u0.w, s);
-    s = fmaf(__uint_as_float(v.z << 16), u1.x, s);
-    s = fmaf(__uint_as_float(v.z & 0xFFFF0000u), u1.y, s);
-    s = fmaf(__uint_as_float(v.w << 16), u1.z, s);
-    s = fmaf(__uint_as_float(v.w & 0xFFFF0000u), u1.w, s);
+// ---- low-rank adapters (LORA) ---------------------------------------------
+// C[t] += scale[i] B[i] (A[i] x[t]), i = ids[t], beside the W stream:
+//   * u = scale A x is small (m * rank values) but reads A whole, so its dot
+//     products, cut into `parts` along K, are spread over the workgroups: the
+//     side wave of each computes its share while the workers stream W, and
+//     stores every partial as a (value, epoch) pair, as split-K does.
+//   * Each side wave then collects all pairs, sums the parts in ascending K
+//     order and leaves u in LDS as high and low BF16 parts (hi = bf16(u), lo =
+//     bf16(u - hi), together 17 bits).
+//   * After its K loop every worker adds B u to its own partial tile: B's rows
+//     are an MFMA A operand as they lie in memory (8 consecutive ranks a
+//     lane), u the B operand. (Adapter, 32 ranks) units are dealt over the
+//     split-K slices and the waves along K, whose partials are summed anyway.
+//     A unit's product is added in the columns of its adapter's rows alone: an
+//     infinity or NaN in one adapter stays with its rows.
+// A pair not seen after kLoraPolls polls is computed by the wave that wants it,
+// to the same bits: no workgroup depends on another being resident. Workgroup 0
+// advances the epoch once every workgroup has read it; should that wait give up
+// (calls that overlap on one scratch), it marks the scratch, and from then on
+// every wave computes all of u itself until the scratch is armed again.
+constexpr uint32_t kLoraPolls = 256;
+// LDS area: [0] distinct adapters, [1 + j] adapter j, [9 + j] its rows' mask,
+// then u's high parts [m][rank], its low parts, the partials (FP32).
+constexpr int kLoraList = 80;
+
+__device__ __forceinline__ float dot8(const uint4 a, const uint4 b, float s) {
+  const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    s = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), s);
+    s = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), s);
   }
   return s;
+}
+
+// The sum of x over the wave, in lane 63: row shifts, then row broadcasts.
+__device__ __forceinline__ float wave_sum63(float x) {
+#define MXG_DPP_ADD(C, MASK)                                                               \
+  x += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), C, \
+                                                             MASK, 0xF, true))
+  MXG_DPP_ADD(0x111, 0xF);
+  MXG_DPP_ADD(0x112, 0xF);
+  MXG_DPP_ADD(0x114, 0xF);
+  MXG_DPP_ADD(0x118, 0xF);
+  MXG_DPP_ADD(0x142, 0xA);
+  MXG_DPP_ADD(0x143, 0xC);
+#undef MXG_DPP_ADD
+  return x;
+}
+
+// The side wave of an adapter launch, from the kernel's start to its end: it
+// shares the workers' barriers, and with split-K does the control wave's work
+// too. It is one function of its own, called once, so that its loads may be in
+// flight across one without the workers' code waiting for them. Its code runs cold
+// on every CU and is kept short (a first version, unrolled further, lost 2-3 us
+// to instruction fetches).
+template <int SK, bool QX, bool X16, int NW>
+__device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint8_t* lw,
+                                                    int lane) {
+  const LoraArgs& l = a.lora;
+  const int m = a.m, rank = l.rank, K = a.k;
+  int* const list = reinterpret_cast<int*>(lw);
+  uint16_t* const uh = reinterpret_cast<uint16_t*>(lw + kLoraList);
+  float* const part = reinterpret_cast<float*>(uh + 2 * m * rank);
+  // ---- hand-off words, ids, epoch: one round trip ------------------------
+  int lid = l.ids[lane < m ? lane : 0];
+  uint32_t lepoch = ld_agent_u32(l.hdr + MXG_WS_EPOCH);
+  const uint32_t lerr = ld_agent_u32(l.hdr + MXG_WS_ERROR);
+  uint32_t gen = 0, epoch = 0;
+  if (SK > 1 && lane == 0) {
+    if (a.state) gen = ld_agent_u32(a.state + MXG_STATE_NEXT) % MXG_GENERATIONS;
+    epoch = ld_agent_u32(a.ws_hdr + MXG_WS_EPOCH) + a.epoch_bias;
+    hdr[2] = ld_agent_u32(a.ws_hdr + MXG_WS_ERROR);
+    hdr[0] = gen;
+    hdr[1] = epoch;
+    st_agent_u32(a.flags + blockIdx.x, epoch);  // (the epoch has been read)
+  }
+  lepoch = __builtin_amdgcn_readfirstlane(lepoch);
+  if (lane == 0) st_agent_u32(l.flags + blockIdx.x, lepoch);
+  // ---- the distinct adapters and the rows that have one -------------------
+  if (lane >= m || (unsigned)lid >= (unsigned)l.adapters) lid = -1;
+  float scale = 0.f;  // lane t: of row t's adapter
+  if (lid >= 0) scale = l.scale[lid];
+  uint64_t rows = 0;  // 4 bits each
+  int nrows = 0, nd = 0;
+  for (int t = 0; t < m; ++t) {
+    const int i = __builtin_amdgcn_readlane(lid, t);
+    if (i < 0) continue;
+    rows |= (uint64_t)t << (4 * nrows++);
+    const uint64_t same = __ballot(lid == i);
+    if ((int)__ffsll((unsigned long long)same) - 1 == t) {
+      if (lane == 0) {
+        list[1 + nd] = i;
+        list[9 + nd] = (int)same;
+      }
+      ++nd;
+    }
+  }
+  if (lane == 0) list[0] = nd;
+
+  // ---- u's dot products --------------------------------------------------
+  // Task q: the partial (row, rank, part), part fastest, in 512-value pieces.
+  // First this workgroup's tasks, into pairs, and a collection of all pairs;
+  // or all tasks, into LDS: where they are few, where the scratch is marked,
+  // and where a pair did not come.
+  const int ps = l.parts_log2;
+  const int total = (nrows * rank) << ps;
+  const int len = K >> ps;  // of a part: a multiple of 32
+  const int per = (len + 511) >> 9;
+  const uint32_t rinv = ((1u << 20) + rank - 1) / rank;  // item / rank for items < 1024
+  constexpr int kPieces = 8;  // in flight
+  bool before_barrier = true;
+  for (int pass = lerr != 0 || l.workers == 0 ? 1 : 0; pass < 2; ++pass) {
+    const int first = pass == 0 ? (int)blockIdx.x : 0, step = pass == 0 ? l.workers : 1;
+    int q = first < (pass == 0 ? step : 1) ? first : total, piece = 0;
+    float sum = 0.f;
+    while (before_barrier || q < total) {
+      uint4 av[kPieces], xv[kPieces];
+      uint32_t sb[QX ? 1 : kPieces];
+      int ql = q < total ? q : 0, pl = piece;
+      if (q < total) {
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+          const int item = ql >> ps;
+          const int ri = (int)((item * rinv) >> 20);
+          const int t = (int)(rows >> (4 * ri)) & 15;
+          const size_t row = (size_t)__builtin_amdgcn_readlane(lid, t) * rank + (item - ri * rank);
+          int k = pl * 512 + 8 * lane;
+          k = ((ql & ((1 << ps) - 1)) * len) + (k < len ? k : 0);  // past the part: its start
+          av[j] = *reinterpret_cast<const uint4*>(l.a + row * K + k);
+          if constexpr (QX) {
+            xv[j] = *reinterpret_cast<const uint4*>(a.xb + (size_t)t * K + k);
+          } else {
+            const uint2 c = *reinterpret_cast<const uint2*>(a.x + (size_t)t * K + k);
+            xv[j].x = c.x;
+            xv[j].y = c.y;
+            sb[j] = a.xs[(size_t)t * (K >> 5) + (k >> 5)];
+          }
+          if (++pl == per) {
+            pl = 0;
+            if (ql + step < total) ql += step;  // past the last task: it again, not used
+          }
+        }
+      }
+      if (before_barrier) {
+        // The workers' first barrier (x staged; the list and the hand-off words
+        // are in LDS), with the loads above in flight.
+        before_barrier = false;
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if constexpr (X16) {  // the exact path's second stage has its own
+          uint32_t rflags = 0;
+          for (int w = 0; w < NW; ++w) rflags |= hdr[kHdrFlags + w];
+          if (rflags) __builtin_amdgcn_s_barrier();
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        if (q >= total) break;
+        if (piece * 512 + 8 * lane < len) {
+          if constexpr (QX) {
+            sum = dot8(av[j], xv[j], sum);
+          } else {  // the codes' products, then their scale (exact short of FP32's range)
+            const v8bf c = fp8x8_to_bf16(xv[j].x, xv[j].y, 1.0f);
+            sum += __builtin_amdgcn_ldexpf(dot8(av[j], __builtin_bit_cast(uint4, c), 0.f),
+                                           (int)sb[j] - 127);
+          }
+        }
+        if (++piece == per) {
+          sum = wave_sum63(sum);
+          if (lane == 63) {
+            if (pass == 0)
+              st_agent_u64(l.pairs + q, (uint64_t)__float_as_uint(sum) | ((uint64_t)lepoch << 32));
+            else
+              part[q] = sum;
+          }
+          sum = 0.f;
+          piece = 0;
+          q += step;
+        }
+      }
+    }
+    if (pass == 1) break;
+    // All pairs, eight loads per lane in flight.
+    constexpr int B = 8;
+    bool missed = false;
+    for (int q0 = 0; q0 < total; q0 += 64 * B) {
+      uint64_t pv[B];
+      uint32_t polls = 0;
+      bool pending = true;
+      while (pending && polls++ < kLoraPolls) {
+        if (polls > 1) __builtin_amdgcn_s_sleep(1);
+        pending = false;
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+          const int p = q0 + 64 * j + lane;
+          pv[j] = ld_agent_u64(l.pairs + (p < total ? p : 0));
+        }
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+          pending |= q0 + 64 * j + lane < total && (uint32_t)(pv[j] >> 32) != lepoch;
+        pending = __any(pending);
+      }
+      missed |= pending;
+#pragma unroll
+      for (int j = 0; j < B; ++j)
+        if (q0 + 64 * j + lane < total) part[q0 + 64 * j + lane] = __uint_as_float((uint32_t)pv[j]);
+    }
+    if (!missed) break;
+  }
+  __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
+  for (int i0 = 0; i0 < nrows * rank; i0 += 64) {
+    const int item = i0 + lane < nrows * rank ? i0 + lane : 0;
+    float u = part[item << ps];
+    for (int p = 1; p < 1 << ps; ++p) u += part[(item << ps) + p];
+    const int ri = (int)((item * rinv) >> 20);
+    const int t = (int)(rows >> (4 * ri)) & 15;
+    u *= __shfl(scale, t, 64);
+    const __bf16 hi = (__bf16)u;
+    // A high part beyond BF16's range has no remainder.
+    const __bf16 lo = fabsf((float)hi) < INFINITY ? (__bf16)(u - (float)hi) : (__bf16)0.f;
+    const int at = t * rank + item - ri * rank;
+    if (i0 + lane < nrows * rank) {
+      uh[at] = __builtin_bit_cast(uint16_t, hi);
+      uh[m * rank + at] = __builtin_bit_cast(uint16_t, lo);
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();        // the workers' K loops are done, u is there
+  __builtin_amdgcn_s_barrier();        // the partial tiles are in LDS
+  if (blockIdx.x != 0) return;
+  // Workgroup 0: the next epochs once every workgroup has read this call's
+  // (its flag words hold it), and the generation handed to the consumer.
+  uint32_t polls = 0;
+  bool pending = true;
+  epoch = __builtin_amdgcn_readfirstlane(epoch);
+  while (pending && polls++ < a.spin_limit) {
+    pending = false;
+    for (int i = lane; i < (int)gridDim.x; i += 64) {
+      pending |= ld_agent_u32(l.flags + i) != lepoch;
+      if (SK > 1) pending |= ld_agent_u32(a.flags + i) != epoch;
+    }
+    pending = __any(pending);
+    if (pending) __builtin_amdgcn_s_sleep(2);
+  }
+  if (lane != 0) return;
+  if (pending) {
+    __hip_atomic_fetch_or(l.hdr + MXG_WS_ERROR, MXG_ERR_SPLITK_SPIN, __ATOMIC_RELAXED,
+                          __HIP_MEMORY_SCOPE_AGENT);
+    if (SK > 1)
+      __hip_atomic_fetch_or(a.ws_hdr + MXG_WS_ERROR, MXG_ERR_SPLITK_SPIN, __ATOMIC_RELAXED,
+                            __HIP_MEMORY_SCOPE_AGENT);
+  }
+  st_agent_u32(l.hdr + MXG_WS_EPOCH, lepoch + 1u == 0u ? 1u : lepoch + 1u);
+  if (SK > 1 && !pending)
+    st_agent_u32(a.ws_hdr + MXG_WS_EPOCH, (epoch + 1u == 0u ? 1u : epoch + 1u) - a.epoch_bias);
+  if (SK > 1 && a.state) st_agent_u32(a.state + MXG_STATE_ACTIVE, gen);
 }
 
 // At least two waves per SIMD (<= 256 VGPRs): with split-K the grid must be
@@ -405,11 +643,12 @@ __device__ __forceinline__ float lora_term(const LoraArgs& l, int t, int n, int 
 // loads all go out before the W prologue).
 // X16: the staged slice holds exact BF16 values (XStage::dest16 layout), not
 // FP8 codes and scale bytes, and the main loop reads the B operand as is.
-// LORA: each row's adapter is added before the rounding (a.lora).
+// LORA: each row's adapter is added before the rounding (a.lora); the side
+// wave computes its A x.
 // Without a mailbox (a.state null) the kernel is a plain GEMM into c_out.
 template <int RB, int WN, int WK, int D, int SK, bool QX, int XR = 1, bool X16 = false,
           bool LORA = false>
-__global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
+__global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 || LORA ? 1 : 0)))
     __attribute__((amdgpu_waves_per_eu(2))) gemm_publish_kernel(GemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   constexpr int NT = 64 * WN * WK;  // worker threads
@@ -421,7 +660,7 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
   // Wave-uniform in a scalar register, so the W stream's base addresses and
   // the per-block selects stay on the scalar unit.
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const bool ctl = SK > 1 && wave >= NT / 64;  // the control wave (split-K only)
+  const bool ctl = (SK > 1 || LORA) && wave >= NT / 64;  // the side wave
   const int hand_tid = SK > 1 ? NT : 0; // reads the hand-off words
   const int wn = wave % WN;
   const int wk = wave / WN;
@@ -455,6 +694,16 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
   uint4* xl = reinterpret_cast<uint4*>(lds + kHeaderBytes);
   uint8_t* xsl = lds + kHeaderBytes + (size_t)m * KS;
 
+  // ---- the adapters' side wave -------------------------------------------
+  uint8_t* const lw = lds + (LORA ? a.lora.lds_off : 0);
+  const int* const llist = reinterpret_cast<const int*>(lw);
+  if constexpr (LORA) {
+    if (ctl) {
+      lora_side<SK, QX, X16, NT / 64>(a, hdr, lw, lane);
+      return;
+    }
+  }
+
   // ---- call hand-off: generation and epoch ------------------------------
   // Read once per workgroup, before it counts itself (all_gather page,
   // _AllGatherKernel.kernel: the last CTA to arrive advances the state).
@@ -470,7 +719,7 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
   // their whole W prologue at the first register they reuse.
   uint32_t gen = 0, epoch = 0;
   if (S == 1 && a.state) gen = ld_uniform_u32(a.state + MXG_STATE_NEXT) % MXG_GENERATIONS;
-  if (S > 1 && tid == hand_tid) {
+  if (S > 1 && !LORA && tid == hand_tid) {
     if (a.state) gen = ld_agent_u32(a.state + MXG_STATE_NEXT) % MXG_GENERATIONS;
     epoch = ld_agent_u32(a.ws_hdr + MXG_WS_EPOCH) + a.epoch_bias;
     const uint32_t wserr = ld_agent_u32(a.ws_hdr + MXG_WS_ERROR);
@@ -662,7 +911,7 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
   const bool exact_path = rflags != 0;
 
   // ---- control wave: epoch bookkeeping while the workers stream ---------
-  if (S > 1 && ctl) {
+  if (S > 1 && !LORA && ctl) {
     if (blockIdx.x == 0) {
       // Every workgroup's word holding this call's epoch means every
       // workgroup has read it: only then may the next epoch be stored.
@@ -703,6 +952,33 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
       }
       __syncthreads();
     }
+  }
+
+  // ---- adapters: this wave's (adapter, 32 ranks) units -------------------
+  // The rows of B of the first kLoraAhead units are loaded ahead of the K loop.
+  constexpr int kLoraAhead = LORA ? 2 : 1;
+  const int lora_chunks = LORA ? (a.lora.rank + 31) >> 5 : 1;
+  const int lora_units = LORA && !ctl ? llist[0] * lora_chunks : 0;
+  const int lora_q0 = slice + S * wk;
+  v8bf lb[kLoraAhead][RB];
+  auto lora_load = [&](int q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < kLoraAhead; ++h) {
+      const int qh = q + h * S * WK;
+      const int j = qh / lora_chunks;
+      const int k = 32 * (qh - j * lora_chunks) + 8 * grp;  // this lane's 8 ranks
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const int n = row0 + (wn * RB + b) * 16 + r16;
+        lb[h][b] = v8bf{};
+        if (qh < lora_units && k < a.lora.rank && n < N)
+          lb[h][b] = *reinterpret_cast<const v8bf*>(
+              a.lora.b + ((size_t)llist[1 + j] * N + n) * a.lora.rank + k);
+      }
+    }
+  };
+  if constexpr (LORA) {
+    if (lora_q0 < lora_units) lora_load(lora_q0);
   }
 
   // ---- main loop: K blocks of this wave ---------------------------------
@@ -882,6 +1158,37 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
 
   // ---- partial tile -> LDS [wk][t][row], summed over waves in K order ---
   __syncthreads();  // every wave is done with x in LDS
+  // ---- B u of the adapters into this wave's partial tile ----------------
+  if constexpr (LORA) {
+    if (!ctl) {
+      const int rank = a.lora.rank;
+      const uint16_t* const uh = reinterpret_cast<const uint16_t*>(lw + kLoraList);
+      for (int q = lora_q0; q < lora_units; q += kLoraAhead * S * WK) {
+        if (q != lora_q0) lora_load(q);
+#pragma unroll
+        for (int h = 0; h < kLoraAhead; ++h) {
+          const int qh = q + h * S * WK;
+          if (qh >= lora_units) break;
+          const int j = qh / lora_chunks;
+          const int k = 32 * (qh - j * lora_chunks) + 8 * grp;  // this lane's 8 ranks
+          const bool mine = tok && ((llist[9 + j] >> r16) & 1) != 0;
+          v8bf hi = {}, lo = {};
+          if (mine && k < rank) {
+            hi = *reinterpret_cast<const v8bf*>(uh + r16 * rank + k);
+            lo = *reinterpret_cast<const v8bf*>(uh + (m + r16) * rank + k);
+          }
+#pragma unroll
+          for (int b = 0; b < RB; ++b) {
+            v4f t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lb[h][b], hi,
+                                                            v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lb[h][b], lo, t, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[b][r] += mine ? t[r] : 0.f;
+          }
+        }
+      }
+    }
+  }
   float* red = reinterpret_cast<float*>(lds + kHeaderBytes);
   if (tok && !ctl) {
 #pragma unroll
@@ -974,9 +1281,6 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
           v = r;
         }
       }
-      if constexpr (LORA) {
-        if (live) v += lora_term(a.lora, t, row0 + row, N);
-      }
       // BF16 (nearest even) of this column, then the pack's eight halves
       // gathered into lane e = 0: raw store, negative-zero clear, publish.
       const __bf16 hb = (__bf16)v;
@@ -1009,7 +1313,8 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 ? 1 : 0)))
 
   // Hand the generation to the consumer once per grid (publishing_gemm page,
   // epilog_warp: block 0, one thread, sets the active stage word).
-  if (a.state && blockIdx.x == 0 && tid == hand_tid) st_agent_u32(a.state + MXG_STATE_ACTIVE, gen);
+  if (a.state && blockIdx.x == 0 && tid == hand_tid && !(LORA && S > 1))
+    st_agent_u32(a.state + MXG_STATE_ACTIVE, gen);
 }
 
 }  // namespace
@@ -1034,6 +1339,10 @@ struct Variant {
           MXG_FN(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr,               \
           {MXG_FNL(RB, WN, WK, D, SK, false, 1, false),                              \
            MXG_FNL(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr}}
+// Sixteen worker waves leave no room for the adapters' side wave.
+#define MXG_V_16WAVES(RB, WN, WK, D, SK, XR)                                         \
+  Variant{TileCfg{RB, WN, WK, D, XR}, SK, MXG_FN(RB, WN, WK, D, SK, false, XR, false), \
+          MXG_FN(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr, {}}
 // Also built with x staged as BF16 (the tiles the chooser takes for the
 // workload shapes).
 #define MXG_V16(RB, WN, WK, D, SK)                                                   \

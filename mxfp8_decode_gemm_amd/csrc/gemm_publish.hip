@@ -125,21 +125,25 @@ size_t gemm_lds_bytes(const TileCfg& c, int m, int k_slice) {
   return kHeaderBytes + std::max(xbytes, red);
 }
 
+size_t lora_lds_bytes(int m, int rank) {
+  return kLoraList + (size_t)2 * m * rank * sizeof(uint16_t) + kLoraMaxPairs * sizeof(float) + 16;
+}
+
 bool tile_available(const TileCfg& c) { return find_variant(c, 1) != nullptr; }
 
 static bool choose_tile_uncached(int m, int n, int k, int split_k, const char* tile,
-                                 TileCfg* out, bool lora);
+                                 TileCfg* out, int lora_rank);
 
 // The default choice depends only on the sizes and the device: remembered
 // per key (a memo of device queries, not state that changes a result). A
 // forced tile is not remembered.
-bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* out, bool lora) {
-  if (tile) return choose_tile_uncached(m, n, k, split_k, tile, out, lora);
+bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* out, int lora_rank) {
+  if (tile) return choose_tile_uncached(m, n, k, split_k, tile, out, lora_rank);
   static std::mutex mu;
-  static std::map<std::tuple<int, int, int, int, int, bool>, std::pair<bool, TileCfg>> cache;
+  static std::map<std::tuple<int, int, int, int, int, int>, std::pair<bool, TileCfg>> cache;
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return false;
-  const auto key = std::make_tuple(dev, m, n, k, split_k, lora);
+  const auto key = std::make_tuple(dev, m, n, k, split_k, lora_rank);
   {
     std::lock_guard<std::mutex> g(mu);
     auto it = cache.find(key);
@@ -149,7 +153,7 @@ bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* ou
     }
   }
   TileCfg c{};
-  const bool ok = choose_tile_uncached(m, n, k, split_k, nullptr, &c, lora);
+  const bool ok = choose_tile_uncached(m, n, k, split_k, nullptr, &c, lora_rank);
   std::lock_guard<std::mutex> g(mu);
   cache[key] = std::make_pair(ok, c);
   *out = c;
@@ -157,16 +161,20 @@ bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* ou
 }
 
 static bool choose_tile_uncached(int m, int n, int k, int split_k, const char* tile,
-                                 TileCfg* out, bool lora) {
+                                 TileCfg* out, int lora_rank) {
+  const bool lora = lora_rank > 0;
+  const size_t lora_lds = lora ? lora_lds_bytes(m, lora_rank) : 0;
   const int ks = k / split_k;
   auto fits = [&](const TileCfg& c) {
     const Variant* v = find_variant(c, split_k);
-    if (!v || (c.x16 && !v->fn16) || gemm_lds_bytes(c, m, ks) > 160 * 1024) return false;
+    if (!v || !variant_fn(*v, false, c.x16, lora)) return false;
+    const size_t lds = gemm_lds_bytes(c, m, ks) + lora_lds;
+    if (lds > 160 * 1024) return false;
     if (split_k == 1) return true;
     // The workgroups of one tile wait for each other: the grid must be
     // resident all at once.
     const long tiles = (n + tile_rows(c) - 1) / tile_rows(c);
-    const long resident = gemm_resident_blocks(c, split_k, gemm_lds_bytes(c, m, ks), lora);
+    const long resident = gemm_resident_blocks(c, split_k, lds, lora);
     return resident > 0 && tiles * split_k <= resident && tiles * split_k <= MXG_WS_MAX_GROUPS;
   };
   int cus = 256;
@@ -284,7 +292,7 @@ long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool 
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds_bytes) !=
             hipSuccess)
       return -1;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, tile_threads(c, split_k),
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, tile_threads(c, split_k, lora),
                                                      lds_bytes) != hipSuccess)
       return -1;
     per_cu = n < per_cu ? n : per_cu;
@@ -316,11 +324,27 @@ hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t 
   const Variant* v = find_variant(c, a.split_k);
   if (!v) return hipErrorInvalidValue;
   const int tiles = (a.n + tile_rows(c) - 1) / tile_rows(c);
-  const dim3 grid(tiles * a.split_k), block(tile_threads(c, a.split_k));
-  const size_t lds = gemm_lds_bytes(c, a.m, a.k / a.split_k);
+  const bool lora = a.lora.b != nullptr;
+  const dim3 grid(tiles * a.split_k), block(tile_threads(c, a.split_k, lora));
+  size_t lds = gemm_lds_bytes(c, a.m, a.k / a.split_k);
   GemmArgs args = a;
+  if (lora) {
+    args.lora.lds_off = (int32_t)((lds + 15) / 16 * 16);
+    lds += lora_lds_bytes(a.m, a.lora.rank);
+    // u's dot products over at most 512 workgroups, each cut along K while
+    // there are workgroups left over.
+    args.lora.workers = grid.x < 512 ? (int32_t)grid.x : 512;
+    const int items = a.m * a.lora.rank;
+    int ps = 0;
+    if (items * ((a.k + 511) / 512) <= 16) {
+      args.lora.workers = 0;  // a few loads: no exchange
+    } else {
+      while (ps < 2 && (items << (ps + 1)) <= args.lora.workers && a.k >> (ps + 1) >= 512) ++ps;
+    }
+    args.lora.parts_log2 = ps;
+  }
   args.xcd_groups = a.split_k > 1 && tiles % 8 == 0 ? 1 : 0;
-  const void* fn = variant_fn(*v, a.xb != nullptr, c.x16, a.lora.b != nullptr);
+  const void* fn = variant_fn(*v, a.xb != nullptr, c.x16, lora);
   if (!fn) return hipErrorInvalidValue;
   if (lds > 64 * 1024) {
     const hipError_t e =

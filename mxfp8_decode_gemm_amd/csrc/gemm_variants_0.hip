@@ -9,7 +9,7 @@ namespace {
 const Variant kPart[] = {
     MXG_VARIANT16(1, 1, 4, 4),
     MXG_VARIANT(1, 1, 8, 4),
-    MXG_V(1, 1, 16, 4, 1),
+    MXG_V_16WAVES(1, 1, 16, 4, 1, 1),
 };
 }  // namespace
 

@@ -36,19 +36,4 @@ struct ExpertArgs {
 
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
 
-// u[t][r] = scale[i] * sum_k A[i][r][k] x[t][k], i = ids[t] (zeros without an
-// adapter), FP32. xb: BF16 x, or x and xs.
-struct ShrinkArgs {
-  const uint16_t* a;
-  const float* scale;
-  const int32_t* ids;
-  const uint16_t* xb;
-  const uint8_t* x;
-  const uint8_t* xs;
-  float* u;
-  int32_t adapters, rank, m, k;
-};
-
-hipError_t launch_shrink(const ShrinkArgs& a, hipStream_t s);
-
 }  // namespace mxg

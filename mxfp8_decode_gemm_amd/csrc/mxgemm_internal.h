@@ -10,14 +10,25 @@
 
 namespace mxg {
 
-// The adapters of mxgemm_lora as the GEMM's epilogue reads them:
-// C[t, n] += sum_r b[ids[t]][n][r] u[t][r], u holding the scaled A x.
+// The rows' adapters of mxgemm_lora, for the GEMM kernel's side wave and its
+// expansion step (gemm_kernel.h).
 struct LoraArgs {
-  const uint16_t* b;   // [adapters, n, rank] BF16, or null
-  const float* u;      // [m, rank]
-  const int32_t* ids;  // [m]
+  const uint16_t* a;      // [adapters, rank, k] BF16
+  const uint16_t* b;      // [adapters, n, rank] BF16, or null: no adapters
+  const float* scale;     // [adapters]
+  const int32_t* ids;     // [m]
   int32_t adapters, rank;
+  uint32_t* hdr;          // scratch header (words as the split-K workspace's)
+  uint32_t* flags;        // scratch: one epoch word per workgroup
+  uint64_t* pairs;        // scratch: (value, epoch) of every partial of u
+  // Set by the launcher: the K parts a value of u is summed from (1 << this),
+  // the workgroups that compute them (0: each computes all of u for itself),
+  // and where the kernel's LDS area starts.
+  int32_t parts_log2, workers, lds_off;
 };
+
+// Most (value, epoch) pairs of one call's u: rows * rank * parts.
+constexpr int kLoraMaxPairs = 8 * 128;
 
 // Everything one GEMM+publish launch needs, by value.
 struct GemmArgs {
@@ -63,21 +74,23 @@ struct TileCfg {
 };
 
 inline int tile_rows(const TileCfg& c) { return 16 * c.rb * c.wn; }
-// Worker waves, plus the control wave of split-K launches.
-inline int tile_threads(const TileCfg& c, int split_k) {
-  return 64 * (c.wn * c.wk + (split_k > 1 ? 1 : 0));
+// Worker waves, plus the side wave of split-K and adapter launches.
+inline int tile_threads(const TileCfg& c, int split_k, bool lora = false) {
+  return 64 * (c.wn * c.wk + (split_k > 1 || lora ? 1 : 0));
 }
 
 // Dynamic LDS bytes of a launch (x slice and its scales, or its BF16 form when
 // c.x16; the partial tile).
 size_t gemm_lds_bytes(const TileCfg& c, int m, int k_slice);
+// The adapters' LDS area, which a launch with them adds behind that.
+size_t lora_lds_bytes(int m, int rank);
 
 // The tile for a problem. tile null: the default choice; "fp8": the default
 // tile with x kept in FP8 in LDS; "rb,wn,wk,depth[,xr[,x16]]": exactly that
-// variant (fails when it does not fit). lora: the kernels with the adapters in
-// their epilogue. Returns false when no variant fits.
+// variant (fails when it does not fit). lora_rank: not 0 for the kernels
+// with adapters. Returns false when no variant fits.
 bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* out,
-                 bool lora = false);
+                 int lora_rank = 0);
 
 // Whether a variant is compiled in.
 bool tile_available(const TileCfg& c);

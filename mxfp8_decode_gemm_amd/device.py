@@ -274,14 +274,15 @@ class AdaptedLinear:
         adapters, rank = a.shape[:2]
         _tensor(b, "b", torch.bfloat16, (adapters, self.n, rank), dev)
         _tensor(scale, "scale", torch.float32, (adapters,), dev)
-        self.scratch_bytes = mx.mxgemm_lora_scratch_bytes(mx.MAX_ROWS, rank)
-        if self.scratch_bytes == 0 or adapters < 1:
-            raise ValueError("a: an adapter rank that mxgemm_lora does not take")
+        self.scratch_bytes = mx.mxgemm_lora_scratch_bytes(self.n)
+        if self.scratch_bytes == 0 or adapters < 1 or rank % 8 or not 8 <= rank <= mx.LORA_MAX_RANK:
+            raise ValueError("w or a: sizes that mxgemm_lora does not take")
         self.split_k = split_k
         self.w, self.w_scale = pack_weight(w, w_scale, self.n, self.k, stream)
         self.a, self.b, self.scale = a, b, scale
         self.workspace = Workspace(self.n, split_k, dev, stream) if split_k > 1 else None
-        self.scratch = torch.empty(self.scratch_bytes // 4, dtype=torch.float32, device=dev)
+        self.scratch = torch.empty(self.scratch_bytes // 4, dtype=torch.int32, device=dev)
+        mx.mxgemm_lora_scratch_init(self.scratch, self.scratch_bytes, stream)
         self.lora = mx.mxg_lora(a.data_ptr(), b.data_ptr(), scale.data_ptr(), None, adapters, rank)
 
     def _call(self, mb, x, ids, x_scale, c_out, stream):

@@ -9,8 +9,8 @@ BF16 may be off. The pieces of those bounds:
   ``tolerance``;
 * one BF16 rounding: one BF16 ulp of the exact value (half of it, doubled for
   a value that crosses a binade), as in ``tolerance``;
-* h held as two BF16 parts: the second part is at most 2^-9 |h| and rounded
-  by 2^-9 of itself, so 2^-18 |h|;
+* h, or an adapter's u, held as two BF16 parts: the second part is at most 2^-9 |h| and rounded
+  by 2^-9 of itself, so 2^-18 of the value;
 * silu and its product in FP32: exp, add, divide and two multiplies at no more
   than 2 ulp (2^-23) each, so 10 * 2^-23 of |h|; a change of the gate by d
   moves silu by at most 1.1 d (the largest slope of silu is 1.0998).
@@ -115,7 +115,7 @@ def adapted(x_shared, x, w, w_scale, a, b, scale, ids):
         if not 0 <= i < len(a):
             continue
         u = a[i] @ x[t]
-        du = REL_ABS_SUM * (np.abs(a[i]) @ np.abs(x[t])) + 2.0**-23 * np.abs(u)
+        du = REL_ABS_SUM * (np.abs(a[i]) @ np.abs(x[t])) + (2.0**-18 + 2.0**-23) * np.abs(u)
         exact[t] += scale[i] * (b[i] @ u)
         slack[t] += abs(scale[i]) * (np.abs(b[i]) @ (du + REL_ABS_SUM * np.abs(u)))
     return exact, bf16_quantum(exact) + slack + 2.0**-23 * np.abs(exact)

@@ -23,7 +23,8 @@ def mx():
 
 def test_exports_every_declared_function(mx):
     names = mx.header_functions(mx.DECODE_HEADER_PATH)
-    assert names == ["mxgemm_lora", "mxgemm_lora_scratch_bytes", "mxmoe_experts",
+    assert names == ["mxgemm_lora", "mxgemm_lora_scratch_bytes",
+                     "mxgemm_lora_scratch_init", "mxmoe_experts",
                      "mxmoe_pack_weight", "mxmoe_packed_scale_bytes", "mxmoe_packed_weight_bytes",
                      "mxmoe_route", "mxmoe_workspace_bytes"]
     assert not [n for n in names if not hasattr(mx.library(), n) or not hasattr(mx, n)]
@@ -52,9 +53,16 @@ def test_sizes(mx):
     for bad in ((0, 8, 128, 128), (129, 8, 128, 128), (1, 0, 128, 128), (1, 1, 192, 128),
                 (1, 1, 128, 64), (1, 1, 32896, 128), (1, 1, 128, 32896), (1 << 30, 4, 128, 128)):
         assert mx.mxmoe_workspace_bytes(*bad) == 0
-    assert mx.mxgemm_lora_scratch_bytes(8, 128) >= 8 * 128 * 4
-    for bad in ((0, 8), (9, 8), (1, 0), (1, 12), (1, 136)):
-        assert mx.mxgemm_lora_scratch_bytes(*bad) == 0
+    # header, an epoch word per workgroup, 1024 pairs
+    assert mx.mxgemm_lora_scratch_bytes(8) == 256 + 2048 * 4 + 1024 * 8
+    assert mx.mxgemm_lora_scratch_bytes(1 << 20) == 256 + (1 << 16) * 4 + 1024 * 8
+    for bad in (0, 12, -8):
+        assert mx.mxgemm_lora_scratch_bytes(bad) == 0
+    lib = mx.library()
+    assert lib.mxgemm_lora_scratch_init(None, 1 << 20, None) == -1
+    assert lib.mxgemm_lora_scratch_init(4096, 1024, None) == -1
+    assert lib.mxgemm_lora_scratch_init(4096, (1 << 20) + 8, None) == -1
+    assert lib.mxgemm_lora_scratch_init(4104, 1 << 20, None) == -2
 
 
 @pytest.mark.parametrize("kw,code", [

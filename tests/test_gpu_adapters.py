@@ -151,18 +151,53 @@ def test_publish_and_collect(env, split_k):
     assert mbx.state_words()[mx.STATE_ERROR] == 0
 
 
-def test_rows_behind_and_scratch(env):
-    """Rows behind the last stay as they were; what the scratch held before
-    does not matter."""
+def test_rows_behind(env):
+    """Rows behind the last stay as they were."""
     mx, dv = env
     c = Case(dv, 3, 264, 512, 1, 16, 3, seed=6)
     ids = torch.tensor([2, -1, 0], dtype=torch.int32, device="cuda")
     x = c._bf(c.xb)
     want = c.lin(x, ids).clone()
     out = torch.full((5, 264), 3.0, dtype=torch.bfloat16, device="cuda")
-    c.lin.scratch.view(torch.int32).fill_(-1)
     c.lin(x, ids, c_out=out[1:4])
     assert torch.equal(out[1:4], want) and (out[[0, 4]] == 3).all()
+
+
+def test_one_scratch_for_calls_of_all_sizes(env):
+    """The epoch keeps a call from taking an earlier one's pairs: other rows,
+    ids and values through one scratch, on two streams in order."""
+    mx, dv = env
+    c = Case(dv, 8, 1032, 1024, 4, 16, 3, seed=8)
+    side = torch.cuda.Stream()
+    x = c._bf(c.xb)
+    rng = np.random.default_rng(1)
+    for call in range(12):
+        m = int(rng.integers(1, 9))
+        ids = torch.from_numpy(rng.integers(-1, 3, m).astype(np.int32)).cuda()
+        rows = torch.from_numpy(rng.permutation(8)[:m]).cuda()
+        part = x[rows].contiguous()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side if call % 2 else torch.cuda.default_stream()):
+            got = c.lin(part, ids)
+        torch.cuda.synchronize()
+        fresh = dv.AdaptedLinear(torch.from_numpy(c.p.w).cuda(), torch.from_numpy(c.p.ws).cuda(),
+                                 c.lin.a, c.lin.b, c.lin.scale, 4)
+        assert torch.equal(got, fresh(part, ids))
+
+
+def test_marked_scratch(env):
+    """A scratch with its error word set (as a wait that gave up leaves it): the
+    same bits, every workgroup on its own."""
+    mx, dv = env
+    for split_k in (1, 4):
+        c = Case(dv, 3, 520, 1024, split_k, 24, 2, seed=9)
+        x, ids = c._bf(c.xb), torch.tensor([1, -1, 0], dtype=torch.int32, device="cuda")
+        want = c.lin(x, ids).clone()
+        c.lin.scratch[mx.WS_ERROR] = mx.ERR_SPLITK_SPIN
+        for _ in range(3):
+            assert torch.equal(c.lin(x, ids), want)
+        mx.mxgemm_lora_scratch_init(c.lin.scratch, c.lin.scratch_bytes)
+        assert torch.equal(c.lin(x, ids), want)
 
 
 def test_refusals(env):

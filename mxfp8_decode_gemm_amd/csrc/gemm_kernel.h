@@ -395,14 +395,16 @@ constexpr uint32_t kLoraPolls = 256;
 // then u's high parts [m][rank], its low parts, the partials (FP32).
 constexpr int kLoraList = 80;
 
-__device__ __forceinline__ float dot8(const uint4 a, const uint4 b, float s) {
-  const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    s = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), s);
-    s = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), s);
-  }
-  return s;
+// a . b of eight BF16 pairs (v_dot2_f32_bf16, FP32 sums).
+__device__ __forceinline__ float dot8(const uint4 a, const uint4 b) {
+  float s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, a.x),
+                                            __builtin_bit_cast(v2bf, b.x), 0.f, false);
+  s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, a.y), __builtin_bit_cast(v2bf, b.y),
+                                      s, false);
+  s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, a.z), __builtin_bit_cast(v2bf, b.z),
+                                      s, false);
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2bf, a.w),
+                                         __builtin_bit_cast(v2bf, b.w), s, false);
 }
 
 // The sum of x over the wave, in lane 63: row shifts, then row broadcasts.
@@ -434,6 +436,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
   int* const list = reinterpret_cast<int*>(lw);
   uint16_t* const uh = reinterpret_cast<uint16_t*>(lw + kLoraList);
   float* const part = reinterpret_cast<float*>(uh + 2 * m * rank);
+  float* const stage = part + kLoraMaxPairs;  // the pieces' sums, lane by lane
   // ---- hand-off words, ids, epoch: one round trip ------------------------
   int lid = l.ids[lane < m ? lane : 0];
   uint32_t lepoch = ld_agent_u32(l.hdr + MXG_WS_EPOCH);
@@ -529,16 +532,19 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
       }
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
-        if (q >= total) break;
-        if (piece * 512 + 8 * lane < len) {
-          if constexpr (QX) {
-            sum = dot8(av[j], xv[j], sum);
-          } else {  // the codes' products, then their scale (exact short of FP32's range)
-            const v8bf c = fp8x8_to_bf16(xv[j].x, xv[j].y, 1.0f);
-            sum += __builtin_amdgcn_ldexpf(dot8(av[j], __builtin_bit_cast(uint4, c), 0.f),
-                                           (int)sb[j] - 127);
-          }
+        float d;
+        if constexpr (QX) {
+          d = dot8(av[j], xv[j]);
+        } else {  // the codes' products, then their scale (exact short of FP32's range)
+          const v8bf c = fp8x8_to_bf16(xv[j].x, xv[j].y, 1.0f);
+          d = __builtin_amdgcn_ldexpf(dot8(av[j], __builtin_bit_cast(uint4, c)), (int)sb[j] - 127);
         }
+        stage[64 * j + lane] = d;
+      }
+      __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
+#pragma unroll 1
+      for (int j = 0; j < kPieces && q < total; ++j) {
+        if (piece * 512 + 8 * lane < len) sum += stage[64 * j + lane];
         if (++piece == per) {
           sum = wave_sum63(sum);
           if (lane == 63) {

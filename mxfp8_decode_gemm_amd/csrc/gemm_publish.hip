@@ -126,7 +126,7 @@ size_t gemm_lds_bytes(const TileCfg& c, int m, int k_slice) {
 }
 
 size_t lora_lds_bytes(int m, int rank) {
-  return kLoraList + (size_t)2 * m * rank * sizeof(uint16_t) + kLoraMaxPairs * sizeof(float) + 16;
+  return kLoraList + (size_t)2 * m * rank * sizeof(uint16_t) + (kLoraMaxPairs + 8 * 64) * sizeof(float) + 16;
 }
 
 bool tile_available(const TileCfg& c) { return find_variant(c, 1) != nullptr; }

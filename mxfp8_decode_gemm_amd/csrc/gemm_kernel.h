@@ -530,6 +530,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
           if (rflags) __builtin_amdgcn_s_barrier();
         }
       }
+      const bool one = q < total && per - piece >= kPieces;  // all of one task
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         float d;
@@ -539,12 +540,16 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
           const v8bf c = fp8x8_to_bf16(xv[j].x, xv[j].y, 1.0f);
           d = __builtin_amdgcn_ldexpf(dot8(av[j], __builtin_bit_cast(uint4, c)), (int)sb[j] - 127);
         }
-        stage[64 * j + lane] = d;
+        if (one)
+          sum += (piece + j) * 512 + 8 * lane < len ? d : 0.f;
+        else
+          stage[64 * j + lane] = d;
       }
+      if (one) piece += kPieces - 1;
       __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
 #pragma unroll 1
-      for (int j = 0; j < kPieces && q < total; ++j) {
-        if (piece * 512 + 8 * lane < len) sum += stage[64 * j + lane];
+      for (int j = one ? kPieces - 1 : 0; j < kPieces && q < total; ++j) {
+        if (!one && piece * 512 + 8 * lane < len) sum += stage[64 * j + lane];
         if (++piece == per) {
           sum = wave_sum63(sum);
           if (lane == 63) {

@@ -331,15 +331,18 @@ hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t 
   if (lora) {
     args.lora.lds_off = (int32_t)((lds + 15) / 16 * 16);
     lds += lora_lds_bytes(a.m, a.lora.rank);
-    // u's dot products over at most 512 workgroups, each cut along K while
-    // there are workgroups left over.
+    // u's dot products over at most 512 workgroups.
     args.lora.workers = grid.x < 512 ? (int32_t)grid.x : 512;
     const int items = a.m * a.lora.rank;
     int ps = 0;
     if (items * ((a.k + 511) / 512) <= 16) {
       args.lora.workers = 0;  // a few loads: no exchange
     } else {
-      while (ps < 2 && (items << (ps + 1)) <= args.lora.workers && a.k >> (ps + 1) >= 512) ++ps;
+      // A task's 8 pieces of 512 values are one round trip; beyond that, cut it
+      // while there are workgroups left over.
+      while (ps < 2 && a.k >> (ps + 1) >= 512 && (items << (ps + 1)) <= kLoraMaxPairs &&
+             (a.k >> ps > 8 * 512 || (items << (ps + 1)) <= args.lora.workers))
+        ++ps;
     }
     args.lora.parts_log2 = ps;
   }

@@ -145,30 +145,49 @@ def as_u16(t: torch.Tensor) -> np.ndarray:
 # ---------------------------------------------------------------------------
 
 
-def _tensor(t, name: str, dtype, shape, device=None, contiguous: bool = True) -> torch.Tensor:
-    """``t`` itself when it is a device tensor of this type and shape (None in
-    ``shape``: any size)."""
+# A decode step's calls take a few microseconds on the GPU, so the checks below
+# are written to cost less than that on the host.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_device = torch._C._cuda_getDevice
+
+
+def _refuse(t, name: str, dtype, shape, device) -> None:
+    """The reason why ``t`` is not a contiguous tensor of this type, shape (None:
+    any size) and device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name}: a device tensor is needed")
     if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise ValueError(f"{name}: {t.dtype} instead of {dtype}")
     if t.dim() != len(shape) or any(w is not None and w != g for g, w in zip(t.shape, shape)):
         raise ValueError(f"{name}: shape {tuple(t.shape)} instead of {tuple(shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
     if device is not None and t.device != device:
         raise ValueError(f"{name}: on {t.device}, not on {device}")
-    return t
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
 
 
-def _current(device: torch.device) -> None:
-    """A call runs on the current device: its tensors have to be there."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+def _address(t, name: str, dtype, shape: tuple, device) -> int:
+    """The address of a contiguous device tensor of this type and shape."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _on(device: torch.device, stream):
+    """The stream handle of a call whose tensors are on ``device``, which has to
+    be the current one."""
+    if device.index != _device():
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{_device()}")
+    if stream is None:
+        return _raw_stream(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 _SCORES = {"softmax": mx.ROUTE_SOFTMAX, "sigmoid": mx.ROUTE_SIGMOID}
+_LOGITS = {torch.float32: mx.F32, torch.bfloat16: mx.BF16}
+_lib = mx.library()
 
 
 def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor = None,
@@ -177,10 +196,10 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
           stream=None):
     """One mxmoe_route call on [tokens, experts] logits (float32 or bfloat16,
     rows of any stride): (ids int32, weights float32), each [tokens, top_k]."""
-    _tensor(logits, "logits", (torch.float32, torch.bfloat16), (None, None), contiguous=False)
+    kind = _LOGITS.get(logits.dtype) if isinstance(logits, torch.Tensor) else None
+    if kind is None or logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits: a float32 or bfloat16 device tensor [tokens, experts] is needed")
     tokens, experts = logits.shape
-    dev = logits.device
-    _current(dev)
     row_stride, step = logits.stride()
     if step != 1 and experts > 1:
         raise ValueError("logits: a row's values have to be contiguous")
@@ -188,32 +207,34 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
         row_stride = experts
     if score not in _SCORES:
         raise ValueError(f"score: {score!r} instead of one of {sorted(_SCORES)}")
-    if bias is not None:
-        _tensor(bias, "bias", torch.float32, (experts,), dev)
-    if ids is None:
-        ids = torch.empty(tokens, max(top_k, 0), dtype=torch.int32, device=dev)
-    else:
-        _tensor(ids, "ids", torch.int32, (tokens, top_k), dev)
-    if weights is None:
-        weights = torch.empty(tokens, max(top_k, 0), dtype=torch.float32, device=dev)
-    else:
-        _tensor(weights, "weights", torch.float32, (tokens, top_k), dev)
+    dev = logits.device
+    handle = _on(dev, stream)
+    out = (tokens, top_k)
+    if ids is None and top_k > 0:
+        ids = torch.empty(out, dtype=torch.int32, device=dev)
+    if weights is None and top_k > 0:
+        weights = torch.empty(out, dtype=torch.float32, device=dev)
     router = mx.mxmoe_router(experts, top_k, _SCORES[score], groups, top_groups, group_best,
                              int(renormalize), scale)
-    mx.mxmoe_route(router, logits, mx.F32 if logits.dtype == torch.float32 else mx.BF16,
-                   row_stride, bias, tokens, ids, weights, stream)
+    code = _lib.mxmoe_route(
+        router, logits.data_ptr(), kind, row_stride,
+        None if bias is None else _address(bias, "bias", torch.float32, (experts,), dev), tokens,
+        _address(ids, "ids", torch.int32, out, dev),
+        _address(weights, "weights", torch.float32, out, dev), handle)
+    if code:
+        mx._check(code, "mxmoe_route")
     return ids, weights
 
 
 def pack_experts(w: torch.Tensor, ws: torch.Tensor, stream=None):
     """Packed copies of [experts, n, k] codes and their scales."""
-    _tensor(w, "w", torch.uint8, (None, None, None))
+    _refuse(w, "w", torch.uint8, (None, None, None), None)
     e, n, k = w.shape
-    _tensor(ws, "w_scale", torch.uint8, (e, n, k // 32), w.device)
-    _current(w.device)
+    _refuse(ws, "w_scale", torch.uint8, (e, n, k // 32), w.device)
+    handle = _on(w.device, stream)
     wp = torch.empty(mx.mxmoe_packed_weight_bytes(e, n, k), dtype=torch.uint8, device=w.device)
     wsp = torch.empty(mx.mxmoe_packed_scale_bytes(e, n, k), dtype=torch.uint8, device=w.device)
-    mx.mxmoe_pack_weight(w, ws, e, n, k, wp, wsp, stream)
+    mx.mxmoe_pack_weight(w, ws, e, n, k, wp, wsp, handle)
     return wp, wsp
 
 
@@ -225,35 +246,40 @@ class Experts:
 
     def __init__(self, w13: torch.Tensor, w13_scale: torch.Tensor, w2: torch.Tensor,
                  w2_scale: torch.Tensor, max_pairs: int = mx.MOE_MAX_PAIRS, stream=None) -> None:
-        _tensor(w13, "w13", torch.uint8, (None, None, None))
+        _refuse(w13, "w13", torch.uint8, (None, None, None), None)
         self.experts, two, self.hidden = w13.shape
         self.inter = two // 2
-        _tensor(w2, "w2", torch.uint8, (self.experts, self.hidden, self.inter), w13.device)
+        dev = self.device = w13.device
+        _refuse(w2, "w2", torch.uint8, (self.experts, self.hidden, self.inter), dev)
         self.nbytes = mx.mxmoe_workspace_bytes(max_pairs, 1, self.hidden, self.inter)
         if two % 2 or self.nbytes == 0:
             raise ValueError("w13, w2 or max_pairs: sizes that mxmoe_experts does not take")
-        self.max_pairs, self.device = max_pairs, w13.device
         self.w13, self.w13_scale = pack_experts(w13, w13_scale, stream)
         self.w2, self.w2_scale = pack_experts(w2, w2_scale, stream)
-        self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=w13.device)
+        self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
+        self._weights = (self.w13.data_ptr(), self.w13_scale.data_ptr(), self.w2.data_ptr(),
+                         self.w2_scale.data_ptr())
 
     def __call__(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
                  out: torch.Tensor = None, stream=None) -> torch.Tensor:
         """One mxmoe_experts call: BF16 x [tokens, hidden], ids and weights as
         ``route`` returns them; BF16 [tokens, hidden]."""
         dev = self.device
-        _current(dev)
-        _tensor(ids, "ids", torch.int32, (None, None), dev)
-        tokens, top_k = ids.shape
-        _tensor(x, "x", torch.bfloat16, (tokens, self.hidden), dev)
-        _tensor(weights, "weights", torch.float32, (tokens, top_k), dev)
+        handle = _on(dev, stream)
+        if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+            raise ValueError("ids: a device tensor [tokens, top_k] is needed")
+        chosen = ids.shape
+        rows = (chosen[0], self.hidden)
+        px = _address(x, "x", torch.bfloat16, rows, dev)
         if out is None:
             out = torch.empty_like(x)
-        else:
-            _tensor(out, "out", torch.bfloat16, (tokens, self.hidden), dev)
-        mx.mxmoe_experts(x, ids, weights, self.w13, self.w13_scale, self.w2, self.w2_scale,
-                         tokens, top_k, self.experts, self.hidden, self.inter, self.workspace,
-                         self.nbytes, out, stream)
+        code = _lib.mxmoe_experts(
+            px, _address(ids, "ids", torch.int32, chosen, dev),
+            _address(weights, "weights", torch.float32, chosen, dev), *self._weights, chosen[0],
+            chosen[1], self.experts, self.hidden, self.inter, self.workspace.data_ptr(),
+            self.nbytes, _address(out, "out", torch.bfloat16, rows, dev), handle)
+        if code:
+            mx._check(code, "mxmoe_experts")
         return out
 
 
@@ -265,55 +291,58 @@ class AdaptedLinear:
 
     def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
                  scale: torch.Tensor, split_k: int = 1, stream=None) -> None:
-        _tensor(w, "w", torch.uint8, (None, None))
+        _refuse(w, "w", torch.uint8, (None, None), None)
         self.n, self.k = w.shape
         dev = self.device = w.device
-        _current(dev)
-        _tensor(w_scale, "w_scale", torch.uint8, (self.n, self.k // 32), dev)
-        _tensor(a, "a", torch.bfloat16, (None, None, self.k), dev)
+        handle = _on(dev, stream)
+        _refuse(w_scale, "w_scale", torch.uint8, (self.n, self.k // 32), dev)
+        _refuse(a, "a", torch.bfloat16, (None, None, self.k), dev)
         adapters, rank = a.shape[:2]
-        _tensor(b, "b", torch.bfloat16, (adapters, self.n, rank), dev)
-        _tensor(scale, "scale", torch.float32, (adapters,), dev)
+        _refuse(b, "b", torch.bfloat16, (adapters, self.n, rank), dev)
+        _refuse(scale, "scale", torch.float32, (adapters,), dev)
         self.scratch_bytes = mx.mxgemm_lora_scratch_bytes(self.n)
         if self.scratch_bytes == 0 or adapters < 1 or rank % 8 or not 8 <= rank <= mx.LORA_MAX_RANK:
             raise ValueError("w or a: sizes that mxgemm_lora does not take")
         self.split_k = split_k
-        self.w, self.w_scale = pack_weight(w, w_scale, self.n, self.k, stream)
+        self.w, self.w_scale = pack_weight(w, w_scale, self.n, self.k, handle)
         self.a, self.b, self.scale = a, b, scale
-        self.workspace = Workspace(self.n, split_k, dev, stream) if split_k > 1 else None
+        self.workspace = Workspace(self.n, split_k, dev, handle) if split_k > 1 else None
         self.scratch = torch.empty(self.scratch_bytes // 4, dtype=torch.int32, device=dev)
-        mx.mxgemm_lora_scratch_init(self.scratch, self.scratch_bytes, stream)
+        mx.mxgemm_lora_scratch_init(self.scratch, self.scratch_bytes, handle)
         self.lora = mx.mxg_lora(a.data_ptr(), b.data_ptr(), scale.data_ptr(), None, adapters, rank)
+        self._weights = self.w.data_ptr(), self.w_scale.data_ptr()
+        ws = self.workspace
+        self._memory = (ws.buf.data_ptr(), ws.nbytes) if ws else (None, 0)
 
     def _call(self, mb, x, ids, x_scale, c_out, stream):
         dev = self.device
-        _current(dev)
+        handle = _on(dev, stream)
+        if not isinstance(x, torch.Tensor) or x.dim() != 2:
+            raise ValueError("x: a device tensor [m, k] is needed")
         m = x.shape[0]
         if x_scale is None:
-            _tensor(x, "x", torch.bfloat16, (None, self.k), dev)
-            form = (None, None, x)
+            form = None, None, _address(x, "x", torch.bfloat16, (m, self.k), dev)
         else:
-            _tensor(x, "x", torch.uint8, (None, self.k), dev)
-            _tensor(x_scale, "x_scale", torch.uint8, (m, self.k // 32), dev)
-            form = (x, x_scale, None)
-        _tensor(ids, "ids", torch.int32, (m,), dev)
-        if c_out is not None:
-            _tensor(c_out, "c_out", torch.bfloat16, (m, self.n), dev)
-        self.lora.ids = ids.data_ptr()
-        ws = self.workspace
-        mx.mxgemm_lora(mb, self.w, self.w_scale, *form, m, self.n, self.k, self.split_k,
-                       ws.buf if ws else None, ws.nbytes if ws else 0, self.lora, self.scratch,
-                       self.scratch_bytes, c_out, stream)
+            form = (_address(x, "x", torch.uint8, (m, self.k), dev),
+                    _address(x_scale, "x_scale", torch.uint8, (m, self.k // 32), dev), None)
+        # (Read by the library within the call.)
+        self.lora.ids = _address(ids, "ids", torch.int32, (m,), dev)
+        if mb is None and c_out is None:
+            c_out = torch.empty(m, self.n, dtype=torch.bfloat16, device=dev)
+        pc = None if c_out is None else _address(c_out, "c_out", torch.bfloat16, (m, self.n), dev)
+        code = _lib.mxgemm_lora(mb, *self._weights, *form, m, self.n, self.k, self.split_k,
+                                *self._memory, self.lora, self.scratch.data_ptr(),
+                                self.scratch_bytes, pc, handle)
+        if code:
+            mx._check(code, "mxgemm_lora")
+        return c_out
 
     def __call__(self, x: torch.Tensor, ids: torch.Tensor, x_scale: torch.Tensor = None,
                  c_out: torch.Tensor = None, stream=None) -> torch.Tensor:
         """One mxgemm_lora call without a mailbox: BF16 x [m, k], or uint8 codes
         with x_scale [m, k/32]; ids int32 [m] (outside 0..adapters-1: none).
         BF16 [m, n]."""
-        if c_out is None:
-            c_out = torch.empty(x.shape[0], self.n, dtype=torch.bfloat16, device=x.device)
-        self._call(None, x, ids, x_scale, c_out, stream)
-        return c_out
+        return self._call(None, x, ids, x_scale, c_out, stream)
 
     def publish(self, mailbox: Mailbox, x: torch.Tensor, ids: torch.Tensor,
                 x_scale: torch.Tensor = None, c_out: torch.Tensor = None, stream=None) -> None:

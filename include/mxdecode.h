@@ -100,8 +100,10 @@ int mxmoe_pack_weight(const uint8_t* w, const uint8_t* w_scale, int32_t experts,
                       int32_t k, uint8_t* w_packed, uint8_t* ws_packed, void* stream);
 
 /* Bytes of workspace mxmoe_experts needs for these sizes; 0 on bad sizes. It
- * needs no arming, and holds nothing from one call to the next. */
-size_t mxmoe_workspace_bytes(int32_t tokens, int32_t top_k, int32_t hidden, int32_t inter);
+ * needs no arming, and holds nothing from one call to the next. A workspace
+ * serves every call with as many pairs (tokens * top_k) or fewer. */
+size_t mxmoe_workspace_bytes(int32_t tokens, int32_t top_k, int32_t experts, int32_t hidden,
+                             int32_t inter);
 
 /* The gated product of the chosen experts:
  *

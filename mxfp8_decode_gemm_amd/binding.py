@@ -159,7 +159,7 @@ def _load() -> ctypes.CDLL:
         "mxmoe_packed_weight_bytes": (sz, [i32, i32, i32]),
         "mxmoe_packed_scale_bytes": (sz, [i32, i32, i32]),
         "mxmoe_pack_weight": (ctypes.c_int, [vp, vp, i32, i32, i32, vp, vp, vp]),
-        "mxmoe_workspace_bytes": (sz, [i32, i32, i32, i32]),
+        "mxmoe_workspace_bytes": (sz, [i32, i32, i32, i32, i32]),
         "mxmoe_experts": (ctypes.c_int, [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp,
                                          sz, vp, vp]),
         "mxgemm_lora_scratch_bytes": (sz, [i32]),
@@ -452,8 +452,8 @@ def mxmoe_pack_weight(w, w_scale, experts: int, n: int, k: int, w_packed, ws_pac
                                   _ptr(ws_packed), _stream(stream)), "mxmoe_pack_weight")
 
 
-def mxmoe_workspace_bytes(tokens: int, top_k: int, hidden: int, inter: int) -> int:
-    return int(_lib.mxmoe_workspace_bytes(tokens, top_k, hidden, inter))
+def mxmoe_workspace_bytes(tokens: int, top_k: int, experts: int, hidden: int, inter: int) -> int:
+    return int(_lib.mxmoe_workspace_bytes(tokens, top_k, experts, hidden, inter))
 
 
 def mxmoe_experts(x, ids, weights, w13, w13_scale, w2, w2_scale, tokens: int, top_k: int,

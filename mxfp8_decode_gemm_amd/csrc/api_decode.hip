@@ -19,15 +19,12 @@ int hip_code(hipError_t e) { return e == hipSuccess ? MXG_OK : MXG_EHIP; }
 
 constexpr int32_t kMaxDim = 32768;  // of hidden and inter
 
-bool expert_sizes_ok(int32_t tokens, int32_t top_k, int32_t hidden, int32_t inter) {
-  return tokens >= 1 && top_k >= 1 && (int64_t)tokens * top_k <= MXG_MOE_MAX_PAIRS && hidden > 0 &&
+bool expert_sizes_ok(int32_t tokens, int32_t top_k, int32_t experts, int32_t hidden,
+                     int32_t inter) {
+  return experts >= 1 && experts <= MXG_MOE_MAX_EXPERTS && tokens >= 1 && top_k >= 1 && (int64_t)tokens * top_k <= MXG_MOE_MAX_PAIRS && hidden > 0 &&
          hidden <= kMaxDim && hidden % 128 == 0 && inter > 0 && inter <= kMaxDim &&
          inter % 128 == 0;
 }
-
-// The workspace: h (two BF16 parts), then y (FP32).
-size_t h_bytes(int64_t pairs, int32_t inter) { return (size_t)pairs * inter * 4; }
-size_t y_bytes(int64_t pairs, int32_t hidden) { return (size_t)pairs * hidden * 4; }
 }  // namespace
 
 extern "C" {
@@ -90,10 +87,16 @@ int mxmoe_pack_weight(const uint8_t* w, const uint8_t* w_scale, int32_t experts,
   return MXG_OK;
 }
 
-size_t mxmoe_workspace_bytes(int32_t tokens, int32_t top_k, int32_t hidden, int32_t inter) {
-  if (!expert_sizes_ok(tokens, top_k, hidden, inter)) return 0;
-  const int64_t pairs = (int64_t)tokens * top_k;
-  return h_bytes(pairs, inter) + y_bytes(pairs, hidden);
+size_t mxmoe_workspace_bytes(int32_t tokens, int32_t top_k, int32_t experts, int32_t hidden,
+                             int32_t inter) {
+  if (!expert_sizes_ok(tokens, top_k, experts, hidden, inter)) return 0;
+  ExpertArgs a = {};
+  a.tokens = tokens;
+  a.top_k = top_k;
+  a.experts = experts;
+  a.hidden = hidden;
+  a.inter = inter;
+  return experts_workspace(&a, nullptr);
 }
 
 int mxmoe_experts(const uint16_t* x, const int32_t* ids, const float* weights,
@@ -102,16 +105,13 @@ int mxmoe_experts(const uint16_t* x, const int32_t* ids, const float* weights,
                   int32_t hidden, int32_t inter, void* workspace, size_t workspace_bytes,
                   uint16_t* out, void* stream) {
   if (!x || !ids || !weights || !w13 || !w13_scale || !w2 || !w2_scale || !out) return MXG_EINVAL;
-  if (!expert_sizes_ok(tokens, top_k, hidden, inter) || experts < 1 ||
-      experts > MXG_MOE_MAX_EXPERTS)
-    return MXG_EINVAL;
+  if (!expert_sizes_ok(tokens, top_k, experts, hidden, inter)) return MXG_EINVAL;
   if (!aligned16(x) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned16(w13) ||
       !aligned16(w13_scale) || !aligned16(w2) || !aligned16(w2_scale) || !aligned16(out))
     return MXG_EALIGN;
-  if (!workspace || workspace_bytes < mxmoe_workspace_bytes(tokens, top_k, hidden, inter))
+  if (!workspace || workspace_bytes < mxmoe_workspace_bytes(tokens, top_k, experts, hidden, inter))
     return MXG_EWORKSPACE;
   if (!aligned16(workspace)) return MXG_EALIGN;
-  const int64_t pairs = (int64_t)tokens * top_k;
   ExpertArgs a;
   a.x = x;
   a.ids = ids;
@@ -129,8 +129,7 @@ int mxmoe_experts(const uint16_t* x, const int32_t* ids, const float* weights,
   a.experts = experts;
   a.hidden = hidden;
   a.inter = inter;
-  a.h = static_cast<uint16_t*>(workspace);
-  a.y = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + h_bytes(pairs, inter));
+  experts_workspace(&a, workspace);
   a.out = out;
   return hip_code(launch_experts(a, static_cast<hipStream_t>(stream)));
 }

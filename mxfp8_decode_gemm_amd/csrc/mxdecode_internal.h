@@ -22,6 +22,8 @@ struct RouteArgs {
 
 hipError_t launch_route(const RouteArgs& a, int logits_type, hipStream_t s);
 
+struct WidePlan;  // experts.hip
+
 struct ExpertArgs {
   const uint16_t* x;       // [tokens, hidden] BF16
   const int32_t* ids;      // [tokens * top_k]
@@ -29,10 +31,18 @@ struct ExpertArgs {
   const uint8_t *w13, *w13s, *w2, *w2s;  // packed
   size_t w13_bytes, w13s_bytes, w2_bytes, w2s_bytes;  // of one expert
   int32_t tokens, top_k, experts, hidden, inter;
-  uint16_t* h;             // workspace: [2][pairs][inter] BF16, high then low parts
-  float* y;                // workspace: [pairs][hidden]
+  // Workspace (experts_workspace): the sorted pairs, x in column tiles, h in
+  // two BF16 parts, y [pairs][hidden].
+  WidePlan* plan;
+  uint4* xp;
+  uint16_t* h;
+  float* y;
   uint16_t* out;           // [tokens, hidden] BF16
 };
+
+// Lays the workspace pointers of a call of these sizes out from base; returns
+// the bytes.
+size_t experts_workspace(ExpertArgs* a, void* base);
 
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
 

@@ -251,7 +251,7 @@ class Experts:
         self.inter = two // 2
         dev = self.device = w13.device
         _refuse(w2, "w2", torch.uint8, (self.experts, self.hidden, self.inter), dev)
-        self.nbytes = mx.mxmoe_workspace_bytes(max_pairs, 1, self.hidden, self.inter)
+        self.nbytes = mx.mxmoe_workspace_bytes(max_pairs, 1, self.experts, self.hidden, self.inter)
         if two % 2 or self.nbytes == 0:
             raise ValueError("w13, w2 or max_pairs: sizes that mxmoe_experts does not take")
         self.w13, self.w13_scale = pack_experts(w13, w13_scale, stream)

@@ -49,9 +49,14 @@ def test_sizes(mx):
         assert mx.mxmoe_packed_weight_bytes(*bad) == 0
         assert mx.mxmoe_packed_scale_bytes(*bad) == 0
     # at least h in two BF16 parts and y in FP32 for every pair
-    assert mx.mxmoe_workspace_bytes(8, 8, 7168, 2048) >= 64 * 4 * (7168 + 2048)
-    for bad in ((0, 8, 128, 128), (129, 8, 128, 128), (1, 0, 128, 128), (1, 1, 192, 128),
-                (1, 1, 128, 64), (1, 1, 32896, 128), (1, 1, 128, 32896), (1 << 30, 4, 128, 128)):
+    assert mx.mxmoe_workspace_bytes(8, 8, 64, 7168, 2048) >= 64 * 4 * (7168 + 2048)
+    # and more for more pairs, whatever the shape of the call
+    sizes = [mx.mxmoe_workspace_bytes(p, 1, 24, 256, 384) for p in range(1, 1025)]
+    assert sizes == sorted(sizes) and mx.mxmoe_workspace_bytes(16, 8, 24, 256, 384) == sizes[127]
+    for bad in ((0, 8, 4, 128, 128), (129, 8, 4, 128, 128), (1, 0, 4, 128, 128),
+                (1, 1, 0, 128, 128), (1, 1, 1025, 128, 128), (1, 1, 4, 192, 128),
+                (1, 1, 4, 128, 64), (1, 1, 4, 32896, 128), (1, 1, 4, 128, 32896),
+                (1 << 30, 4, 4, 128, 128)):
         assert mx.mxmoe_workspace_bytes(*bad) == 0
     # header, an epoch word per workgroup, 1024 pairs
     assert mx.mxgemm_lora_scratch_bytes(8) == 256 + 2048 * 4 + 1024 * 8

@@ -18,6 +18,10 @@ struct RouteArgs {
   int32_t tokens;
   int32_t* ids;
   float* weights;
+  // Set by the launcher: e / (experts / groups) = e * per_inv >> 20, and the
+  // power of two of lanes that share a group (aligned: that hold it).
+  uint32_t per_inv;
+  int32_t group_log, aligned;
 };
 
 hipError_t launch_route(const RouteArgs& a, int logits_type, hipStream_t s);

@@ -1,19 +1,23 @@
 // Expert routing (gfx950): mxmoe_route of include/mxdecode.h.
 //
-// One wave per row. Lane l holds the logits of experts l, l + 64, ... in
-// registers (V of them), so a row is read once, coalesced, and everything
-// after it is cross-lane work:
+// One wave per row. Lane l holds the logits of V neighbouring experts in
+// registers, so a row is read once, in wide loads, and everything after it is
+// cross-lane work:
 //   * score s = softmax or sigmoid, choice c = s + bias;
 //   * group scores (with groups), the kept groups as one 64-bit lane mask;
 //   * top_k rounds of a wave-wide maximum of c, each taking the lowest index
 //     among equals, the chosen one struck out.
-// Choices are compared in FP64: among thousands of rows, two FP32 choices
-// (a rounded sum of a rounded exponential) do fall on the wrong side of each
-// other. Where the choice has the order of the logits themselves (no bias,
-// and no sum of two in a group score), the logits are compared instead and no
-// FP64 exponential is taken, except above kNearOne. The weights are FP32.
+// Choices are compared as FP64 would compare them: among thousands of rows, two
+// FP32 choices (a rounded sum of a rounded exponential) do fall on the wrong
+// side of each other. Where the choice has the order of the logits themselves
+// (no bias, and no sum of two in a group score) the FP32 logits decide;
+// otherwise FP32 choices do where all that matter lie further apart than
+// their error, and the row is done again in FP64 where not (one row in some
+// hundred). The weights are FP32.
 
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "mxdecode_internal.h"
 
@@ -51,10 +55,19 @@ __device__ __forceinline__ double wave_max(double x) {
   return lane_f64(x, 63);
 }
 
+// The sum of the wave, uniform.
 __device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
-  return x;
+#define MXG_DPP_ADD(C, MASK)                                                               \
+  x += __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), C, \
+                                                             MASK, 0xF, true))
+  MXG_DPP_ADD(0x111, 0xF);
+  MXG_DPP_ADD(0x112, 0xF);
+  MXG_DPP_ADD(0x114, 0xF);
+  MXG_DPP_ADD(0x118, 0xF);
+  MXG_DPP_ADD(0x142, 0xA);
+  MXG_DPP_ADD(0x143, 0xC);
+#undef MXG_DPP_ADD
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 63));
 }
 __device__ __forceinline__ double wave_sum(double x) {
 #pragma unroll
@@ -90,96 +103,59 @@ __device__ __forceinline__ double sigmoid_order(float l) {
   return l > (float)kZeroBelow ? (double)l : kZeroBelow;
 }
 
-template <int V, bool BF16>
-__global__ void __launch_bounds__(64 * kWaves) route_kernel(RouteArgs a) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row = blockIdx.x * kWaves + wave;
-  if (row >= a.tokens) return;  // whole waves; no barrier below
-  const int E = a.r.experts;
+// What the lanes of a row's wave hold: lane l the experts V l .. V l + V - 1, so
+// that a row is read in wide loads and the lowest index of equals is the first
+// lane's.
+template <int V>
+struct Row {
+  float l[V];  // the logits; -infinity: out
+  float top, inv;  // softmax: the largest, 1 / sum of the terms
+};
+
+// Chooses in FP64: lane j gets the expert of place j (-1: none).
+template <int V>
+__device__ __forceinline__ int choose_wide(const RouteArgs& a, const Row<V>& row,
+                                                     double* cs, int lane) {
+  const int E = a.r.experts, G = a.r.groups, per = E / G;
   const bool softmax = a.r.score == MXG_ROUTE_SOFTMAX;
-  const int per = E / a.r.groups;
-
-  float l[V];
+  const bool by_logit = !a.bias && (G == 1 || a.r.group_best == 1 || per == 1);
+  double c[V];
+  double inv = 1.0;
+  if (softmax && !by_logit) {
+    double sum = 0.0;
+    if (row.top > -INFINITY) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = i * 64 + lane;
-    float v = -INFINITY;
-    if (e < E) {
-      const int64_t at = (int64_t)row * a.row_stride + e;
-      if constexpr (BF16)
-        v = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(a.logits)[at] << 16);
-      else
-        v = reinterpret_cast<const float*>(a.logits)[at];
-    }
-    l[i] = v > -INFINITY ? v : -INFINITY;  // NaN: out
-  }
-
-  // Softmax: the largest logit and the sum of the terms.
-  float top = 0.f, inv = 0.f;
-  if (softmax) {
-    double m = l[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) m = fmax(m, (double)l[i]);
-    top = (float)wave_max(m);
-    float sum = 0.f;
-    if (top > -INFINITY) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) sum += soft_term<float>(l[i], top);
+      for (int i = 0; i < V; ++i) sum += soft_term<double>(row.l[i], row.top);
     }
     sum = wave_sum(sum);
-    inv = sum > 0.f ? 1.f / sum : 0.f;
+    inv = sum > 0.0 ? 1.0 / sum : 0.0;
   }
-
-  // The choices.
-  double c[V];
-  const bool by_logit = !a.bias && (a.r.groups == 1 || a.r.group_best == 1 || per == 1);
-  if (by_logit) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      c[i] = -INFINITY;
-      if (l[i] > -INFINITY) {
+  for (int i = 0; i < V; ++i) {
+    const float l = row.l[i];
+    double s = -INFINITY;
+    if (l > -INFINITY) {
+      if (by_logit) {
         if (softmax)  // (the difference is NaN where both are +infinity)
-          c[i] = l[i] == top ? 0.0 : fmax((double)l[i] - (double)top, kZeroBelow);
+          s = l == row.top ? 0.0 : fmax((double)l - (double)row.top, kZeroBelow);
         else
-          c[i] = sigmoid_order(l[i]);
-      }
-    }
-  } else {
-    double inv64 = 1.0;
-    if (softmax) {
-      double sum = 0.0;
-      if (top > -INFINITY) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum += soft_term<double>(l[i], top);
-      }
-      sum = wave_sum(sum);
-      inv64 = sum > 0.0 ? 1.0 / sum : 0.0;
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = i * 64 + lane;
-      double s = -INFINITY;
-      if (l[i] > -INFINITY) {
-        s = softmax ? soft_term<double>(l[i], top) * inv64 : sigmoid64(l[i]);
+          s = sigmoid_order(l);
+      } else {
+        s = softmax ? soft_term<double>(l, row.top) * inv : sigmoid64(l);
         if (s < kLeast) s = 0.0;
-        if (a.bias) s += (double)a.bias[e];
+        if (a.bias) s += (double)a.bias[V * lane + i];
         if (!(s > -INFINITY)) s = -INFINITY;  // a NaN bias: out
       }
-      c[i] = s;
     }
+    c[i] = s;
   }
-
-  if (a.r.groups > 1 && a.r.top_groups < a.r.groups) {
-    double* cs = reinterpret_cast<double*>(lds) + (size_t)wave * E;
+  if (G > 1 && a.r.top_groups < G) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (i * 64 + lane < E) cs[i * 64 + lane] = c[i];
+      if (V * lane + i < E) cs[V * lane + i] = c[i];
     __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
-    // Lane g: the score of group g.
-    double score = -INFINITY;
-    if (lane < a.r.groups) {
+    double score = -INFINITY;         // lane g: of group g
+    if (lane < G) {
       double b1 = -INFINITY, b2 = -INFINITY;
       for (int q = lane * per; q < (lane + 1) * per; ++q) {
         const double v = cs[q];
@@ -189,52 +165,285 @@ __global__ void __launch_bounds__(64 * kWaves) route_kernel(RouteArgs a) {
       score = a.r.group_best == 2 && b2 > -INFINITY ? b1 + b2 : b1;
     }
     int ahead = 0;  // groups before this one
-    for (int g = 0; g < a.r.groups; ++g) {
-      const double s = lane_f64(score, g);
-      ahead += s > score || (s == score && g < lane) ? 1 : 0;
+    for (int g = 0; g < G; ++g) {
+      const double o = lane_f64(score, g);
+      ahead += o > score || (o == score && g < lane) ? 1 : 0;
     }
-    const uint64_t kept = __ballot(lane < a.r.groups && ahead < a.r.top_groups);
+    const uint64_t kept = __ballot(lane < G && ahead < a.r.top_groups);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = i * 64 + lane;
+      const int e = V * lane + i;
       if (e < E && !((kept >> (e / per)) & 1)) c[i] = -INFINITY;
     }
   }
-
-  // top_k rounds; lane j keeps the j-th expert and its logit.
   int id = -1;
-  float logit = -INFINITY;
   for (int j = 0; j < a.r.top_k; ++j) {
-    double m = c[0];
+    double best = c[0];
 #pragma unroll
-    for (int i = 1; i < V; ++i) m = fmax(m, c[i]);
-    m = wave_max(m);
+    for (int i = 1; i < V; ++i) best = fmax(best, c[i]);
+    const double m = wave_max(best);
     if (!(m > -INFINITY)) break;  // nothing left
-    bool found = false;
+    const int who = __ffsll((unsigned long long)__ballot(best == m)) - 1;
+    int at = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint64_t eq = __ballot(c[i] == m);
-      if (!found && eq) {
-        found = true;
-        const int who = __ffsll((unsigned long long)eq) - 1;
-        const float li = __uint_as_float(
-            (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(l[i]), who));
-        if (lane == j) {
-          id = i * 64 + who;
-          logit = li;
-        }
-        if (lane == who) c[i] = -INFINITY;
+    for (int i = V - 1; i >= 0; --i)
+      if (c[i] == m) at = i;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (lane == who && at == i) c[i] = -INFINITY;
+    at = __builtin_amdgcn_readlane(at, who);
+    if (lane == j) id = V * who + at;
+  }
+  return id;
+}
+
+// ---- FP32 choices, where they decide ---------------------------------------
+// Either the logits themselves (exact), or choices with an error below
+// 2^-19 (1 + |c|), given up where two that matter lie closer than kTol:
+//   sigmoid: 1 / (1 + e), e = 2^(-l log2 e) to 1.5 |l| 2^-24 + 2^-22 relative,
+//   moves s by at most s (1 - s) of that, s (1 - s) |l| < 0.23; softmax: the
+//   term the same with s |d| < 0.37, the sum's 22 roundings; one reciprocal; the
+//   sum with the bias. A group's score adds two.
+constexpr float kTol = 0x1p-17f;
+
+// Floats as integers of the same order (negative zero just below zero).
+__device__ __forceinline__ int key_of(float x) {
+  const int b = (int)__float_as_uint(x);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float of_key(int k) {
+  return __uint_as_float((uint32_t)(k ^ ((k >> 31) & 0x7FFFFFFF)));
+}
+constexpr int kOut = (int)0x80000000;  // below every key
+
+// The largest x of the wave, uniform.
+__device__ __forceinline__ int wave_max(int x) {
+#define MXG_DPP_MAX(C, MASK) \
+  x = max(x, __builtin_amdgcn_update_dpp(kOut, x, C, MASK, 0xF, false))
+  MXG_DPP_MAX(0x111, 0xF);
+  MXG_DPP_MAX(0x112, 0xF);
+  MXG_DPP_MAX(0x114, 0xF);
+  MXG_DPP_MAX(0x118, 0xF);
+  MXG_DPP_MAX(0x142, 0xA);
+  MXG_DPP_MAX(0x143, 0xC);
+#undef MXG_DPP_MAX
+  return __builtin_amdgcn_readlane(x, 63);
+}
+
+// exp(x) to 1.5 |x| 2^-24 + 2^-22 relative.
+__device__ __forceinline__ float exp_near(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
+}
+
+// A lane's two largest keys and their places; of equals the lower place first.
+struct Two {
+  int b1 = kOut, b2 = kOut, a1 = 0, a2 = 0;
+
+  __device__ __forceinline__ void add(int k, int place) {
+    const bool first = k > b1, second = k > b2;
+    b2 = first ? b1 : (second ? k : b2);
+    a2 = first ? a1 : (second ? place : a2);
+    b1 = first ? k : b1;
+    a1 = first ? place : a1;
+  }
+  // The two largest of this and another lane's (places are not kept).
+  __device__ __forceinline__ void merge(int o1, int o2) {
+    b2 = max(max(b2, o2), min(b1, o1));
+    b1 = max(b1, o1);
+  }
+};
+
+template <int C>
+__device__ __forceinline__ int dpp(int x) {
+  return __builtin_amdgcn_update_dpp(x, x, C, 0xF, 0xF, false);
+}
+
+// The two largest of the 2^log lanes around, in each of them.
+__device__ __forceinline__ Two around(Two t, int log) {
+  if (log > 0) t.merge(dpp<0xB1>(t.b1), dpp<0xB1>(t.b2));    // lane ^ 1
+  if (log > 1) t.merge(dpp<0x4E>(t.b1), dpp<0x4E>(t.b2));    // lane ^ 2
+  if (log > 2) t.merge(dpp<0x141>(t.b1), dpp<0x141>(t.b2));  // the other quad of 8
+  if (log > 3) t.merge(dpp<0x140>(t.b1), dpp<0x140>(t.b2));  // the other 8 of 16
+  for (int o = 16; o < 1 << log; o <<= 1)
+    t.merge(__shfl_xor(t.b1, o, 64), __shfl_xor(t.b2, o, 64));
+  return t;
+}
+
+// Lane j gets the expert of place j in *id; false: FP64 has to decide.
+template <int V>
+__device__ __forceinline__ bool choose(const RouteArgs& a, const Row<V>& row, int* cs, int lane,
+                                       int* id) {
+  const int E = a.r.experts, G = a.r.groups, per = E / G;
+  const bool softmax = a.r.score == MXG_ROUTE_SOFTMAX;
+  const bool by_logit = !a.bias && (G == 1 || a.r.group_best == 1 || per == 1);
+  int k[V];  // the choices' keys
+  Two two;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float c = row.l[i];
+    if (!by_logit) {
+      c = softmax ? exp_near(c - row.top) * row.inv
+                  : __builtin_amdgcn_rcpf(1.f + exp_near(-c));
+      if (a.bias) c += a.bias[V * lane + i < E ? V * lane + i : 0];
+    }
+    // (Negative zero becomes zero. A NaN bias: out.)
+    k[i] = row.l[i] > -INFINITY && c > -INFINITY ? key_of(c + 0.f) : kOut;
+    two.add(k[i], i);
+  }
+  if (G > 1 && a.r.top_groups < G) {
+    // The 2^log lanes of a group hold its experts (aligned), or else scan its
+    // choices in LDS; their two largest make its score.
+    const int log = a.group_log, g = lane >> log, sub = lane & ((1 << log) - 1);
+    Two best = two;
+    if (!a.aligned) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (V * lane + i < E) cs[V * lane + i] = k[i];
+      __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
+      best = Two();
+      if (g < G)
+        for (int q = sub; q < per; q += 1 << log) best.merge(cs[g * per + q], kOut);
+    }
+    best = around(best, log);
+    float score = best.b1 == kOut ? -INFINITY : of_key(best.b1);
+    if (a.r.group_best == 2 && best.b2 != kOut) score += of_key(best.b2);
+    // Lane sub of a group compares it with groups sub, sub + 2^log, ...
+    const uint64_t mine = (log == 6 ? ~0ull : (1ull << (1 << log)) - 1) << (g << log);
+    int ahead = 0;  // groups before this one
+    bool close = false;
+    for (int h0 = 0; h0 < G; h0 += 1 << log) {
+      const int h = h0 + sub;
+      const float o = __shfl(score, (h < G ? h : 0) << log, 64);
+      const bool other = h < G && h != g;
+      ahead += __popcll(__ballot(other && (o > score || (o == score && h < g))) & mine);
+      if (!by_logit) {
+        const float big = fmaxf(fabsf(o), fabsf(score));
+        close |= other && g < G && o > -INFINITY && score > -INFINITY &&
+                 !(fabsf(o - score) > 2 * kTol * (1.f + big));
+      }
+    }
+    if (__any(close)) return false;
+    if (a.aligned) {
+      const bool out = ahead >= a.r.top_groups;
+#pragma unroll
+      for (int i = 0; i < V; ++i) k[i] = out ? kOut : k[i];
+      two.b1 = out ? kOut : two.b1;
+      two.b2 = out ? kOut : two.b2;
+    } else {
+      const uint64_t kept = __ballot(ahead < a.r.top_groups);
+      two = Two();
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int of = (int)(((uint32_t)(V * lane + i) * a.per_inv) >> 20);  // its group
+        if (!((kept >> (of << log)) & 1)) k[i] = kOut;
+        two.add(k[i], i);
       }
     }
   }
+  // Rounds of the largest: the lowest lane that has it gives up its first. A
+  // lane that has given both looks again at all it holds (seldom).
+  int out = -1, key = kOut, n = 0;
+  uint64_t gave = 0;  // lanes whose first of two is gone
+  const int rounds = by_logit ? a.r.top_k : a.r.top_k + 1;
+  for (; n < rounds; ++n) {
+    const int m = wave_max(two.b1);
+    if (m == kOut) break;  // nothing left
+    const uint64_t has = __ballot(two.b1 == m);
+    const int who = __ffsll((unsigned long long)has) - 1;
+    const int place = __builtin_amdgcn_readlane(two.a1, who);
+    out = lane == n ? V * who + place : out;
+    key = lane == n ? m : key;
+    if (lane == who) {
+      two.b1 = two.b2;
+      two.a1 = two.a2;
+      two.b2 = kOut;
+    }
+    if constexpr (V > 2) {
+      if ((gave >> who) & 1) {
+        if (lane == who) {
+          two = Two();
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            two.add(k[i] < m || (k[i] == m && i > place) ? k[i] : kOut, i);
+        }
+        gave &= ~(1ull << who);
+      } else {
+        gave |= 1ull << who;
+      }
+    }
+  }
+  if (!by_logit) {  // neighbours in the order lie apart (one round more than top_k)
+    const float c = of_key(key), before = __shfl_up(c, 1, 64);
+    if (__any(lane > 0 && lane < n && !(before - c > kTol * (1.f + fabsf(c))))) return false;
+  }
+  *id = lane < a.r.top_k ? out : -1;
+  return true;
+}
+
+template <int V, bool BF16>
+__global__ void __launch_bounds__(64 * kWaves) route_kernel(RouteArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int t = blockIdx.x * kWaves + wave;
+  if (t >= a.tokens) return;  // whole waves; no barrier below
+  const int E = a.r.experts;
+  const bool softmax = a.r.score == MXG_ROUTE_SOFTMAX;
+
+  Row<V> row;
+  using Raw = std::conditional_t<BF16, uint16_t, uint32_t>;
+  const Raw* src = reinterpret_cast<const Raw*>(a.logits) + (int64_t)t * a.row_stride;
+  Raw raw[V];
+  struct alignas(sizeof(Raw) * V) Wide { Raw v[V]; };
+  if (E % V == 0 && (reinterpret_cast<uintptr_t>(src) & (sizeof(Wide) - 1)) == 0) {
+    if (V * lane < E) *reinterpret_cast<Wide*>(raw) = reinterpret_cast<const Wide*>(src)[lane];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (V * lane + i < E) raw[i] = src[V * lane + i];
+  }
+  float hi = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float v = -INFINITY;
+    if (V * lane + i < E) v = __uint_as_float(BF16 ? (uint32_t)raw[i] << 16 : (uint32_t)raw[i]);
+    row.l[i] = v > -INFINITY ? v : -INFINITY;  // NaN: out
+    hi = fmaxf(hi, row.l[i]);
+  }
+  row.top = 0.f;
+  row.inv = 0.f;
+  if (softmax) {
+    row.top = hi = of_key(wave_max(key_of(hi)));
+    float sum = 0.f;
+    if (hi > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += soft_term<float>(row.l[i], hi);
+    }
+    sum = wave_sum(sum);
+    row.inv = sum > 0.f ? 1.f / sum : 0.f;
+  }
+
+  // FP32 first; FP64 for rows with choices too close to each other, or with
+  // scores that are one, or zero, in FP64.
+  uint8_t* const cs = lds + sizeof(double) * (size_t)wave * E;
+  bool odd = softmax ? hi == INFINITY : hi > kNearOne;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    odd |= row.l[i] > -INFINITY && row.l[i] < (softmax ? hi : 0.f) - 700.f;
+  int id = -1;
+  if (__any(odd) || !choose<V>(a, row, reinterpret_cast<int*>(cs), lane, &id))
+    id = choose_wide<V>(a, row, reinterpret_cast<double*>(cs), lane);
+  float logit = -INFINITY;
+  if (id >= 0) logit = BF16 ? __uint_as_float((uint32_t)src[id] << 16) : __uint_as_float(src[id]);
+
   float w = 0.f;
-  if (id >= 0) w = softmax ? soft_term<float>(logit, top) * inv : 1.f / (1.f + expf(-logit));
+  if (id >= 0) w = softmax ? soft_term<float>(logit, row.top) * row.inv : 1.f / (1.f + expf(-logit));
   if (a.r.renormalize) {
     const float sum = wave_sum(w);
     w = sum > 0.f ? w / sum : 0.f;
   }
   if (lane < a.r.top_k) {
-    const int64_t at = (int64_t)row * a.r.top_k + lane;
+    const int64_t at = (int64_t)t * a.r.top_k + lane;
     a.ids[at] = id;
     a.weights[at] = id >= 0 ? w * a.r.scale : 0.f;
   }
@@ -259,7 +468,19 @@ void launch(const RouteArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs& a, int logits_type, hipStream_t s) {
+hipError_t launch_route(const RouteArgs& args, int logits_type, hipStream_t s) {
+  RouteArgs a = args;
+  const int per = a.r.experts / a.r.groups;
+  a.per_inv = ((1u << 20) + per - 1) / per;  // exact for e < 1024, per <= 1024
+  a.group_log = 6;
+  while ((a.r.groups << a.group_log) > 64) --a.group_log;
+  // Where a group fills 2^i whole lanes, these are its lanes.
+  int v = 1;
+  while (64 * v < a.r.experts) v *= 2;
+  const int lanes = per / v;
+  a.aligned = per % v == 0 && (lanes & (lanes - 1)) == 0;
+  if (a.aligned)
+    for (a.group_log = 0; 1 << a.group_log < lanes;) ++a.group_log;
   if (logits_type == MXG_BF16)
     launch<true>(a, s);
   else

@@ -73,15 +73,19 @@ struct Plan {
   int order[N];
 };
 
-__device__ __forceinline__ int wave_prefix(int v, int lane) {  // exclusive
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(x, o, 64);
-    if (lane >= o) x += y;
-  }
-  return x - v;
+// The sum of v over this lane and the ones below.
+__device__ __forceinline__ int wave_scan(int v) {
+#define MXG_DPP_ADD(C, MASK) v += __builtin_amdgcn_update_dpp(0, v, C, MASK, 0xF, true)
+  MXG_DPP_ADD(0x111, 0xF);  // rows of 16, then across them
+  MXG_DPP_ADD(0x112, 0xF);
+  MXG_DPP_ADD(0x114, 0xF);
+  MXG_DPP_ADD(0x118, 0xF);
+  MXG_DPP_ADD(0x142, 0xA);
+  MXG_DPP_ADD(0x143, 0xC);
+#undef MXG_DPP_ADD
+  return v;
 }
+__device__ __forceinline__ int wave_prefix(int v) { return wave_scan(v) - v; }
 
 // Up to 64 pairs: one per lane, without a barrier. Every wave computes the
 // whole plan and writes the same words, so each may read it after its own
@@ -101,8 +105,8 @@ __device__ __forceinline__ int make_plan(Plan<kNarrowPairs>& p, const int32_t* i
   }
   const bool first = e >= 0 && lead == lane;
   const int ch = (all + RC - 1) / RC;
-  const int s = wave_prefix(first ? 1 : 0, lane);
-  const int no = wave_prefix(first ? all : 0, lane), co = wave_prefix(first ? ch : 0, lane);
+  const int s = wave_prefix(first ? 1 : 0);
+  const int no = wave_prefix(first ? all : 0), co = wave_prefix(first ? ch : 0);
   if (first) {
     p.expert[s] = e;
     p.off[s] = no;
@@ -127,76 +131,114 @@ __device__ __forceinline__ int piece_k(int q, int grp) {
 
 // Sorts the pairs and copies the rows of x into column tiles of 16:
 // xp[tile][K block][q][grp][column] in 16-byte pieces. Every workgroup sorts
-// for itself; the first one writes the plan out. rc0, rc1: rows per chunk.
-__global__ void __launch_bounds__(kThreads) sort_kernel(ExpertArgs a, int rc0, int rc1) {
-  __shared__ int cnt[MXG_MOE_MAX_EXPERTS], at[MXG_MOE_MAX_EXPERTS];
+// for itself; the first one writes the plan out. 2^log0, 2^log1: rows per chunk.
+// 2^share threads compare a pair with all others (in LDS, four at a time), with
+// more than 512 pairs each thread does so for two; experts come in the order of
+// their first pair, an expert's pairs in ascending order.
+template <int kPer>
+__global__ void __launch_bounds__(kThreads) sort_kernel(ExpertArgs a, int log0, int log1,
+                                                        int share) {
+  __shared__ __attribute__((aligned(16))) int sid[MXG_MOE_MAX_PAIRS];
+  __shared__ int lead_off[MXG_MOE_MAX_PAIRS];   // of a first pair: its expert's place
+  __shared__ int slot_of[MXG_MOE_MAX_PAIRS];    // of a column tile of 16
+  __shared__ int totals[kPer][kWaves][3];
   __shared__ WidePlan p;
-  const int tid = threadIdx.x;
-  const int pairs = a.tokens * a.top_k, experts = a.experts;
-  for (int e = tid; e < experts; e += kThreads) cnt[e] = 0;
-  __syncthreads();
-  for (int i = tid; i < pairs; i += kThreads) {
-    const int e = a.ids[i];
-    if ((unsigned)e < (unsigned)experts) atomicAdd(&cnt[e], 1);
-  }
-  __syncthreads();
-  if (tid < 64) {
-    const int epl = (experts + 63) >> 6;
-    const int lo = tid * epl, hi = min(lo + epl, experts);
-    int v[6] = {};  // pairs, active experts, chunks, column tiles
-    auto add = [&](int c) __attribute__((always_inline)) {
-      v[0] += c;
-      v[1] += c > 0 ? 1 : 0;
-      v[2] += (c + rc0 - 1) / rc0;
-      v[3] += (c + rc1 - 1) / rc1;
-      v[4] += (c + 15) / 16;
-      v[5] += (c + 7) / 8;
-    };
-    for (int e = lo; e < hi; ++e) add(cnt[e]);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int pairs = a.tokens * a.top_k;
+  const int padded = (pairs + 3) & ~3;
+  const int part = tid & ((1 << share) - 1);
+  int pair[kPer], e[kPer], below[kPer], all[kPer], lead[kPer], v[kPer][6];
 #pragma unroll
-    for (int i = 0; i < 6; ++i) v[i] = wave_prefix(v[i], tid);
-    auto put = [&]() __attribute__((always_inline)) {
-      p.off[v[1]] = v[0];
-      p.first[0][v[1]] = v[2];
-      p.first[1][v[1]] = v[3];
-      p.tile[0][v[1]] = v[4];
-      p.tile[1][v[1]] = v[5];
-    };
-    for (int e = lo; e < hi; ++e) {
-      const int c = cnt[e];
-      if (c == 0) continue;
-      at[e] = v[0];
-      p.expert[v[1]] = e;
-      put();
-      add(c);
-    }
-    if (tid == 63) {
-      p.slots = v[1];
-      put();
-    }
-    // 64 pairs at a time: a pair's place is its expert's next free one plus the
-    // lower lanes of the same expert; the last of them moves the free place on.
-    __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
-    for (int i0 = 0; i0 < pairs; i0 += 64) {
-      const int i = i0 + tid;
-      int e = i < pairs ? a.ids[i] : -1;
-      if ((unsigned)e >= (unsigned)experts) e = -1;
-      const int here = pairs - i0 < 64 ? pairs - i0 : 64;
-      int below = 0, all = 0;
-      for (int j = 0; j < here; ++j) {
-        const int same = __builtin_amdgcn_readlane(e, j) == e ? 1 : 0;
-        all += same;
-        below += j < tid ? same : 0;
-      }
-      if (e >= 0) {
-        const int to = at[e];
-        p.order[to + below] = i;
-        if (below == all - 1) at[e] = to + all;
+  for (int r = 0; r < kPer; ++r) {
+    pair[r] = r * kThreads + (tid >> share);
+    e[r] = pair[r] < pairs ? a.ids[pair[r]] : -1;
+    if ((unsigned)e[r] >= (unsigned)a.experts) e[r] = -1;
+    if (part == 0 && pair[r] < padded) sid[pair[r]] = e[r];
+    below[r] = all[r] = 0;
+    lead[r] = MXG_MOE_MAX_PAIRS;
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int j = 4 * part; j < padded; j += 4 << share) {
+    const int4 o = *reinterpret_cast<const int4*>(sid + j);
+    const int ov[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bool same = ov[q] == e[r];
+        all[r] += same ? 1 : 0;
+        below[r] += same && j + q < pair[r] ? 1 : 0;
+        lead[r] = same ? min(lead[r], j + q) : lead[r];
       }
     }
   }
+  for (int o = 1; o < 1 << share; o <<= 1) {  // (share > 0 only with one pair per thread)
+    all[0] += __shfl_xor(all[0], o, 64);
+    below[0] += __shfl_xor(below[0], o, 64);
+    lead[0] = min(lead[0], __shfl_xor(lead[0], o, 64));
+  }
+  // Places of the experts: prefix sums over the first pairs, two sums in a word
+  // (each at most 1024).
+  int own[kPer][3];
+#pragma unroll
+  for (int r = 0; r < kPer; ++r) {
+    const int c = e[r] >= 0 && below[r] == 0 && part == 0 ? all[r] : 0;
+    own[r][0] = c | (c > 0 ? 1 : 0) << 16;
+    own[r][1] = (c + (1 << log0) - 1) >> log0 | ((c + (1 << log1) - 1) >> log1) << 16;
+    own[r][2] = (c + 15) >> 4 | ((c + 7) >> 3) << 16;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int to = wave_scan(own[r][k]);
+      if (lane == 63) totals[r][wave][k] = to;
+      v[r][2 * k] = to - own[r][k];  // for now both sums
+    }
+  }
   __syncthreads();
-  const int slots = p.slots;
+  int sum[3] = {};  // over all pairs
+#pragma unroll
+  for (int r = 0; r < kPer; ++r)
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        if (w == wave) v[r][2 * k] += sum[k];
+        sum[k] += totals[r][w][k];
+      }
+  int end[6];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    end[2 * k] = sum[k] & 0xFFFF;
+    end[2 * k + 1] = sum[k] >> 16;
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      v[r][2 * k + 1] = v[r][2 * k] >> 16;
+      v[r][2 * k] &= 0xFFFF;
+    }
+  }
+  auto put = [&](const int (&u)[6]) __attribute__((always_inline)) {
+    p.off[u[1]] = u[0];
+    p.first[0][u[1]] = u[2];
+    p.first[1][u[1]] = u[3];
+    p.tile[0][u[1]] = u[4];
+    p.tile[1][u[1]] = u[5];
+  };
+#pragma unroll
+  for (int r = 0; r < kPer; ++r) {
+    if (e[r] < 0 || below[r] != 0 || part != 0) continue;
+    lead_off[pair[r]] = v[r][0];
+    p.expert[v[r][1]] = e[r];
+    put(v[r]);
+    for (int t = 0; t < (all[r] + 15) >> 4; ++t) slot_of[v[r][4] + t] = v[r][1];
+  }
+  const int slots = end[1];
+  if (tid == 0) put(end);
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kPer; ++r)
+    if (e[r] >= 0 && part == 0) p.order[lead_off[lead[r]] + below[r]] = pair[r];
+  __syncthreads();
   if (blockIdx.x == 0) {
     WidePlan& g = *a.plan;
     if (tid == 0) g.slots = slots;
@@ -208,22 +250,20 @@ __global__ void __launch_bounds__(kThreads) sort_kernel(ExpertArgs a, int rc0, i
       g.tile[0][i] = p.tile[0][i];
       g.tile[1][i] = p.tile[1][i];
     }
-    for (int i = tid; i < p.off[slots]; i += kThreads) g.order[i] = p.order[i];
+    for (int i = tid; i < end[0]; i += kThreads) g.order[i] = p.order[i];
   }
-  // One wave per (tile, 4 K blocks' quarter): lane = (grp, column).
+  // One wave per (tile, quarter of a K block): lane = (grp, column).
   const int K = a.hidden, pieces = K >> 5;  // 1 KiB pieces per tile
-  const int lane = tid & 63, col = lane & 15, grp = lane >> 4;
-  const int64_t units = (int64_t)p.tile[0][slots] * pieces;
-  const int waves = gridDim.x * kWaves;
-  int s = 0;
-  for (int64_t u = blockIdx.x * kWaves + (tid >> 6); u < units; u += waves) {
-    const int t = (int)(u / pieces), q = (int)(u - (int64_t)t * pieces);
-    while (p.tile[0][s + 1] <= t) ++s;  // tiles come in ascending order
+  const int col = lane & 15, grp = lane >> 4;
+  const int units = end[4] * pieces;
+  for (int u = blockIdx.x * kWaves + wave; u < units; u += gridDim.x * kWaves) {
+    const int t = u / pieces, q = u - t * pieces;
+    const int s = slot_of[t];
     const int pos = p.off[s] + 16 * (t - p.tile[0][s]) + col;
     if (pos >= p.off[s + 1]) continue;
     const int row = p.order[pos] / a.top_k;
     const int k = (q >> 2) * 128 + piece_k(q & 3, grp);
-    a.xp[u * 64 + lane] = *reinterpret_cast<const uint4*>(a.x + (size_t)row * K + k);
+    a.xp[(size_t)u * 64 + lane] = *reinterpret_cast<const uint4*>(a.x + (size_t)row * K + k);
   }
 }
 
@@ -615,8 +655,16 @@ hipError_t launch_experts(const ExpertArgs& a, hipStream_t s) {
     launch_product<false, false, 1>(a, cus, s);
   } else {
     const int nc0 = rows <= 16 ? 1 : 2, nc1 = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    hipLaunchKernelGGL(sort_kernel, dim3((unsigned)(pairs < 64 ? pairs : 64)), dim3(kThreads), 0,
-                       s, a, 16 * nc0, 8 * nc1);
+    const size_t units = most_tiles(pairs, a.experts, 16) * (a.hidden >> 5);
+    const size_t groups = (units + kWaves - 1) / kWaves;
+    const dim3 grid((unsigned)(groups < 256 ? groups : 256)), block(kThreads);
+    const int log0 = nc0 == 1 ? 4 : 5, log1 = nc1 == 1 ? 3 : nc1 == 2 ? 4 : 5;
+    int share = 0;
+    while (share < 4 && pairs << (share + 1) <= kThreads) ++share;
+    if (pairs <= kThreads)
+      hipLaunchKernelGGL((sort_kernel<1>), grid, block, 0, s, a, log0, log1, share);
+    else
+      hipLaunchKernelGGL((sort_kernel<2>), grid, block, 0, s, a, log0, log1, 0);
     if (nc0 == 1)
       launch_product<true, true, 1>(a, cus, s);
     else

@@ -209,18 +209,21 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
         raise ValueError(f"score: {score!r} instead of one of {sorted(_SCORES)}")
     dev = logits.device
     handle = _on(dev, stream)
-    out = (tokens, top_k)
-    if ids is None and top_k > 0:
-        ids = torch.empty(out, dtype=torch.int32, device=dev)
-    if weights is None and top_k > 0:
-        weights = torch.empty(out, dtype=torch.float32, device=dev)
+    out = (tokens, top_k if top_k > 0 else 0)
+    if ids is None:
+        ids = logits.new_empty(out, dtype=torch.int32)
+    else:
+        _address(ids, "ids", torch.int32, out, dev)
+    if weights is None:
+        weights = logits.new_empty(out, dtype=torch.float32)
+    else:
+        _address(weights, "weights", torch.float32, out, dev)
     router = mx.mxmoe_router(experts, top_k, _SCORES[score], groups, top_groups, group_best,
                              int(renormalize), scale)
     code = _lib.mxmoe_route(
         router, logits.data_ptr(), kind, row_stride,
         None if bias is None else _address(bias, "bias", torch.float32, (experts,), dev), tokens,
-        _address(ids, "ids", torch.int32, out, dev),
-        _address(weights, "weights", torch.float32, out, dev), handle)
+        ids.data_ptr(), weights.data_ptr(), handle)
     if code:
         mx._check(code, "mxmoe_route")
     return ids, weights
@@ -272,12 +275,14 @@ class Experts:
         rows = (chosen[0], self.hidden)
         px = _address(x, "x", torch.bfloat16, rows, dev)
         if out is None:
-            out = torch.empty_like(x)
+            out = x.new_empty(rows)
+        else:
+            _address(out, "out", torch.bfloat16, rows, dev)
         code = _lib.mxmoe_experts(
             px, _address(ids, "ids", torch.int32, chosen, dev),
             _address(weights, "weights", torch.float32, chosen, dev), *self._weights, chosen[0],
             chosen[1], self.experts, self.hidden, self.inter, self.workspace.data_ptr(),
-            self.nbytes, _address(out, "out", torch.bfloat16, rows, dev), handle)
+            self.nbytes, out.data_ptr(), handle)
         if code:
             mx._check(code, "mxmoe_experts")
         return out

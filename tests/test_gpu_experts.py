@@ -178,3 +178,54 @@ def test_refusals(dv):
             layer.layer(*bad)
     with pytest.raises(ValueError):
         dv.Experts(*(torch.from_numpy(v).cuda() for v in layer.host), 1025)
+
+
+@pytest.mark.parametrize("tokens,top_k,experts,hidden,inter", [
+    (40, 1, 1, 256, 384), (33, 2, 2, 1152, 1024), (65, 1, 3, 128, 2048), (9, 8, 8, 512, 128),
+    (256, 4, 1000, 128, 128), (24, 3, 3, 2048, 1152), (512, 2, 16, 128, 256),
+])
+def test_many_rows(dv, tokens, top_k, experts, hidden, inter):
+    """Rows copied into column tiles: chunks that end inside a tile, experts of
+    one row among full ones, both halves of the pairs."""
+    layer = Layer(dv, 77 + tokens, experts, hidden, inter)
+    x, ids, w = layer.inputs(tokens + experts, tokens, top_k)
+    layer.check(x, ids, w)
+    ids[::3, 0] = 0  # one crowded expert, twice in some rows
+    ids[1] = -1
+    got = layer.check(x, ids, w)
+    assert (got[1] == 0).all()
+    none = layer.run(x, np.full_like(ids, experts), w)
+    assert (none == 0).all()
+
+
+def test_one_row_set_through_both_paths(dv):
+    """A row's result does not depend on the rows beside it: the first 8 of 64
+    rows, alone (gathered) and among the others (in column tiles)."""
+    layer = Layer(dv, 78, 6, 640, 384)
+    x, ids, w = layer.inputs(5, 64, 2)
+    many = layer.run(x, ids, w).clone()
+    assert torch.equal(layer.run(x[:8].copy(), ids[:8].copy(), w[:8].copy()), many[:8])
+
+
+def test_captured(dv):
+    """Replays of both paths with new inputs, eager calls between."""
+    for tokens in (3, 48):
+        layer = Layer(dv, 79, 5, 512, 256, 96)
+        other = Layer(dv, 79, 5, 512, 256, 96)
+        ins = [layer.inputs(s, tokens, 2) for s in range(5)]
+        x = torch.empty(tokens, 512, dtype=torch.bfloat16, device="cuda")
+        ids = torch.zeros(tokens, 2, dtype=torch.int32, device="cuda")
+        w = torch.zeros(tokens, 2, device="cuda")
+        out = torch.empty_like(x)
+        layer.layer(x.zero_(), ids, w, out=out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            layer.layer(x, ids, w, out=out)
+        for bits, i, wt in ins:
+            x.copy_(torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16))
+            ids.copy_(torch.from_numpy(i))
+            w.copy_(torch.from_numpy(wt))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, other.run(bits, i, wt))

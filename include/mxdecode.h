@@ -63,7 +63,8 @@ typedef struct mxmoe_router {
  * bits.
  *
  * An expert whose logit is -infinity or NaN is out: it is never chosen and
- * adds nothing to the softmax or to its group. Where fewer than top_k
+ * adds nothing to the softmax or to its group. A bias of -infinity or NaN
+ * keeps its expert from being chosen. Where fewer than top_k
  * experts are left, the rest of the row is id -1 with weight 0, which
  * mxmoe_experts passes over. A sum of weights of zero leaves them zero. With
  * softmax, logits of +infinity share the row's weight.
@@ -114,8 +115,9 @@ size_t mxmoe_workspace_bytes(int32_t tokens, int32_t top_k, int32_t experts, int
  * inter], and silu(v) = v / (1 + exp(-v)). An id outside 0..experts-1 adds
  * nothing; a row without any expert comes out as zeros. A row may name an
  * expert more than once. Products accumulate in FP32, h is held as the sum of
- * two BF16 values (about 17 bits), the sum over j runs in FP32 in ascending
- * order, and the result is rounded once to BF16. A weight is the BF16 value
+ * two BF16 values (about 17 bits; beyond BF16's range it is infinite), the sum
+ * over j runs in FP32 in ascending order, and the result is rounded once to
+ * BF16. A weight is the BF16 value
  * nearest to its code times its scale: exact for scale bytes 3..246 (255 is the
  * E8M0 NaN and not taken). Results are the same bits on every call.
  *
@@ -186,8 +188,11 @@ int mxgemm_lora_scratch_init(void* scratch, size_t scratch_bytes, void* stream);
  *            MXG_ERR_SPLITK_SPIN in the scratch's ERROR word (MXG_WS_ERROR):
  *            later calls are right but slow until it is armed again
  *   c_out    device [m, n] BF16 as rounded; may be NULL with mb
- * Other arguments as mxgemm_publish. Errors: its errors, MXG_EINVAL for a bad
- * adapter argument, MXG_EWORKSPACE for a missing or small scratch. */
+ * Other arguments as mxgemm_publish. With split_k > 1 the workgroups of a call
+ * wait for each other, as there: two such calls must not run at once on one
+ * device. Errors: its errors (MXG_EUNSUPPORTED also where the x slice leaves no
+ * LDS for u), MXG_EINVAL for a bad adapter argument, MXG_EWORKSPACE for a missing
+ * or small scratch. */
 int mxgemm_lora(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scale,
                 const uint8_t* x, const uint8_t* x_scale, const uint16_t* x_bf16, int32_t m,
                 int32_t n, int32_t k, int32_t split_k, void* workspace, size_t workspace_bytes,

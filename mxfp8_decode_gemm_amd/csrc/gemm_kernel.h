@@ -422,6 +422,15 @@ __device__ __forceinline__ float wave_sum63(float x) {
   return x;
 }
 
+// The workgroup's barrier for LDS alone: this wave's LDS accesses are done and
+// no access moves across it, while its global loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // The side wave of an adapter launch, from the kernel's start to its end: it
 // shares the workers' barriers, and with split-K does the control wave's work
 // too. It is one function of its own, called once, so that its loads may be in
@@ -521,13 +530,11 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
         // The workers' first barrier (x staged; the list and the hand-off words
         // are in LDS), with the loads above in flight.
         before_barrier = false;
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        lds_barrier();
         if constexpr (X16) {  // the exact path's second stage has its own
           uint32_t rflags = 0;
           for (int w = 0; w < NW; ++w) rflags |= hdr[kHdrFlags + w];
-          if (rflags) __builtin_amdgcn_s_barrier();
+          if (rflags) lds_barrier();
         }
       }
       const bool one = q < total && per - piece >= kPieces;  // all of one task
@@ -573,7 +580,15 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
       uint32_t polls = 0;
       bool pending = true;
       while (pending && polls++ < kLoraPolls) {
-        if (polls > 1) __builtin_amdgcn_s_sleep(1);
+        // The first look comes about 0.9 us after this workgroup's own stores: one
+        // that comes too early costs a round trip behind the W stream. Without
+        // the wait N=7168/K=8192/m=8/S=4 rank 16 took 15.4 us instead of 14.0,
+        // N=7168/K=2048/m=4 rank 64 10.4 instead of 9.0, N=4096/K=16384/m=5/S=8
+        // rank 32 16.1 instead of 14.4; 48 was 0.5 us slower on the second.
+        if (polls > 1)
+          __builtin_amdgcn_s_sleep(1);
+        else
+          __builtin_amdgcn_s_sleep(32);
         pending = false;
 #pragma unroll
         for (int j = 0; j < B; ++j) {
@@ -609,9 +624,8 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
       uh[m * rank + at] = __builtin_bit_cast(uint16_t, lo);
     }
   }
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();        // the workers' K loops are done, u is there
-  __builtin_amdgcn_s_barrier();        // the partial tiles are in LDS
+  lds_barrier();  // the workers' K loops are done, u is there
+  lds_barrier();  // the partial tiles are in LDS
   if (blockIdx.x != 0) return;
   // Workgroup 0: the next epochs once every workgroup has read this call's
   // (its flag words hold it), and the generation handed to the consumer.

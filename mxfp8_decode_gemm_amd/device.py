@@ -185,6 +185,13 @@ def _on(device: torch.device, stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _keep(t: torch.Tensor, stream) -> None:
+    """Keeps a fresh output's memory until a call on a stream other than the
+    one it was allocated on has ended."""
+    if stream is not None and not isinstance(stream, int):
+        t.record_stream(stream)
+
+
 _SCORES = {"softmax": mx.ROUTE_SOFTMAX, "sigmoid": mx.ROUTE_SIGMOID}
 _LOGITS = {torch.float32: mx.F32, torch.bfloat16: mx.BF16}
 _lib = mx.library()
@@ -212,10 +219,12 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
     out = (tokens, top_k if top_k > 0 else 0)
     if ids is None:
         ids = logits.new_empty(out, dtype=torch.int32)
+        _keep(ids, stream)
     else:
         _address(ids, "ids", torch.int32, out, dev)
     if weights is None:
         weights = logits.new_empty(out, dtype=torch.float32)
+        _keep(weights, stream)
     else:
         _address(weights, "weights", torch.float32, out, dev)
     router = mx.mxmoe_router(experts, top_k, _SCORES[score], groups, top_groups, group_best,
@@ -276,6 +285,7 @@ class Experts:
         px = _address(x, "x", torch.bfloat16, rows, dev)
         if out is None:
             out = x.new_empty(rows)
+            _keep(out, stream)
         else:
             _address(out, "out", torch.bfloat16, rows, dev)
         code = _lib.mxmoe_experts(
@@ -332,9 +342,13 @@ class AdaptedLinear:
                     _address(x_scale, "x_scale", torch.uint8, (m, self.k // 32), dev), None)
         # (Read by the library within the call.)
         self.lora.ids = _address(ids, "ids", torch.int32, (m,), dev)
-        if mb is None and c_out is None:
-            c_out = torch.empty(m, self.n, dtype=torch.bfloat16, device=dev)
-        pc = None if c_out is None else _address(c_out, "c_out", torch.bfloat16, (m, self.n), dev)
+        pc = None
+        if c_out is not None:
+            pc = _address(c_out, "c_out", torch.bfloat16, (m, self.n), dev)
+        elif mb is None:
+            c_out = x.new_empty((m, self.n), dtype=torch.bfloat16)
+            _keep(c_out, stream)
+            pc = c_out.data_ptr()
         code = _lib.mxgemm_lora(mb, *self._weights, *form, m, self.n, self.k, self.split_k,
                                 *self._memory, self.lora, self.scratch.data_ptr(),
                                 self.scratch_bytes, pc, handle)

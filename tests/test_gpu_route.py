@@ -146,3 +146,44 @@ def test_refusals(dv):
         dv.route(x.double(), 4)
     with pytest.raises(ValueError):
         dv.route(x.t(), 4)
+
+
+def test_odd_biases(dv):
+    """Biases of infinity and NaN, and large ones, whose FP32 sums lose the score."""
+    x = _logits(31, 6, 96)
+    bias = _bias(5, 96)
+    bias[3], bias[4], bias[50] = float("-inf"), float("nan"), float("inf")
+    for score in ("softmax", "sigmoid"):
+        ids, _ = dv.route(x, 8, score=score, bias=bias, groups=3, top_groups=2, group_best=2)
+        ids = ids.cpu()
+        assert (ids[:, 0] == 50).all() and not torch.isin(ids, torch.tensor([3, 4])).any()
+    _check(dv, x, 8, 1e6 + 0.25 * torch.arange(96, device="cuda") % 3, score="sigmoid")
+
+
+def test_on_a_given_stream(dv):
+    """Another stream than the current one, outputs of its own."""
+    x = _logits(41, 64, 256)
+    want = dv.route(x, 8)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = dv.route(x, 8, stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_captured(dv):
+    """Replays with other logits, eager calls between."""
+    x, ids, w = _logits(51, 17, 72), *(torch.empty(17, 6, dtype=t, device="cuda")
+                                       for t in (torch.int32, torch.float32))
+    kw = dict(score="sigmoid", bias=_bias(7, 72), groups=9, top_groups=4, group_best=2)
+    dv.route(x, 6, ids=ids, weights=w, **kw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dv.route(x, 6, ids=ids, weights=w, **kw)
+    for seed in range(4):
+        x.copy_(_logits(60 + seed, 17, 72))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = dv.route(x, 6, **kw)
+        assert torch.equal(ids, want[0]) and torch.equal(w, want[1])

@@ -74,17 +74,11 @@ size_t mxmoe_packed_scale_bytes(int32_t experts, int32_t n, int32_t k) {
 int mxmoe_pack_weight(const uint8_t* w, const uint8_t* w_scale, int32_t experts, int32_t n,
                       int32_t k, uint8_t* w_packed, uint8_t* ws_packed, void* stream) {
   if (!w || !w_scale || !w_packed || !ws_packed) return MXG_EINVAL;
-  const size_t wb = mxgemm_packed_weight_bytes(n, k), sb = mxgemm_packed_scale_bytes(n, k);
   if (mxmoe_packed_weight_bytes(experts, n, k) == 0) return MXG_EINVAL;
   if (!aligned16(w) || !aligned16(w_scale) || !aligned16(w_packed) || !aligned16(ws_packed))
     return MXG_EALIGN;
-  for (int32_t e = 0; e < experts; ++e) {
-    const hipError_t err = launch_pack_weight(
-        w + (size_t)e * n * k, w_scale + (size_t)e * n * (k / 32), n, k, w_packed + e * wb,
-        ws_packed + e * sb, static_cast<hipStream_t>(stream));
-    if (err != hipSuccess) return MXG_EHIP;
-  }
-  return MXG_OK;
+  return hip_code(launch_pack_weight(w, w_scale, n, k, w_packed, ws_packed,
+                                     static_cast<hipStream_t>(stream), experts));
 }
 
 size_t mxmoe_workspace_bytes(int32_t tokens, int32_t top_k, int32_t experts, int32_t hidden,

@@ -22,9 +22,14 @@ namespace {
 //             rb*16 + l%16, K = kb*128 + 64*h + 16*(l/16) .. +16
 //   ws_packed + ((rb*K/128 + kb)*16 + r)*4            : the 4 scale bytes of
 //             row rb*16 + r for that K block (byte 127 past n)
-// One thread per 16-byte chunk; every index is checked against the sizes.
+// One thread per 16-byte chunk; every index is checked against the sizes. Grid
+// row y packs the y-th of a stack of such matrices.
 __global__ void pack_weight_kernel(const uint8_t* w, const uint8_t* ws, int n, int k,
-                                   uint8_t* wp, uint8_t* wsp) {
+                                   uint8_t* wp, uint8_t* wsp, size_t wp_bytes, size_t wsp_bytes) {
+  w += (size_t)blockIdx.y * n * k;
+  ws += (size_t)blockIdx.y * n * (k >> 5);
+  wp += blockIdx.y * wp_bytes;
+  wsp += blockIdx.y * wsp_bytes;
   const int kbt = k >> 7;
   const int rbn = (n + 15) >> 4;
   const size_t chunks = (size_t)rbn * kbt * 128;
@@ -59,8 +64,11 @@ __global__ void pack_weight_kernel(const uint8_t* w, const uint8_t* ws, int n, i
 // tile, lane l's 16-byte pieces at 16 l and 1024 + 16 l hold row l % 16 and K
 // 16 (l / 16) .. +16 and 64 + 16 (l / 16) .. +16, so lanes l and l ^ 16 hold
 // the two halves of the 32-wide blocks l / 32 and 2 + l / 32 of row l % 16.
-__global__ void scale_summary_kernel(const uint8_t* wp, const uint8_t* wsp, int rbn, int kbt,
-                                     uint32_t* summary) {
+__global__ void scale_summary_kernel(const uint8_t* wp, uint8_t* wsp, int rbn, int kbt,
+                                     size_t wp_bytes, size_t wsp_bytes) {
+  wp += blockIdx.y * wp_bytes;
+  wsp += blockIdx.y * wsp_bytes;
+  uint32_t* summary = reinterpret_cast<uint32_t*>(wsp + (size_t)rbn * kbt * 64);
   const int rb = blockIdx.x * (blockDim.x >> 6) + (int)(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (rb >= rbn) return;  // whole waves
@@ -306,16 +314,17 @@ long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool 
 }
 
 hipError_t launch_pack_weight(const uint8_t* w, const uint8_t* ws, int n, int k, uint8_t* wp,
-                              uint8_t* wsp, hipStream_t s) {
+                              uint8_t* wsp, hipStream_t s, int count) {
+  const size_t wpb = mxgemm_packed_weight_bytes(n, k), wspb = mxgemm_packed_scale_bytes(n, k);
   const size_t chunks = (size_t)((n + 15) / 16) * (k / 128) * 128;
   const size_t blocks = std::min<size_t>((chunks + 255) / 256, 65536);
-  hipLaunchKernelGGL(pack_weight_kernel, dim3((unsigned)blocks), dim3(256), 0, s, w, ws, n, k,
-                     wp, wsp);
+  hipLaunchKernelGGL(pack_weight_kernel, dim3((unsigned)blocks, (unsigned)count), dim3(256), 0, s,
+                     w, ws, n, k, wp, wsp, wpb, wspb);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int rbn = (n + 15) / 16, kbt = k / 128;
-  hipLaunchKernelGGL(scale_summary_kernel, dim3((unsigned)((rbn + 3) / 4)), dim3(256), 0, s, wp,
-                     wsp, rbn, kbt, reinterpret_cast<uint32_t*>(wsp + (size_t)rbn * kbt * 64));
+  hipLaunchKernelGGL(scale_summary_kernel, dim3((unsigned)((rbn + 3) / 4), (unsigned)count),
+                     dim3(256), 0, s, wp, wsp, rbn, kbt, wpb, wspb);
   return hipGetLastError();
 }
 

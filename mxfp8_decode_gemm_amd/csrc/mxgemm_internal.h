@@ -103,9 +103,10 @@ long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool 
 hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t s,
                                hipEvent_t ev_start = nullptr, hipEvent_t ev_stop = nullptr);
 
-// Packs row-major W and scales into the GEMM's tile layout.
+// Packs row-major W and scales, or a stack of count of them, into the GEMM's
+// tile layout.
 hipError_t launch_pack_weight(const uint8_t* w, const uint8_t* ws, int n, int k, uint8_t* wp,
-                              uint8_t* wsp, hipStream_t s);
+                              uint8_t* wsp, hipStream_t s, int count = 1);
 
 // Stand-alone activation quantizer: [rows, k] BF16 -> codes and scales.
 hipError_t launch_quantize(const uint16_t* x, int rows, int k, uint8_t* xq, uint8_t* xs,

@@ -229,3 +229,16 @@ def test_captured(dv):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, other.run(bits, i, wt))
+
+
+def test_pack_is_the_projections_layout(dv):
+    """Every expert's packed weight is mxgemm_pack_weight's of its matrix."""
+    rng = np.random.default_rng(3)
+    q, s = _quantized(rng, 5, 48, 384)
+    w, ws = dv.pack_experts(torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda())
+    one = [dv.pack_weight(torch.from_numpy(q[e]).cuda(), torch.from_numpy(s[e]).cuda(), 48, 384)
+           for e in range(5)]
+    assert torch.equal(w, torch.cat([a for a, _ in one]))
+    for e, (_, b) in enumerate(one):  # (the bytes that round the range words up are not written)
+        used = 48 * 12 + 12
+        assert torch.equal(ws.view(5, -1)[e, :used], b[:used])

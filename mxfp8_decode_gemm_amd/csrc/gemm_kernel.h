@@ -375,7 +375,10 @@ __device__ __attribute__((noinline)) bool stage_rest(const uint8_t* x, const uin
 //   * u = scale A x is small (m * rank values) but reads A whole, so its dot
 //     products, cut into `parts` along K, are spread over the workgroups: the
 //     side wave of each computes its share while the workers stream W, and
-//     stores every partial as a (value, epoch) pair, as split-K does.
+//     stores every partial as a (value, epoch) pair, as split-K does. A small N
+//     has few workgroups: up to one more per CU then joins them, all of whose
+//     waves compute u and nothing else (N=64/K=16384/m=8 rank 64 699 -> 32 us,
+//     N=1024/K=4096/m=8 rank 128 36 -> 16 us, no difference from 256 tiles on).
 //   * Each side wave then collects all pairs, sums the parts in ascending K
 //     order and leaves u in LDS as high and low BF16 parts (hi = bf16(u), lo =
 //     bf16(u - hi), together 17 bits).
@@ -439,7 +442,7 @@ __device__ __forceinline__ void lds_barrier() {
 // to instruction fetches).
 template <int SK, bool QX, bool X16, int NW>
 __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint8_t* lw,
-                                                    int lane) {
+                                          int wave, int lane) {
   const LoraArgs& l = a.lora;
   const int m = a.m, rank = l.rank, K = a.k;
   int* const list = reinterpret_cast<int*>(lw);
@@ -451,7 +454,9 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
   uint32_t lepoch = ld_agent_u32(l.hdr + MXG_WS_EPOCH);
   const uint32_t lerr = ld_agent_u32(l.hdr + MXG_WS_ERROR);
   uint32_t gen = 0, epoch = 0;
-  if (SK > 1 && lane == 0) {
+  // A helping workgroup: all its waves compute tasks, and none else.
+  const bool helps = (int)blockIdx.x >= l.groups;
+  if (SK > 1 && lane == 0 && !helps) {
     if (a.state) gen = ld_agent_u32(a.state + MXG_STATE_NEXT) % MXG_GENERATIONS;
     epoch = ld_agent_u32(a.ws_hdr + MXG_WS_EPOCH) + a.epoch_bias;
     hdr[2] = ld_agent_u32(a.ws_hdr + MXG_WS_ERROR);
@@ -460,7 +465,9 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
     st_agent_u32(a.flags + blockIdx.x, epoch);  // (the epoch has been read)
   }
   lepoch = __builtin_amdgcn_readfirstlane(lepoch);
-  if (lane == 0) st_agent_u32(l.flags + blockIdx.x, lepoch);
+  if (helps) lds_barrier();  // every wave of it has read the epoch
+  if (lane == 0 && (!helps || wave == 0)) st_agent_u32(l.flags + blockIdx.x, lepoch);
+  if (helps && lerr != 0) return;
   // ---- the distinct adapters and the rows that have one -------------------
   if (lane >= m || (unsigned)lid >= (unsigned)l.adapters) lid = -1;
   float scale = 0.f;  // lane t: of row t's adapter
@@ -473,14 +480,14 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
     rows |= (uint64_t)t << (4 * nrows++);
     const uint64_t same = __ballot(lid == i);
     if ((int)__ffsll((unsigned long long)same) - 1 == t) {
-      if (lane == 0) {
+      if (lane == 0 && !helps) {
         list[1 + nd] = i;
         list[9 + nd] = (int)same;
       }
       ++nd;
     }
   }
-  if (lane == 0) list[0] = nd;
+  if (lane == 0 && !helps) list[0] = nd;
 
   // ---- u's dot products --------------------------------------------------
   // Task q: the partial (row, rank, part), part fastest, in 512-value pieces.
@@ -493,9 +500,13 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
   const int per = (len + 511) >> 9;
   const uint32_t rinv = ((1u << 20) + rank - 1) / rank;  // item / rank for items < 1024
   constexpr int kPieces = 8;  // in flight
-  bool before_barrier = true;
+  bool before_barrier = !helps;
   for (int pass = lerr != 0 || l.workers == 0 ? 1 : 0; pass < 2; ++pass) {
-    const int first = pass == 0 ? (int)blockIdx.x : 0, step = pass == 0 ? l.workers : 1;
+    const int first =
+        pass != 0 ? 0
+                  : helps ? l.groups + ((int)blockIdx.x - l.groups) * (NW + 1) + wave
+                          : (int)blockIdx.x;
+    const int step = pass == 0 ? l.workers : 1;
     int q = first < (pass == 0 ? step : 1) ? first : total, piece = 0;
     float sum = 0.f;
     while (before_barrier || q < total) {
@@ -537,7 +548,9 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
           if (rflags) lds_barrier();
         }
       }
-      const bool one = q < total && per - piece >= kPieces;  // all of one task
+      // All of one task; a helping wave, which has no LDS of its own and hardly
+      // more than one task, leaves the pieces behind it out.
+      const bool one = q < total && (helps || per - piece >= kPieces);
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         float d;
@@ -552,7 +565,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
         else
           stage[64 * j + lane] = d;
       }
-      if (one) piece += kPieces - 1;
+      if (one) piece = (piece + kPieces < per ? piece + kPieces : per) - 1;
       __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
 #pragma unroll 1
       for (int j = one ? kPieces - 1 : 0; j < kPieces && q < total; ++j) {
@@ -571,6 +584,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
         }
       }
     }
+    if (helps) return;
     if (pass == 1) break;
     // All pairs, eight loads per lane in flight.
     constexpr int B = 8;
@@ -636,7 +650,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
     pending = false;
     for (int i = lane; i < (int)gridDim.x; i += 64) {
       pending |= ld_agent_u32(l.flags + i) != lepoch;
-      if (SK > 1) pending |= ld_agent_u32(a.flags + i) != epoch;
+      if (SK > 1 && i < l.groups) pending |= ld_agent_u32(a.flags + i) != epoch;
     }
     pending = __any(pending);
     if (pending) __builtin_amdgcn_s_sleep(2);
@@ -723,8 +737,8 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 || LORA ? 1 : 0)))
   uint8_t* const lw = lds + (LORA ? a.lora.lds_off : 0);
   const int* const llist = reinterpret_cast<const int*>(lw);
   if constexpr (LORA) {
-    if (ctl) {
-      lora_side<SK, QX, X16, NT / 64>(a, hdr, lw, lane);
+    if (ctl || (int)blockIdx.x >= a.lora.groups) {
+      lora_side<SK, QX, X16, NT / 64>(a, hdr, lw, wave, lane);
       return;
     }
   }

@@ -334,24 +334,36 @@ hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t 
   if (!v) return hipErrorInvalidValue;
   const int tiles = (a.n + tile_rows(c) - 1) / tile_rows(c);
   const bool lora = a.lora.b != nullptr;
-  const dim3 grid(tiles * a.split_k), block(tile_threads(c, a.split_k, lora));
+  dim3 grid(tiles * a.split_k);
+  const dim3 block(tile_threads(c, a.split_k, lora));
   size_t lds = gemm_lds_bytes(c, a.m, a.k / a.split_k);
   GemmArgs args = a;
   if (lora) {
     args.lora.lds_off = (int32_t)((lds + 15) / 16 * 16);
     lds += lora_lds_bytes(a.m, a.lora.rank);
-    // u's dot products over at most 512 workgroups.
-    args.lora.workers = grid.x < 512 ? (int32_t)grid.x : 512;
+    // u's dot products: one wave of each workgroup of the GEMM, of at most 512,
+    // and where these are few, workgroups that only help (up to one per CU: a
+    // small N leaves the rest of the device idle). They come last in the grid.
+    constexpr int kFull = 256;
+    const int groups = (int)grid.x, waves = (int)block.x / 64;
+    const int most = groups < kFull ? groups + (kFull - groups) * waves : groups;
     const int items = a.m * a.lora.rank;
     int ps = 0;
+    args.lora.groups = groups;
     if (items * ((a.k + 511) / 512) <= 16) {
       args.lora.workers = 0;  // a few loads: no exchange
     } else {
       // A task's 8 pieces of 512 values are one round trip; beyond that, cut it
-      // while there are workgroups left over.
+      // while there are waves left over.
       while (ps < 2 && a.k >> (ps + 1) >= 512 && (items << (ps + 1)) <= kLoraMaxPairs &&
-             (a.k >> ps > 8 * 512 || (items << (ps + 1)) <= args.lora.workers))
+             (a.k >> ps > 8 * 512 || (items << (ps + 1)) <= (groups < 512 ? groups : 512)))
         ++ps;
+      const int tasks = items << ps;
+      int helping = 0;
+      if (tasks > groups && most > groups)
+        helping = ((tasks < most ? tasks : most) - groups + waves - 1) / waves;
+      args.lora.workers = groups < 512 ? groups + helping * waves : 512;
+      grid.x += helping;
     }
     args.lora.parts_log2 = ps;
   }

@@ -22,9 +22,10 @@ struct LoraArgs {
   uint32_t* flags;        // scratch: one epoch word per workgroup
   uint64_t* pairs;        // scratch: (value, epoch) of every partial of u
   // Set by the launcher: the K parts a value of u is summed from (1 << this),
-  // the workgroups that compute them (0: each computes all of u for itself),
-  // and where the kernel's LDS area starts.
-  int32_t parts_log2, workers, lds_off;
+  // the waves that compute them (0: each workgroup computes all of u for
+  // itself), where the kernel's LDS area starts, and the workgroups of the
+  // GEMM itself: those from there on only help with u.
+  int32_t parts_log2, workers, lds_off, groups;
 };
 
 // Most (value, epoch) pairs of one call's u: rows * rank * parts.

@@ -80,6 +80,9 @@ class Case:
     (8, 1000, 1024, 2, 128, 5), (8, 520, 2048, 4, 32, 9), (5, 2056, 1024, 8, 64, 3),
     (4, 7168, 2048, 1, 64, 2), (7, 904, 1920, 1, 40, 4), (8, 64, 16384, 8, 16, 2),
     (6, 136, 6400, 1, 120, 6), (8, 4096, 4096, 4, 8, 8),
+    # few workgroups, many dot products: others help
+    (8, 8, 16384, 1, 128, 3), (8, 64, 4096, 8, 128, 8), (7, 2048, 1024, 1, 128, 2),
+    (8, 1024, 2176, 1, 72, 5),
 ])
 def test_adapted(env, m, n, k, split_k, rank, adapters):
     c = Case(env[1], m, n, k, split_k, rank, adapters)
@@ -189,8 +192,8 @@ def test_marked_scratch(env):
     """A scratch with its error word set (as a wait that gave up leaves it): the
     same bits, every workgroup on its own."""
     mx, dv = env
-    for split_k in (1, 4):
-        c = Case(dv, 3, 520, 1024, split_k, 24, 2, seed=9)
+    for split_k, rank in ((1, 24), (4, 24), (1, 128), (4, 128)):
+        c = Case(dv, 3, 520, 1024, split_k, rank, 2, seed=9)
         x, ids = c._bf(c.xb), torch.tensor([1, -1, 0], dtype=torch.int32, device="cuda")
         want = c.lin(x, ids).clone()
         c.lin.scratch[mx.WS_ERROR] = mx.ERR_SPLITK_SPIN

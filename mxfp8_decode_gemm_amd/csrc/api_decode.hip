@@ -174,8 +174,10 @@ int mxgemm_lora(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scale,
   l.adapters = lora->adapters;
   l.rank = lora->rank;
   l.hdr = static_cast<uint32_t*>(scratch);
-  l.flags = reinterpret_cast<uint32_t*>(s + MXG_WS_HEADER_BYTES);
-  l.pairs = reinterpret_cast<uint64_t*>(s + MXG_WS_HEADER_BYTES + lora_flag_bytes(n));
+  // The pairs lie at one place for every n: a word that one call uses for a value
+  // must not be another's flag.
+  l.pairs = reinterpret_cast<uint64_t*>(s + MXG_WS_HEADER_BYTES);
+  l.flags = reinterpret_cast<uint32_t*>(s + MXG_WS_HEADER_BYTES + kLoraMaxPairs * sizeof(uint64_t));
   return gemm_call(mb, w, w_scale, x, x_scale, x_bf16, m, n, k, split_k, workspace,
                    workspace_bytes, 0, c_out, nullptr, nullptr, stream, nullptr, nullptr, nullptr,
                    &l);

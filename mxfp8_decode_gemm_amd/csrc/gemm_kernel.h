@@ -439,8 +439,9 @@ __device__ __forceinline__ void lds_barrier() {
 // too. It is one function of its own, called once, so that its loads may be in
 // flight across one without the workers' code waiting for them. Its code runs cold
 // on every CU and is kept short (a first version, unrolled further, lost 2-3 us
-// to instruction fetches).
-template <int SK, bool QX, bool X16, int NW>
+// to instruction fetches). HELPS: a workgroup that only helps, all of whose waves
+// compute tasks and nothing else; ALONE: the launch has none of these.
+template <int SK, bool QX, bool X16, int NW, bool HELPS, bool ALONE>
 __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint8_t* lw,
                                           int wave, int lane) {
   const LoraArgs& l = a.lora;
@@ -454,9 +455,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
   uint32_t lepoch = ld_agent_u32(l.hdr + MXG_WS_EPOCH);
   const uint32_t lerr = ld_agent_u32(l.hdr + MXG_WS_ERROR);
   uint32_t gen = 0, epoch = 0;
-  // A helping workgroup: all its waves compute tasks, and none else.
-  const bool helps = (int)blockIdx.x >= l.groups;
-  if (SK > 1 && lane == 0 && !helps) {
+  if (SK > 1 && lane == 0 && !HELPS) {
     if (a.state) gen = ld_agent_u32(a.state + MXG_STATE_NEXT) % MXG_GENERATIONS;
     epoch = ld_agent_u32(a.ws_hdr + MXG_WS_EPOCH) + a.epoch_bias;
     hdr[2] = ld_agent_u32(a.ws_hdr + MXG_WS_ERROR);
@@ -465,9 +464,9 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
     st_agent_u32(a.flags + blockIdx.x, epoch);  // (the epoch has been read)
   }
   lepoch = __builtin_amdgcn_readfirstlane(lepoch);
-  if (helps) lds_barrier();  // every wave of it has read the epoch
-  if (lane == 0 && (!helps || wave == 0)) st_agent_u32(l.flags + blockIdx.x, lepoch);
-  if (helps && lerr != 0) return;
+  if (HELPS) lds_barrier();  // every wave of it has read the epoch
+  if (lane == 0 && (!HELPS || wave == 0)) st_agent_u32(l.flags + blockIdx.x, lepoch);
+  if (HELPS && lerr != 0) return;
   // ---- the distinct adapters and the rows that have one -------------------
   if (lane >= m || (unsigned)lid >= (unsigned)l.adapters) lid = -1;
   float scale = 0.f;  // lane t: of row t's adapter
@@ -480,14 +479,14 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
     rows |= (uint64_t)t << (4 * nrows++);
     const uint64_t same = __ballot(lid == i);
     if ((int)__ffsll((unsigned long long)same) - 1 == t) {
-      if (lane == 0 && !helps) {
+      if (lane == 0 && !HELPS) {
         list[1 + nd] = i;
         list[9 + nd] = (int)same;
       }
       ++nd;
     }
   }
-  if (lane == 0 && !helps) list[0] = nd;
+  if (lane == 0 && !HELPS) list[0] = nd;
 
   // ---- u's dot products --------------------------------------------------
   // Task q: the partial (row, rank, part), part fastest, in 512-value pieces.
@@ -500,11 +499,11 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
   const int per = (len + 511) >> 9;
   const uint32_t rinv = ((1u << 20) + rank - 1) / rank;  // item / rank for items < 1024
   constexpr int kPieces = 8;  // in flight
-  bool before_barrier = !helps;
+  bool before_barrier = !HELPS;
   for (int pass = lerr != 0 || l.workers == 0 ? 1 : 0; pass < 2; ++pass) {
     const int first =
         pass != 0 ? 0
-                  : helps ? l.groups + ((int)blockIdx.x - l.groups) * (NW + 1) + wave
+                  : HELPS ? l.groups + ((int)blockIdx.x - l.groups) * (NW + 1) + wave
                           : (int)blockIdx.x;
     const int step = pass == 0 ? l.workers : 1;
     int q = first < (pass == 0 ? step : 1) ? first : total, piece = 0;
@@ -550,7 +549,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
       }
       // All of one task; a helping wave, which has no LDS of its own and hardly
       // more than one task, leaves the pieces behind it out.
-      const bool one = q < total && (helps || per - piece >= kPieces);
+      const bool one = q < total && (HELPS || per - piece >= kPieces);
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         float d;
@@ -565,7 +564,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
         else
           stage[64 * j + lane] = d;
       }
-      if (one) piece = (piece + kPieces < per ? piece + kPieces : per) - 1;
+      if (one) piece = HELPS && piece + kPieces > per ? per - 1 : piece + kPieces - 1;
       __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
 #pragma unroll 1
       for (int j = one ? kPieces - 1 : 0; j < kPieces && q < total; ++j) {
@@ -584,7 +583,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
         }
       }
     }
-    if (helps) return;
+    if (HELPS) return;
     if (pass == 1) break;
     // All pairs, eight loads per lane in flight.
     constexpr int B = 8;
@@ -643,6 +642,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
   if (blockIdx.x != 0) return;
   // Workgroup 0: the next epochs once every workgroup has read this call's
   // (its flag words hold it), and the generation handed to the consumer.
+  const int groups = ALONE ? (int)gridDim.x : l.groups;
   uint32_t polls = 0;
   bool pending = true;
   epoch = __builtin_amdgcn_readfirstlane(epoch);
@@ -650,7 +650,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
     pending = false;
     for (int i = lane; i < (int)gridDim.x; i += 64) {
       pending |= ld_agent_u32(l.flags + i) != lepoch;
-      if (SK > 1 && i < l.groups) pending |= ld_agent_u32(a.flags + i) != epoch;
+      if (SK > 1 && i < groups) pending |= ld_agent_u32(a.flags + i) != epoch;
     }
     pending = __any(pending);
     if (pending) __builtin_amdgcn_s_sleep(2);
@@ -683,10 +683,12 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
 // X16: the staged slice holds exact BF16 values (XStage::dest16 layout), not
 // FP8 codes and scale bytes, and the main loop reads the B operand as is.
 // LORA: each row's adapter is added before the rounding (a.lora); the side
-// wave computes its A x.
+// wave computes its A x. 2: in a grid with helping workgroups. They are an
+// instance of their own: with both in one, those without any lost 0.9-1.8 us
+// under split-K (N=4096/K=16384/m=5/S=8 rank 32 14.2 -> 16.0 us).
 // Without a mailbox (a.state null) the kernel is a plain GEMM into c_out.
 template <int RB, int WN, int WK, int D, int SK, bool QX, int XR = 1, bool X16 = false,
-          bool LORA = false>
+          int LORA = 0>
 __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 || LORA ? 1 : 0)))
     __attribute__((amdgpu_waves_per_eu(2))) gemm_publish_kernel(GemmArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -737,8 +739,14 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 || LORA ? 1 : 0)))
   uint8_t* const lw = lds + (LORA ? a.lora.lds_off : 0);
   const int* const llist = reinterpret_cast<const int*>(lw);
   if constexpr (LORA) {
-    if (ctl || (int)blockIdx.x >= a.lora.groups) {
-      lora_side<SK, QX, X16, NT / 64>(a, hdr, lw, wave, lane);
+    if constexpr (LORA == 2) {
+      if ((int)blockIdx.x >= a.lora.groups) {
+        lora_side<SK, QX, X16, NT / 64, true, false>(a, hdr, lw, wave, lane);
+        return;
+      }
+    }
+    if (ctl) {
+      lora_side<SK, QX, X16, NT / 64, false, LORA == 1>(a, hdr, lw, wave, lane);
       return;
     }
   }
@@ -1366,18 +1374,23 @@ struct Variant {
   const void* fn_q;    // BF16 x, quantized in the activation stage
   const void* fn16;    // MXFP8 x, staged as BF16 (null: not built)
   const void* fn16_q;  // BF16 x, quantized and staged as BF16 (null: not built)
-  const void* lora[4]; // the same four with the adapter epilogue
+  const void* lora[8]; // the same four with the adapter epilogue, then with helping workgroups too
 };
 
 #define MXG_FN(RB, WN, WK, D, SK, QX, XR, X16) \
   reinterpret_cast<const void*>(&gemm_publish_kernel<RB, WN, WK, D, SK, QX, XR, X16>)
-#define MXG_FNL(RB, WN, WK, D, SK, QX, XR, X16) \
-  reinterpret_cast<const void*>(&gemm_publish_kernel<RB, WN, WK, D, SK, QX, XR, X16, true>)
+#define MXG_FNL(RB, WN, WK, D, SK, QX, XR, X16, L) \
+  reinterpret_cast<const void*>(&gemm_publish_kernel<RB, WN, WK, D, SK, QX, XR, X16, L>)
+#define MXG_LORA2(RB, WN, WK, D, SK, XR, L)                                          \
+  MXG_FNL(RB, WN, WK, D, SK, false, XR, false, L), MXG_FNL(RB, WN, WK, D, SK, true, 1, false, L)
+#define MXG_LORA4(RB, WN, WK, D, SK, L)                                              \
+  MXG_LORA2(RB, WN, WK, D, SK, 1, L), MXG_FNL(RB, WN, WK, D, SK, false, 1, true, L), \
+      MXG_FNL(RB, WN, WK, D, SK, true, 1, true, L)
 #define MXG_V(RB, WN, WK, D, SK)                                                     \
   Variant{TileCfg{RB, WN, WK, D}, SK, MXG_FN(RB, WN, WK, D, SK, false, 1, false),    \
           MXG_FN(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr,               \
-          {MXG_FNL(RB, WN, WK, D, SK, false, 1, false),                              \
-           MXG_FNL(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr}}
+          {MXG_LORA2(RB, WN, WK, D, SK, 1, 1), nullptr, nullptr,                     \
+           MXG_LORA2(RB, WN, WK, D, SK, 1, 2), nullptr, nullptr}}
 // Sixteen worker waves leave no room for the adapters' side wave.
 #define MXG_V_16WAVES(RB, WN, WK, D, SK, XR)                                         \
   Variant{TileCfg{RB, WN, WK, D, XR}, SK, MXG_FN(RB, WN, WK, D, SK, false, XR, false), \
@@ -1388,10 +1401,7 @@ struct Variant {
   Variant{TileCfg{RB, WN, WK, D}, SK, MXG_FN(RB, WN, WK, D, SK, false, 1, false),    \
           MXG_FN(RB, WN, WK, D, SK, true, 1, false),                                 \
           MXG_FN(RB, WN, WK, D, SK, false, 1, true), MXG_FN(RB, WN, WK, D, SK, true, 1, true), \
-          {MXG_FNL(RB, WN, WK, D, SK, false, 1, false),                              \
-           MXG_FNL(RB, WN, WK, D, SK, true, 1, false),                               \
-           MXG_FNL(RB, WN, WK, D, SK, false, 1, true),                               \
-           MXG_FNL(RB, WN, WK, D, SK, true, 1, true)}}
+          {MXG_LORA4(RB, WN, WK, D, SK, 1), MXG_LORA4(RB, WN, WK, D, SK, 2)}}
 // The x stage with an 8-chunk first round (xr = 2: a slice of twice the
 // size staged before the first barrier without a second, out-of-line round);
 // BF16 x stages through XQuant either way.
@@ -1400,8 +1410,8 @@ struct Variant {
 #define MXG_V2(RB, WN, WK, D, SK)                                                    \
   Variant{TileCfg{RB, WN, WK, D, 2}, SK, MXG_FN(RB, WN, WK, D, SK, false, 2, false), \
           MXG_FN(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr,               \
-          {MXG_FNL(RB, WN, WK, D, SK, false, 2, false),                              \
-           MXG_FNL(RB, WN, WK, D, SK, true, 1, false), nullptr, nullptr}}
+          {MXG_LORA2(RB, WN, WK, D, SK, 2, 1), nullptr, nullptr,                     \
+           MXG_LORA2(RB, WN, WK, D, SK, 2, 2), nullptr, nullptr}}
 #define MXG_VARIANT(RB, WN, WK, D) \
   MXG_V(RB, WN, WK, D, 1), MXG_V(RB, WN, WK, D, 2), MXG_V(RB, WN, WK, D, 4), \
       MXG_V(RB, WN, WK, D, 8)

@@ -103,8 +103,8 @@ __global__ void scale_summary_kernel(const uint8_t* wp, uint8_t* wsp, int rbn, i
   if (lane == 0) summary[rb] = lo | (hi << 8);
 }
 
-const void* variant_fn(const Variant& v, bool bf16_x, bool x16, bool lora) {
-  if (lora) return v.lora[2 * (x16 ? 1 : 0) + (bf16_x ? 1 : 0)];
+const void* variant_fn(const Variant& v, bool bf16_x, bool x16, bool lora, bool helped = false) {
+  if (lora) return v.lora[4 * (helped ? 1 : 0) + 2 * (x16 ? 1 : 0) + (bf16_x ? 1 : 0)];
   return x16 ? (bf16_x ? v.fn16_q : v.fn16) : (bf16_x ? v.fn_q : v.fn);
 }
 
@@ -334,6 +334,7 @@ hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t 
   if (!v) return hipErrorInvalidValue;
   const int tiles = (a.n + tile_rows(c) - 1) / tile_rows(c);
   const bool lora = a.lora.b != nullptr;
+  bool helped = false;
   dim3 grid(tiles * a.split_k);
   const dim3 block(tile_threads(c, a.split_k, lora));
   size_t lds = gemm_lds_bytes(c, a.m, a.k / a.split_k);
@@ -364,11 +365,12 @@ hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t 
         helping = ((tasks < most ? tasks : most) - groups + waves - 1) / waves;
       args.lora.workers = groups < 512 ? groups + helping * waves : 512;
       grid.x += helping;
+      helped = helping > 0;
     }
     args.lora.parts_log2 = ps;
   }
   args.xcd_groups = a.split_k > 1 && tiles % 8 == 0 ? 1 : 0;
-  const void* fn = variant_fn(*v, a.xb != nullptr, c.x16, lora);
+  const void* fn = variant_fn(*v, a.xb != nullptr, c.x16, lora, helped);
   if (!fn) return hipErrorInvalidValue;
   if (lds > 64 * 1024) {
     const hipError_t e =

@@ -83,6 +83,8 @@ class Case:
     # few workgroups, many dot products: others help
     (8, 8, 16384, 1, 128, 3), (8, 64, 4096, 8, 128, 8), (7, 2048, 1024, 1, 128, 2),
     (8, 1024, 2176, 1, 72, 5),
+    # more workgroups than a split-K grid may have
+    (3, 40960, 512, 1, 16, 4), (8, 33000, 128, 1, 128, 8),
 ])
 def test_adapted(env, m, n, k, split_k, rank, adapters):
     c = Case(env[1], m, n, k, split_k, rank, adapters)

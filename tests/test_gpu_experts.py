@@ -83,6 +83,18 @@ def test_experts(dv, tokens, top_k, experts, hidden, inter):
     layer.check(*layer.inputs(tokens * 7 + top_k, tokens, top_k))
 
 
+@pytest.mark.parametrize("tokens,top_k,experts,hidden,inter", [
+    (1, 1024, 3, 128, 128), (1024, 1, 1024, 128, 128), (2, 3, 2, 32768, 128),
+    (2, 3, 2, 128, 32768), (40, 2, 3, 128, 32768), (40, 2, 3, 32768, 128),
+])
+def test_ends_of_the_ranges(dv, tokens, top_k, experts, hidden, inter):
+    layer = Layer(dv, 3 + tokens, experts, hidden, inter)
+    x, ids, w = layer.inputs(tokens + top_k, tokens, min(top_k, experts))
+    reps = -(-top_k // experts)  # more choices than experts: each one again
+    layer.check(x, np.tile(ids, (1, reps))[:, :top_k].copy(),
+                np.tile(w, (1, reps))[:, :top_k].copy())
+
+
 def test_large_widths(dv):
     layer = Layer(dv, 5, 3, 7168, 2048, 16)
     layer.check(*layer.inputs(6, 4, 2))

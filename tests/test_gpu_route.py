@@ -187,3 +187,15 @@ def test_captured(dv):
         torch.cuda.synchronize()
         want = dv.route(x, 6, **kw)
         assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
+
+
+def test_most_rows(dv):
+    """2^24 rows: the last ones, and a sample of the others."""
+    t = 1 << 24
+    logits = torch.randn(t, 2, device="cuda")
+    ids, weights = dv.route(logits, 1)
+    best = logits.argmax(1)
+    assert torch.equal(ids[:, 0].long(), best)
+    want = torch.softmax(logits.double(), 1).amax(1)
+    # (FP32: exp, sum and quotient, a few halves of 2^-23 each.)
+    assert ((weights[:, 0].double() - want).abs() <= 2.0 ** -20 * want).all()

@@ -168,70 +168,6 @@ def test_rows_behind(env):
     assert torch.equal(out[1:4], want) and (out[[0, 4]] == 3).all()
 
 
-def test_one_scratch_for_calls_of_all_sizes(env):
-    """The epoch keeps a call from taking an earlier one's pairs: other rows,
-    ids and values through one scratch, on two streams in order."""
-    mx, dv = env
-    c = Case(dv, 8, 1032, 1024, 4, 16, 3, seed=8)
-    side = torch.cuda.Stream()
-    x = c._bf(c.xb)
-    rng = np.random.default_rng(1)
-    for call in range(12):
-        m = int(rng.integers(1, 9))
-        ids = torch.from_numpy(rng.integers(-1, 3, m).astype(np.int32)).cuda()
-        rows = torch.from_numpy(rng.permutation(8)[:m]).cuda()
-        part = x[rows].contiguous()
-        torch.cuda.synchronize()
-        with torch.cuda.stream(side if call % 2 else torch.cuda.default_stream()):
-            got = c.lin(part, ids)
-        torch.cuda.synchronize()
-        fresh = dv.AdaptedLinear(torch.from_numpy(c.p.w).cuda(), torch.from_numpy(c.p.ws).cuda(),
-                                 c.lin.a, c.lin.b, c.lin.scale, 4)
-        assert torch.equal(got, fresh(part, ids))
-
-
-def test_one_scratch_for_projections_captured(env):
-    """Projections of other sizes (with helping workgroups, and more workgroups
-    than flag words of a small one) in one graph on one scratch: replays with
-    other activations, eager calls between, each against a scratch of its own."""
-    mx, dv = env
-    cases = [Case(dv, 8, 64, 4096, 1, 128, 4, seed=21), Case(dv, 8, 40960, 128, 1, 128, 4, seed=22),
-             Case(dv, 8, 1032, 1024, 4, 64, 4, seed=23)]
-    own = [(c.lin.scratch, c.lin.scratch_bytes) for c in cases]
-    ids = torch.tensor([3, 0, -1, 2, 0, 1, 1, 3], dtype=torch.int32, device="cuda")
-    xs = [c._bf(c.xb) for c in cases]
-    outs = [torch.empty(8, c.p.n, dtype=torch.bfloat16, device="cuda") for c in cases]
-
-    def share(shared):
-        for c, (scratch, nbytes) in zip(cases, own):
-            c.lin.scratch, c.lin.scratch_bytes = own[1] if shared else (scratch, nbytes)
-
-    def step():
-        for c, x, out in zip(cases, xs, outs):
-            c.lin(x, ids, c_out=out)
-
-    share(True)
-    step()
-    torch.cuda.synchronize()
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        step()
-    for replay in range(4):
-        for x in xs:
-            x.copy_(x.roll(1, 0) * (1 + replay))
-        ids.copy_(ids.roll(1))
-        graph.replay()
-        torch.cuda.synchronize()
-        got = [out.clone() for out in outs]
-        share(False)
-        step()
-        torch.cuda.synchronize()
-        share(True)
-        for a, b in zip(got, outs):
-            assert torch.equal(a, b)
-        step()  # eager, on the shared one
-
-
 def test_marked_scratch(env):
     """A scratch with its error word set (as a wait that gave up leaves it): the
     same bits, every workgroup on its own."""

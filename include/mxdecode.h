@@ -59,8 +59,9 @@ typedef struct mxmoe_router {
  *   - weights[t][j] = s[ids[t][j]], divided by their sum when renormalize is
  *     set, times scale: the bias counts for the choice only.
  * Choices and group scores are compared as 64-bit values (a score below
- * 2^-1022 is zero); equal ones go to the lowest index. Weights are held in 32
- * bits.
+ * 2^-1022 is zero); equal ones go to the lowest index, also those of different
+ * logits (sigmoids of neighbours from about 23 on, logits less than 2^-53
+ * apart). Weights are held in 32 bits.
  *
  * An expert whose logit is -infinity or NaN is out: it is never chosen and
  * adds nothing to the softmax or to its group. A bias of -infinity or NaN

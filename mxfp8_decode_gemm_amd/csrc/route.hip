@@ -7,13 +7,14 @@
 //   * group scores (with groups), the kept groups as one 64-bit lane mask;
 //   * top_k rounds of a wave-wide maximum of c, each taking the lowest index
 //     among equals, the chosen one struck out.
-// Choices are compared as FP64 would compare them: among thousands of rows, two
-// FP32 choices (a rounded sum of a rounded exponential) do fall on the wrong
-// side of each other. Where the choice has the order of the logits themselves
-// (no bias, and no sum of two in a group score) the FP32 logits decide;
-// otherwise FP32 choices do where all that matter lie further apart than
-// their error, and the row is done again in FP64 where not (one row in some
-// hundred). The weights are FP32.
+// Choices are compared as FP64 values: among thousands of rows, two FP32 choices
+// (a rounded sum of a rounded exponential) do fall on the wrong side of each
+// other. Where the choice has the order of the logits themselves (no bias, and
+// no sum of two in a group score) the FP32 logits decide, otherwise FP32
+// choices do; the row is done again in FP64 where two that matter lie too
+// close for that: logits whose FP64 scores may be equal, or choices within
+// their error (of 8 of 256 experts, grouped sigmoid with a bias, one row in 75).
+// The weights are FP32.
 
 #include <hip/hip_runtime.h>
 
@@ -86,22 +87,13 @@ __device__ __forceinline__ F soft_term(float l, float m) {
     return expf(l - m);
 }
 
-// Scores below FP64's normal range count as zero: those of logits this far
-// below the largest (softmax) or below zero (sigmoid).
-constexpr double kZeroBelow = -708.3964185322641;  // ln 2^-1022
+// Scores below FP64's normal range count as zero.
 constexpr double kLeast = 0x1p-1022;
-// From here on neighbouring logits can have the same FP64 sigmoid.
+// Rows with a logit above this are compared in FP64 at once: their largest
+// sigmoids are one but for less than 2^-43.
 constexpr float kNearOne = 30.f;
 
 __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
-
-// A value in the order of the sigmoids' FP64 values, equal where they are. The
-// scores above kNearOne differ by multiples of 2^-53 up to 2^-43, so
-// 30 + 2^46 times their difference from sigmoid(30) is exact.
-__device__ __forceinline__ double sigmoid_order(float l) {
-  if (l > kNearOne) return kNearOne + 0x1p46 * (sigmoid64(l) - sigmoid64(kNearOne));
-  return l > (float)kZeroBelow ? (double)l : kZeroBelow;
-}
 
 // What the lanes of a row's wave hold: lane l the experts V l .. V l + V - 1, so
 // that a row is read in wide loads and the lowest index of equals is the first
@@ -118,34 +110,24 @@ __device__ __forceinline__ int choose_wide(const RouteArgs& a, const Row<V>& row
                                                      double* cs, int lane) {
   const int E = a.r.experts, G = a.r.groups, per = E / G;
   const bool softmax = a.r.score == MXG_ROUTE_SOFTMAX;
-  const bool by_logit = !a.bias && (G == 1 || a.r.group_best == 1 || per == 1);
   double c[V];
-  double inv = 1.0;
-  if (softmax && !by_logit) {
-    double sum = 0.0;
+  double sum = 0.0;
+  if (softmax) {
     if (row.top > -INFINITY) {
 #pragma unroll
       for (int i = 0; i < V; ++i) sum += soft_term<double>(row.l[i], row.top);
     }
     sum = wave_sum(sum);
-    inv = sum > 0.0 ? 1.0 / sum : 0.0;
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const float l = row.l[i];
     double s = -INFINITY;
     if (l > -INFINITY) {
-      if (by_logit) {
-        if (softmax)  // (the difference is NaN where both are +infinity)
-          s = l == row.top ? 0.0 : fmax((double)l - (double)row.top, kZeroBelow);
-        else
-          s = sigmoid_order(l);
-      } else {
-        s = softmax ? soft_term<double>(l, row.top) * inv : sigmoid64(l);
-        if (s < kLeast) s = 0.0;
-        if (a.bias) s += (double)a.bias[V * lane + i];
-        if (!(s > -INFINITY)) s = -INFINITY;  // a NaN bias: out
-      }
+      s = softmax ? soft_term<double>(l, row.top) / sum : sigmoid64(l);
+      if (s < kLeast) s = 0.0;
+      if (a.bias) s += (double)a.bias[V * lane + i];
+      if (!(s > -INFINITY)) s = -INFINITY;  // a NaN bias: out
     }
     c[i] = s;
   }
@@ -198,7 +180,8 @@ __device__ __forceinline__ int choose_wide(const RouteArgs& a, const Row<V>& row
 }
 
 // ---- FP32 choices, where they decide ---------------------------------------
-// Either the logits themselves (exact), or choices with an error below
+// Either the logits themselves, given up where two different ones that matter
+// may have equal FP64 scores (may_tie), or choices with an error below
 // 2^-19 (1 + |c|), given up where two that matter lie closer than kTol:
 //   sigmoid: 1 / (1 + e), e = 2^(-l log2 e) to 1.5 |l| 2^-24 + 2^-22 relative,
 //   moves s by at most s (1 - s) of that, s (1 - s) |l| < 0.23; softmax: the
@@ -233,6 +216,19 @@ __device__ __forceinline__ int wave_max(int x) {
 // exp(x) to 1.5 |x| 2^-24 + 2^-22 relative.
 __device__ __forceinline__ float exp_near(float x) {
   return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
+}
+
+// Whether the FP64 scores of the logits hi >= lo can come out equal, or in the
+// other order. Equal logits are not meant: their scores are the same bits.
+//   softmax: of exp(l - top) / sum the argument, |l - top| <= 700, is rounded by
+//   2^-53 of itself, exp and quotient by 2^-51: 2^-43 relative. Scores
+//   whose logits differ by d differ by d, relative.
+//   sigmoid: exp, sum and reciprocal are off by 2^-51, relative; scores whose logits
+//   differ by d differ by at least d (1 - s(hi)) >= d exp(-max(hi, 0)) / 2. Above
+//   about 19, FP32 neighbours come under this bound.
+__device__ __forceinline__ bool may_tie(float hi, float lo, bool softmax) {
+  const float d = hi - lo;
+  return hi != lo && !(softmax ? d > 0x1p-40f : d * exp_near(-fmaxf(hi, 0.f)) > 0x1p-46f);
 }
 
 // A lane's two largest keys and their places; of equals the lower place first.
@@ -316,7 +312,10 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Row<V>& row, in
       const float o = __shfl(score, (h < G ? h : 0) << log, 64);
       const bool other = h < G && h != g;
       ahead += __popcll(__ballot(other && (o > score || (o == score && h < g))) & mine);
-      if (!by_logit) {
+      if (by_logit) {
+        close |= other && g < G && o > -INFINITY && score > -INFINITY &&
+                 may_tie(fmaxf(o, score), fminf(o, score), softmax);
+      } else {
         const float big = fmaxf(fabsf(o), fabsf(score));
         close |= other && g < G && o > -INFINITY && score > -INFINITY &&
                  !(fabsf(o - score) > 2 * kTol * (1.f + big));
@@ -344,7 +343,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Row<V>& row, in
   // lane that has given both looks again at all it holds (seldom).
   int out = -1, key = kOut, n = 0;
   uint64_t gave = 0;  // lanes whose first of two is gone
-  const int rounds = by_logit ? a.r.top_k : a.r.top_k + 1;
+  const int rounds = a.r.top_k + 1;  // one more: the largest that is not chosen
   for (; n < rounds; ++n) {
     const int m = wave_max(two.b1);
     if (m == kOut) break;  // nothing left
@@ -372,10 +371,11 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Row<V>& row, in
       }
     }
   }
-  if (!by_logit) {  // neighbours in the order lie apart (one round more than top_k)
-    const float c = of_key(key), before = __shfl_up(c, 1, 64);
-    if (__any(lane > 0 && lane < n && !(before - c > kTol * (1.f + fabsf(c))))) return false;
-  }
+  // Neighbours in the order lie apart.
+  const float c = of_key(key), before = __shfl_up(c, 1, 64);
+  const bool close = by_logit ? may_tie(before, c, softmax)
+                              : !(before - c > kTol * (1.f + fabsf(c)));
+  if (__any(lane > 0 && lane < n && close)) return false;
   *id = lane < a.r.top_k ? out : -1;
   return true;
 }
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(64 * kWaves) route_kernel(RouteArgs a) {
   }
 
   // FP32 first; FP64 for rows with choices too close to each other, or with
-  // scores that are one, or zero, in FP64.
+  // scores that are about one, or zero, in FP64.
   uint8_t* const cs = lds + sizeof(double) * (size_t)wave * E;
   bool odd = softmax ? hi == INFINITY : hi > kNearOne;
 #pragma unroll

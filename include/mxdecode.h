@@ -61,7 +61,8 @@ typedef struct mxmoe_router {
  * Choices and group scores are compared as 64-bit values (a score below
  * 2^-1022 is zero); equal ones go to the lowest index, also those of different
  * logits (sigmoids of neighbours from about 23 on, logits less than 2^-53
- * apart). Weights are held in 32 bits.
+ * apart). Weights are rounded to 32 bits from scores that keep their bits: small
+ * ones (below exp(-64) of the largest) are 64-bit values.
  *
  * An expert whose logit is -infinity or NaN is out: it is never chosen and
  * adds nothing to the softmax or to its group. A bias of -infinity or NaN

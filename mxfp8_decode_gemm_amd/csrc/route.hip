@@ -14,7 +14,7 @@
 // choices do; the row is done again in FP64 where two that matter lie too
 // close for that: logits whose FP64 scores may be equal, or choices within
 // their error (of 8 of 256 experts, grouped sigmoid with a bias, one row in 75).
-// The weights are FP32.
+// The weights are FP32, from FP64 scores where FP32 would lose them.
 
 #include <hip/hip_runtime.h>
 
@@ -104,6 +104,17 @@ struct Row {
   float top, inv;  // softmax: the largest, 1 / sum of the terms
 };
 
+// The sum of the softmax's terms, uniform (0: every expert is out).
+template <int V>
+__device__ __forceinline__ double score_sum64(const Row<V>& row) {
+  double sum = 0.0;
+  if (row.top > -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += soft_term<double>(row.l[i], row.top);
+  }
+  return wave_sum(sum);
+}
+
 // Chooses in FP64: lane j gets the expert of place j (-1: none).
 template <int V>
 __device__ __forceinline__ int choose_wide(const RouteArgs& a, const Row<V>& row,
@@ -111,14 +122,7 @@ __device__ __forceinline__ int choose_wide(const RouteArgs& a, const Row<V>& row
   const int E = a.r.experts, G = a.r.groups, per = E / G;
   const bool softmax = a.r.score == MXG_ROUTE_SOFTMAX;
   double c[V];
-  double sum = 0.0;
-  if (softmax) {
-    if (row.top > -INFINITY) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) sum += soft_term<double>(row.l[i], row.top);
-    }
-    sum = wave_sum(sum);
-  }
+  const double sum = softmax ? score_sum64<V>(row) : 0.0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const float l = row.l[i];
@@ -177,6 +181,32 @@ __device__ __forceinline__ int choose_wide(const RouteArgs& a, const Row<V>& row
     if (lane == j) id = V * who + at;
   }
   return id;
+}
+
+// Chosen scores of logits further than this below the largest (softmax), or
+// below zero (sigmoid), make their row's weights in FP64. The others are at least
+// exp(-64) / 1024 and keep all their bits in FP32.
+constexpr float kSmall = 64.f;
+
+// The weight of this lane's choice (id < 0: none) from FP64 scores: their ratios
+// and their products with the scale hold where FP32 scores would be subnormal or
+// zero. One rounding to FP32.
+template <int V>
+__device__ __forceinline__ float wide_weight(const RouteArgs& a, const Row<V>& row, int id,
+                                             float logit) {
+  double s = 0.0;
+  if (a.r.score == MXG_ROUTE_SOFTMAX) {
+    const double sum = score_sum64<V>(row);
+    if (id >= 0) s = soft_term<double>(logit, row.top) / sum;
+  } else if (id >= 0) {
+    s = sigmoid64(logit);
+  }
+  if (s < kLeast) s = 0.0;
+  if (a.r.renormalize) {
+    const double sum = wave_sum(s);
+    s = sum > 0.0 ? s / sum : 0.0;
+  }
+  return (float)(s * (double)a.r.scale);
 }
 
 // ---- FP32 choices, where they decide ---------------------------------------
@@ -437,15 +467,21 @@ __global__ void __launch_bounds__(64 * kWaves) route_kernel(RouteArgs a) {
   if (id >= 0) logit = BF16 ? __uint_as_float((uint32_t)src[id] << 16) : __uint_as_float(src[id]);
 
   float w = 0.f;
-  if (id >= 0) w = softmax ? soft_term<float>(logit, row.top) * row.inv : 1.f / (1.f + expf(-logit));
-  if (a.r.renormalize) {
-    const float sum = wave_sum(w);
-    w = sum > 0.f ? w / sum : 0.f;
+  if (__any(id >= 0 && logit < (softmax ? row.top : 0.f) - kSmall)) {
+    w = wide_weight<V>(a, row, id, logit);
+  } else {
+    if (id >= 0)
+      w = softmax ? soft_term<float>(logit, row.top) * row.inv : 1.f / (1.f + expf(-logit));
+    if (a.r.renormalize) {
+      const float sum = wave_sum(w);
+      w = sum > 0.f ? w / sum : 0.f;
+    }
+    w *= a.r.scale;
   }
   if (lane < a.r.top_k) {
     const int64_t at = (int64_t)t * a.r.top_k + lane;
     a.ids[at] = id;
-    a.weights[at] = id >= 0 ? w * a.r.scale : 0.f;
+    a.weights[at] = id >= 0 ? w : 0.f;
   }
 }
 

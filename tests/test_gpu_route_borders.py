@@ -84,3 +84,31 @@ def test_small_differences_that_count(dv):
     for score in ("softmax", "sigmoid"):
         _check(dv, x, 5, score=score)
         _check(dv, x, 5, score=score, groups=4, top_groups=2)
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.5, 1e30])
+def test_weights_of_small_scores(dv, scale):
+    """Chosen scores below FP32's range: renormalised weights are those of the
+    formula, and so is a product with a large scale."""
+    rows = [[-95, -96, -97, -98, -200, -300], [-60, -61, -120, -300, -699, -699],
+            [-500.5, -500, -501, -502, -503, -700], [-90, -103.5, -104, -88, -89, -87.5],
+            [-64, -65, -63, -66, -80, -81], [-707, -706, -706.5, -900, -1e30, -800]]
+    for k in (1, 2, 5):
+        _check(dv, rows, k, score="sigmoid", renormalize=True, scale=scale)
+        _check(dv, rows, k, score="sigmoid", scale=scale)
+    rows = [[0, -110, -110, -112, -90, -50], [3, -100, -101, -102, -103, -103.5],
+            [0, -650, -651, -650.25, -700, -705], [5, 5, -60, -59, -61, -62]]
+    bias = [0, 3, 2.5, 2.25, 2, 1.75]
+    for k in (1, 2, 5, 6):
+        _check(dv, rows, k, bias=bias, renormalize=True, scale=scale)
+        _check(dv, rows, k, bias=bias, scale=scale)
+
+
+def test_weights_of_zero_scores(dv):
+    """A score below 2^-1022 is zero, and a sum of zero leaves the weights zero."""
+    bias = [0, 3, 2, 0]
+    ids, w = _check(dv, [[0, -800, -900, -1e30]], 2, bias=bias, renormalize=True)
+    assert ids.tolist() == [[1, 2]] and w.tolist() == [[0, 0]]
+    ids, w = _check(dv, [[-800, -900, -750, -1e30]], 2, score="sigmoid", renormalize=True)
+    assert w.tolist() == [[0, 0]]
+    _check(dv, [[0, -800, -700, -1e30]], 2, bias=bias, renormalize=True)

@@ -10,10 +10,10 @@
 // Choices are compared as FP64 values: among thousands of rows, two FP32 choices
 // (a rounded sum of a rounded exponential) do fall on the wrong side of each
 // other. Where the choice has the order of the logits themselves (no bias, and
-// no sum of two in a group score) the FP32 logits decide, otherwise FP32
-// choices do; the row is done again in FP64 where two that matter lie too
-// close for that: logits whose FP64 scores may be equal, or choices within
-// their error (of 8 of 256 experts, grouped sigmoid with a bias, one row in 75).
+// no sum of two in a group score) the FP32 logits decide, unless the row has
+// logits whose FP64 scores may be equal; otherwise FP32 choices do where all that
+// matter lie further apart than their error. The other rows are done in FP64
+// (8 of 256 experts, grouped sigmoid with a bias: one row in 75).
 // The weights are FP32, from FP64 scores where FP32 would lose them.
 
 #include <hip/hip_runtime.h>
@@ -89,8 +89,20 @@ __device__ __forceinline__ F soft_term(float l, float m) {
 
 // Scores below FP64's normal range count as zero.
 constexpr double kLeast = 0x1p-1022;
-// Rows with a logit above this are compared in FP64 at once: their largest
-// sigmoids are one but for less than 2^-43.
+// FP64 decides at once where FP64 scores of different logits may come out equal
+// (or in the other order). Where logits alone order the experts (by_logit):
+//   softmax: exp(l - top) / sum has its argument rounded by 2^-53 |l - top|, exp
+//   and quotient by 2^-51, relative; scores of logits that lie d apart differ
+//   by d. FP32 neighbours lie |l| 2^-24 and more apart: four times the error
+//   of both scores where |l| >= 2^-26 (|top| + 4);
+//   sigmoid: exp, sum and reciprocal are off by 2^-51, relative; scores of logits that
+//   lie d apart differ by d (1 - s) >= d exp(-max(l, 0)) / 2 at the larger l. FP32
+//   neighbours below kNearOneByLogit (2^-19 exp(-18) / 2 at 18) and with
+//   |l| >= 2^-22 are 2^-47 and more apart by that measure.
+// Both hold above kNearZero (|top| + 16), with top = 0 for the sigmoid.
+// With a bias or sums of two, sigmoids above kNearOne are one but for 2^-43.
+constexpr float kNearZero = 0x1p-26f;
+constexpr float kNearOneByLogit = 18.f;
 constexpr float kNearOne = 30.f;
 
 __device__ __forceinline__ double sigmoid64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
@@ -210,8 +222,7 @@ __device__ __forceinline__ float wide_weight(const RouteArgs& a, const Row<V>& r
 }
 
 // ---- FP32 choices, where they decide ---------------------------------------
-// Either the logits themselves, given up where two different ones that matter
-// may have equal FP64 scores (may_tie), or choices with an error below
+// Either the logits themselves (exact), or choices with an error below
 // 2^-19 (1 + |c|), given up where two that matter lie closer than kTol:
 //   sigmoid: 1 / (1 + e), e = 2^(-l log2 e) to 1.5 |l| 2^-24 + 2^-22 relative,
 //   moves s by at most s (1 - s) of that, s (1 - s) |l| < 0.23; softmax: the
@@ -248,19 +259,6 @@ __device__ __forceinline__ float exp_near(float x) {
   return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
 }
 
-// Whether the FP64 scores of the logits hi >= lo can come out equal, or in the
-// other order. Equal logits are not meant: their scores are the same bits.
-//   softmax: of exp(l - top) / sum the argument, |l - top| <= 700, is rounded by
-//   2^-53 of itself, exp and quotient by 2^-51: 2^-43 relative. Scores
-//   whose logits differ by d differ by d, relative.
-//   sigmoid: exp, sum and reciprocal are off by 2^-51, relative; scores whose logits
-//   differ by d differ by at least d (1 - s(hi)) >= d exp(-max(hi, 0)) / 2. Above
-//   about 19, FP32 neighbours come under this bound.
-__device__ __forceinline__ bool may_tie(float hi, float lo, bool softmax) {
-  const float d = hi - lo;
-  return hi != lo && !(softmax ? d > 0x1p-40f : d * exp_near(-fmaxf(hi, 0.f)) > 0x1p-46f);
-}
-
 // A lane's two largest keys and their places; of equals the lower place first.
 struct Two {
   int b1 = kOut, b2 = kOut, a1 = 0, a2 = 0;
@@ -295,13 +293,18 @@ __device__ __forceinline__ Two around(Two t, int log) {
   return t;
 }
 
+// Whether the choices have the order of the logits.
+__device__ __forceinline__ bool ordered_by_logit(const RouteArgs& a) {
+  return !a.bias && (a.r.groups == 1 || a.r.group_best == 1 || a.r.experts == a.r.groups);
+}
+
 // Lane j gets the expert of place j in *id; false: FP64 has to decide.
 template <int V>
 __device__ __forceinline__ bool choose(const RouteArgs& a, const Row<V>& row, int* cs, int lane,
                                        int* id) {
   const int E = a.r.experts, G = a.r.groups, per = E / G;
   const bool softmax = a.r.score == MXG_ROUTE_SOFTMAX;
-  const bool by_logit = !a.bias && (G == 1 || a.r.group_best == 1 || per == 1);
+  const bool by_logit = ordered_by_logit(a);
   int k[V];  // the choices' keys
   Two two;
 #pragma unroll
@@ -342,10 +345,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Row<V>& row, in
       const float o = __shfl(score, (h < G ? h : 0) << log, 64);
       const bool other = h < G && h != g;
       ahead += __popcll(__ballot(other && (o > score || (o == score && h < g))) & mine);
-      if (by_logit) {
-        close |= other && g < G && o > -INFINITY && score > -INFINITY &&
-                 may_tie(fmaxf(o, score), fminf(o, score), softmax);
-      } else {
+      if (!by_logit) {
         const float big = fmaxf(fabsf(o), fabsf(score));
         close |= other && g < G && o > -INFINITY && score > -INFINITY &&
                  !(fabsf(o - score) > 2 * kTol * (1.f + big));
@@ -373,7 +373,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Row<V>& row, in
   // lane that has given both looks again at all it holds (seldom).
   int out = -1, key = kOut, n = 0;
   uint64_t gave = 0;  // lanes whose first of two is gone
-  const int rounds = a.r.top_k + 1;  // one more: the largest that is not chosen
+  const int rounds = by_logit ? a.r.top_k : a.r.top_k + 1;
   for (; n < rounds; ++n) {
     const int m = wave_max(two.b1);
     if (m == kOut) break;  // nothing left
@@ -401,11 +401,10 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Row<V>& row, in
       }
     }
   }
-  // Neighbours in the order lie apart.
-  const float c = of_key(key), before = __shfl_up(c, 1, 64);
-  const bool close = by_logit ? may_tie(before, c, softmax)
-                              : !(before - c > kTol * (1.f + fabsf(c)));
-  if (__any(lane > 0 && lane < n && close)) return false;
+  if (!by_logit) {  // neighbours in the order lie apart (one round more than top_k)
+    const float c = of_key(key), before = __shfl_up(c, 1, 64);
+    if (__any(lane > 0 && lane < n && !(before - c > kTol * (1.f + fabsf(c))))) return false;
+  }
   *id = lane < a.r.top_k ? out : -1;
   return true;
 }
@@ -456,10 +455,14 @@ __global__ void __launch_bounds__(64 * kWaves) route_kernel(RouteArgs a) {
   // FP32 first; FP64 for rows with choices too close to each other, or with
   // scores that are about one, or zero, in FP64.
   uint8_t* const cs = lds + sizeof(double) * (size_t)wave * E;
-  bool odd = softmax ? hi == INFINITY : hi > kNearOne;
+  const bool by_logit = ordered_by_logit(a);
+  const float zero = by_logit ? kNearZero * (fabsf(row.top) + 16.f) : 0.f;
+  bool odd = softmax ? hi == INFINITY : hi > (by_logit ? kNearOneByLogit : kNearOne);
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i) {
     odd |= row.l[i] > -INFINITY && row.l[i] < (softmax ? hi : 0.f) - 700.f;
+    odd |= fabsf(row.l[i]) < zero && row.l[i] != 0.f;
+  }
   int id = -1;
   if (__any(odd) || !choose<V>(a, row, reinterpret_cast<int*>(cs), lane, &id))
     id = choose_wide<V>(a, row, reinterpret_cast<double*>(cs), lane);
@@ -467,7 +470,7 @@ __global__ void __launch_bounds__(64 * kWaves) route_kernel(RouteArgs a) {
   if (id >= 0) logit = BF16 ? __uint_as_float((uint32_t)src[id] << 16) : __uint_as_float(src[id]);
 
   float w = 0.f;
-  if (__any(id >= 0 && logit < (softmax ? row.top : 0.f) - kSmall)) {
+  if (__builtin_expect(__any(id >= 0 && logit < (softmax ? row.top : 0.f) - kSmall), 0)) {
     w = wide_weight<V>(a, row, id, logit);
   } else {
     if (id >= 0)

@@ -227,7 +227,8 @@ __device__ __forceinline__ float wide_weight(const RouteArgs& a, const Row<V>& r
 //   sigmoid: 1 / (1 + e), e = 2^(-l log2 e) to 1.5 |l| 2^-24 + 2^-22 relative,
 //   moves s by at most s (1 - s) of that, s (1 - s) |l| < 0.23; softmax: the
 //   term the same with s |d| < 0.37, the sum's 22 roundings; one reciprocal; the
-//   sum with the bias. A group's score adds two.
+//   sum with the bias. A group's score adds two: its error is below
+//   2^-18 (1 + |c1| + |c2|), however small the sum.
 constexpr float kTol = 0x1p-17f;
 
 // Floats as integers of the same order (negative zero just below zero).
@@ -335,7 +336,11 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Row<V>& row, in
     }
     best = around(best, log);
     float score = best.b1 == kOut ? -INFINITY : of_key(best.b1);
-    if (a.r.group_best == 2 && best.b2 != kOut) score += of_key(best.b2);
+    float size = fabsf(score);  // of what the score is a sum of: its error's measure
+    if (a.r.group_best == 2 && best.b2 != kOut) {
+      size += fabsf(of_key(best.b2));
+      score += of_key(best.b2);
+    }
     // Lane sub of a group compares it with groups sub, sub + 2^log, ...
     const uint64_t mine = (log == 6 ? ~0ull : (1ull << (1 << log)) - 1) << (g << log);
     int ahead = 0;  // groups before this one
@@ -346,9 +351,9 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Row<V>& row, in
       const bool other = h < G && h != g;
       ahead += __popcll(__ballot(other && (o > score || (o == score && h < g))) & mine);
       if (!by_logit) {
-        const float big = fmaxf(fabsf(o), fabsf(score));
+        // (Of two groups each compares with the other, by its own size.)
         close |= other && g < G && o > -INFINITY && score > -INFINITY &&
-                 !(fabsf(o - score) > 2 * kTol * (1.f + big));
+                 !(fabsf(o - score) > 2 * kTol * (1.f + size));
       }
     }
     if (__any(close)) return false;

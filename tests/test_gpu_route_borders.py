@@ -86,6 +86,18 @@ def test_small_differences_that_count(dv):
         _check(dv, x, 5, score=score, groups=4, top_groups=2)
 
 
+def test_group_scores_that_cancel(dv):
+    """Two large biases of opposite sign in a group: the score is the small rest,
+    which FP32 sums lose."""
+    x = np.random.default_rng(3).standard_normal((256, 16)).astype(np.float32)
+    for big in (1e3, 1e5, 1e6):
+        for groups in (2, 3, 8):
+            bias = [big, -big] * groups
+            for score in ("sigmoid", "softmax"):
+                _check(dv, x[:, : 2 * groups], 1, bias=bias, score=score, groups=groups,
+                       top_groups=1, group_best=2)
+
+
 @pytest.mark.parametrize("scale", [1.0, 2.5, 1e30])
 def test_weights_of_small_scores(dv, scale):
     """Chosen scores below FP32's range: renormalised weights are those of the

@@ -271,6 +271,13 @@ static bool choose_tile_uncached(int m, int n, int k, int split_k, const char* t
     if (chunks > 4L * 64 * out->wn * out->wk && fits(c2)) *out = c2;
     upgrade_x16(*out);
   }
+  if (found && lora) {
+    const long resident =
+        gemm_resident_blocks(*out, split_k, gemm_lds_bytes(*out, m, ks) + lora_lds, true);
+    if (resident <= 0) return false;
+    out->cus = cus;
+    out->resident = (int)resident;
+  }
   return found;
 }
 
@@ -291,9 +298,11 @@ long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool 
   }
   const Variant* v = find_variant(c, split_k);
   if (!v) return -1;
-  // Both activation forms of the variant: a shape gets one tile either way.
+  // Both activation forms of the variant (with adapters: with and without
+  // helping workgroups): a shape gets one tile either way.
   int per_cu = 1 << 30, cus = 0;
-  for (const void* fn : {variant_fn(*v, false, c.x16, lora), variant_fn(*v, true, c.x16, lora)}) {
+  for (int form = 0; form < (lora ? 4 : 2); ++form) {
+    const void* fn = variant_fn(*v, form & 1, c.x16, lora, form >> 1);
     int n = 0;
     if (!fn) return -1;
     if (lds_bytes > 64 * 1024 &&
@@ -342,12 +351,17 @@ hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t 
   if (lora) {
     args.lora.lds_off = (int32_t)((lds + 15) / 16 * 16);
     lds += lora_lds_bytes(a.m, a.lora.rank);
-    // u's dot products: one wave of each workgroup of the GEMM, of at most 512,
-    // and where these are few, workgroups that only help (up to one per CU: a
-    // small N leaves the rest of the device idle). They come last in the grid.
-    constexpr int kFull = 256;
+    // u's dot products: one wave of each workgroup of the GEMM that runs from the
+    // start, of at most 512, and where these are few, workgroups that only
+    // help (up to one per CU: a small N leaves the rest of the device idle). They
+    // come last in the grid. A workgroup that starts when others end can take
+    // no share: all of those would wait for it, then compute u alone (dealt to
+    // 512 where 256 ran, N=12288/K=4096/m=4 rank 64 took 665 us instead of 19).
+    constexpr int kShares = 512;
     const int groups = (int)grid.x, waves = (int)block.x / 64;
-    const int most = groups < kFull ? groups + (kFull - groups) * waves : groups;
+    int shares = groups < c.resident ? groups : c.resident;
+    if (shares > kShares) shares = kShares;
+    const int most = groups < c.cus ? groups + (c.cus - groups) * waves : shares;
     const int items = a.m * a.lora.rank;
     int ps = 0;
     args.lora.groups = groups;
@@ -357,13 +371,13 @@ hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t 
       // A task's 8 pieces of 512 values are one round trip; beyond that, cut it
       // while there are waves left over.
       while (ps < 2 && a.k >> (ps + 1) >= 512 && (items << (ps + 1)) <= kLoraMaxPairs &&
-             (a.k >> ps > 8 * 512 || (items << (ps + 1)) <= (groups < 512 ? groups : 512)))
+             (a.k >> ps > 8 * 512 || (items << (ps + 1)) <= shares))
         ++ps;
       const int tasks = items << ps;
       int helping = 0;
       if (tasks > groups && most > groups)
         helping = ((tasks < most ? tasks : most) - groups + waves - 1) / waves;
-      args.lora.workers = groups < 512 ? groups + helping * waves : 512;
+      args.lora.workers = shares + helping * waves;
       grid.x += helping;
       helped = helping > 0;
     }

@@ -72,6 +72,9 @@ struct TileCfg {
   int rb, wn, wk, depth;
   int xr = 1;
   int x16 = 0;
+  // Of the chooser, for launches with adapters: the device's CUs, and the
+  // workgroups of the launch that run at once.
+  int cus = 0, resident = 0;
 };
 
 inline int tile_rows(const TileCfg& c) { return 16 * c.rb * c.wn; }
@@ -97,7 +100,8 @@ bool choose_tile(int m, int n, int k, int split_k, const char* tile, TileCfg* ou
 bool tile_available(const TileCfg& c);
 
 // How many workgroups of this variant can be resident at once on the current
-// device (CUs x blocks per CU); negative on a HIP error.
+// device (CUs x blocks per CU); negative on a HIP error. lora: of its kernels
+// with adapters.
 long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool lora = false);
 
 // ev_start/ev_stop (may be null) are recorded around the kernel itself.

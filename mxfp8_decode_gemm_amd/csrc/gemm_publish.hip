@@ -272,11 +272,13 @@ static bool choose_tile_uncached(int m, int n, int k, int split_k, const char* t
     upgrade_x16(*out);
   }
   if (found && lora) {
-    const long resident =
-        gemm_resident_blocks(*out, split_k, gemm_lds_bytes(*out, m, ks) + lora_lds, true);
-    if (resident <= 0) return false;
     out->cus = cus;
-    out->resident = (int)resident;
+    for (int form = 0; form < 2; ++form) {
+      const long started =
+          gemm_started_blocks(*out, split_k, gemm_lds_bytes(*out, m, ks) + lora_lds, form);
+      if (started <= 0) return false;
+      out->started[form] = (int)started;
+    }
   }
   return found;
 }
@@ -322,6 +324,27 @@ long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool 
   return r;
 }
 
+long gemm_started_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool bf16_x) {
+  const long resident = gemm_resident_blocks(c, split_k, lds_bytes, true);
+  const Variant* v = find_variant(c, split_k);
+  int dev = 0, cus = 0;
+  if (resident <= 0 || !v || hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+    return -1;
+  constexpr int kSimds = 4;
+  const int waves = tile_threads(c, split_k, true) / 64;
+  long started = resident;
+  for (bool helped : {false, true}) {
+    int n = 0;  // single waves a CU holds by their registers
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(
+            &n, variant_fn(*v, bf16_x, c.x16, true, helped), 64, 0) != hipSuccess)
+      return -1;
+    const int per_cu = (n / kSimds) / ((waves + kSimds - 1) / kSimds);
+    started = std::min(started, (long)cus * (per_cu > 1 ? per_cu : 1));
+  }
+  return started;
+}
+
 hipError_t launch_pack_weight(const uint8_t* w, const uint8_t* ws, int n, int k, uint8_t* wp,
                               uint8_t* wsp, hipStream_t s, int count) {
   const size_t wpb = mxgemm_packed_weight_bytes(n, k), wspb = mxgemm_packed_scale_bytes(n, k);
@@ -356,10 +379,11 @@ hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t 
     // help (up to one per CU: a small N leaves the rest of the device idle). They
     // come last in the grid. A workgroup that starts when others end can take
     // no share: all of those would wait for it, then compute u alone (dealt to
-    // 512 where 256 ran, N=12288/K=4096/m=4 rank 64 took 665 us instead of 19).
+    // 512 where 256 ran, N=12288/K=4096/m=4 rank 64 took 663 us instead of 22).
     constexpr int kShares = 512;
     const int groups = (int)grid.x, waves = (int)block.x / 64;
-    int shares = groups < c.resident ? groups : c.resident;
+    const int started = c.started[a.xb != nullptr ? 1 : 0];
+    int shares = groups < started ? groups : started;
     if (shares > kShares) shares = kShares;
     const int most = groups < c.cus ? groups + (c.cus - groups) * waves : shares;
     const int items = a.m * a.lora.rank;

@@ -73,8 +73,9 @@ struct TileCfg {
   int xr = 1;
   int x16 = 0;
   // Of the chooser, for launches with adapters: the device's CUs, and the
-  // workgroups of the launch that run at once.
-  int cus = 0, resident = 0;
+  // workgroups of the launch that run from its start (gemm_started_blocks) with
+  // MXFP8 and with BF16 x.
+  int cus = 0, started[2] = {0, 0};
 };
 
 inline int tile_rows(const TileCfg& c) { return 16 * c.rb * c.wn; }
@@ -103,6 +104,15 @@ bool tile_available(const TileCfg& c);
 // device (CUs x blocks per CU); negative on a HIP error. lora: of its kernels
 // with adapters.
 long gemm_resident_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool lora = false);
+
+// How many workgroups of a launch with adapters run from its start on an idle
+// device, counted by SIMD: a workgroup's waves go to the CU's four SIMDs in turn,
+// from the first one on, so that one SIMD takes a quarter of them, rounded up.
+// gemm_resident_blocks counts a CU's waves as a whole: it says two of the 64-row
+// tile's workgroups with BF16 x (five waves at 132 VGPRs, three to a SIMD), where a
+// second one does not start (measured). Its own callers need no more: workgroups
+// start in order, so a tile's slices that run wait only for ones that will.
+long gemm_started_blocks(const TileCfg& c, int split_k, size_t lds_bytes, bool bf16_x);
 
 // ev_start/ev_stop (may be null) are recorded around the kernel itself.
 hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t s,

@@ -55,3 +55,26 @@ def test_many_workgroups(env, m, n, k, rank, adapters):
     adapted = _us(lambda: c.lin(x, dev_ids, x_scale=xs, c_out=out))
     print(f"m={m} n={n} k={k} rank={rank}: mxgemm {plain:.1f} us, with adapters {adapted:.1f} us")
     assert adapted < 2 * plain + 10
+
+
+@pytest.mark.parametrize("m,n,k,split_k,rank", [(5, 4096, 16384, 8, 32), (1, 32768, 4096, 1, 128)])
+def test_many_workgroups_bf16(env, m, n, k, split_k, rank):
+    """BF16 x on tiles of five waves, of whose workgroups two would fit a CU by the
+    sum of its registers, but not by SIMD: in time, against the same call without
+    adapters in the rows."""
+    mx, dv = env
+    g = torch.Generator(device="cuda").manual_seed(n)
+    codes = torch.randint(0, 120, (n, k), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.full((n, k // 32), 118, dtype=torch.uint8, device="cuda")
+    a = torch.randn(4, rank, k, device="cuda", generator=g).bfloat16()
+    b = torch.randn(4, n, rank, device="cuda", generator=g).bfloat16()
+    lin = dv.AdaptedLinear(codes, scales, a, b, torch.ones(4, device="cuda"), split_k)
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    ids = torch.arange(m, dtype=torch.int32, device="cuda") % 4
+    none = torch.full_like(ids, -1)
+    out = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    bare = _us(lambda: lin(x, none, c_out=out))
+    adapted = _us(lambda: lin(x, ids, c_out=out))
+    print(f"m={m} n={n} k={k} split_k={split_k} rank={rank}: none {bare:.1f} us, adapters "
+          f"{adapted:.1f} us")
+    assert adapted < 2 * bare + 10

@@ -97,7 +97,7 @@ def parse() -> argparse.Namespace:
 TRAFFIC_PROFILE = os.path.join(ROOT, "profiles", "gemm_publish_n7168_k8192_m8_s4_hbm_traffic.md")
 KERNEL_SOURCES = [os.path.join(ROOT, "mxfp8_decode_gemm_amd", "csrc", f)
                   for f in ("gemm_kernel.h", "gemm_publish.hip", "mxgemm_internal.h",
-                            "quant_device.h", "mx_device.h")]
+                            "quant_device.h", "mx_device.h", "hand_off.h")]
 
 
 def strip_comments(src: str) -> str:

@@ -70,6 +70,7 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/mxgemm.h"
+#include "hand_off.h"
 #include "mx_device.h"
 #include "mxgemm_internal.h"
 #include "quant_device.h"
@@ -644,27 +645,28 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
   // (its flag words hold it), and the generation handed to the consumer.
   const int groups = ALONE ? (int)gridDim.x : l.groups;
   uint32_t polls = 0;
-  bool pending = true;
+  bool llate = true, alate = SK > 1;
   epoch = __builtin_amdgcn_readfirstlane(epoch);
-  while (pending && polls++ < a.spin_limit) {
-    pending = false;
+  while ((llate || alate) && polls++ < a.spin_limit) {
+    llate = alate = false;
     for (int i = lane; i < (int)gridDim.x; i += 64) {
-      pending |= ld_agent_u32(l.flags + i) != lepoch;
-      if (SK > 1 && i < groups) pending |= ld_agent_u32(a.flags + i) != epoch;
+      llate |= ld_agent_u32(l.flags + i) != lepoch;
+      if (SK > 1 && i < groups) alate |= ld_agent_u32(a.flags + i) != epoch;
     }
-    pending = __any(pending);
-    if (pending) __builtin_amdgcn_s_sleep(2);
+    llate = __any(llate);
+    alate = __any(alate);
+    if (llate || alate) __builtin_amdgcn_s_sleep(2);
   }
   if (lane != 0) return;
-  if (pending) {
+  const HandOff h = hand_off(llate, alate);
+  if (h.mark_scratch)
     __hip_atomic_fetch_or(l.hdr + MXG_WS_ERROR, MXG_ERR_SPLITK_SPIN, __ATOMIC_RELAXED,
                           __HIP_MEMORY_SCOPE_AGENT);
-    if (SK > 1)
-      __hip_atomic_fetch_or(a.ws_hdr + MXG_WS_ERROR, MXG_ERR_SPLITK_SPIN, __ATOMIC_RELAXED,
-                            __HIP_MEMORY_SCOPE_AGENT);
-  }
+  if (SK > 1 && h.mark_workspace)
+    __hip_atomic_fetch_or(a.ws_hdr + MXG_WS_ERROR, MXG_ERR_SPLITK_SPIN, __ATOMIC_RELAXED,
+                          __HIP_MEMORY_SCOPE_AGENT);
   st_agent_u32(l.hdr + MXG_WS_EPOCH, lepoch + 1u == 0u ? 1u : lepoch + 1u);
-  if (SK > 1 && !pending)
+  if (SK > 1 && h.advance_workspace)
     st_agent_u32(a.ws_hdr + MXG_WS_EPOCH, (epoch + 1u == 0u ? 1u : epoch + 1u) - a.epoch_bias);
   if (SK > 1 && a.state) st_agent_u32(a.state + MXG_STATE_ACTIVE, gen);
 }

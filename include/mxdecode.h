@@ -184,15 +184,20 @@ int mxgemm_lora_scratch_init(void* scratch, size_t scratch_bytes, void* stream);
  *   x, x_scale  MXFP8 x, or both NULL with x_bf16 given
  *   x_bf16   BF16 x, or NULL with x and x_scale given
  *   scratch  device, at least mxgemm_lora_scratch_bytes(n), 16-B aligned, armed
- *            by mxgemm_lora_scratch_init; one call at a time per scratch.
- *            Workgroup 0 gives up waiting for the others to start after
- *            mb->spin_limit polls (MXG_DEFAULT_SPIN_LIMIT without mb) and sets
- *            MXG_ERR_SPLITK_SPIN in the scratch's ERROR word (MXG_WS_ERROR):
- *            later calls are right but slow until it is armed again
+ *            by mxgemm_lora_scratch_init; one call at a time per scratch
  *   c_out    device [m, n] BF16 as rounded; may be NULL with mb
  * Other arguments as mxgemm_publish. With split_k > 1 the workgroups of a call
  * wait for each other, as there: two such calls must not run at once on one
- * device. Errors: its errors (MXG_EUNSUPPORTED also where the x slice leaves no
+ * device.
+ *
+ * Failure: workgroup 0 gives up waiting for the others to start after
+ * mb->spin_limit polls (MXG_DEFAULT_SPIN_LIMIT without mb) and sets
+ * MXG_ERR_SPLITK_SPIN in the scratch's ERROR word (MXG_WS_ERROR): the call and
+ * later ones are right, but slow until the scratch is armed again. A split-K
+ * wait that gives up sets it in the split-K workspace's ERROR word, as in
+ * mxgemm_publish: the values it was for, and all of later calls' on that
+ * workspace until it is armed again, are NaN in c_out and unpublished.
+ * Errors: its errors (MXG_EUNSUPPORTED also where the x slice leaves no
  * LDS for u), MXG_EINVAL for a bad adapter argument, MXG_EWORKSPACE for a missing
  * or small scratch. */
 int mxgemm_lora(const mxg_mailbox* mb, const uint8_t* w, const uint8_t* w_scale,

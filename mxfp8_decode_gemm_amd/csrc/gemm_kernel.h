@@ -1344,11 +1344,14 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 || LORA ? 1 : 0)))
       fp |= row_down<1>(fp);
       fp |= row_down<2>(fp);
       fp |= row_down<4>(fp);
-      if (live && e == 0 && fp == 0 && !ws_failed) {
-        const uint4 raw = {pair, p1, p2, p3};
+      // With adapters c_out says so too: NaN.
+      const bool whole = fp == 0 && !ws_failed;
+      if (live && e == 0 && (whole || LORA)) {
+        uint4 raw = {pair, p1, p2, p3};
+        if (LORA && !whole) raw = uint4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
         const size_t off = ((size_t)t * N + row0 + 8 * jc) * 2;
         if (a.c_out) *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.c_out) + off) = raw;
-        if (a.slot) {
+        if (a.slot && (whole || !LORA)) {
           uint4 clean;
           clean.x = clear_negative_zero(raw.x);
           clean.y = clear_negative_zero(raw.y);

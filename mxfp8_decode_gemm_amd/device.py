@@ -302,7 +302,9 @@ class AdaptedLinear:
     """An MXFP8 projection [n, k] (uint8 codes and scale bytes, packed once)
     with a stack of low-rank adapters: a [adapters, rank, k] and b [adapters,
     n, rank] in BF16, scale [adapters] in FP32. Owns the split-K workspace and
-    the scratch; calls go one at a time, in order, on one stream."""
+    the scratch; calls go one at a time, in order, on one stream. A result whose
+    split-K exchange failed is NaN (or not published); ``errors`` names it, and
+    ``rearm`` makes the object good again."""
 
     def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
                  scale: torch.Tensor, split_k: int = 1, stream=None) -> None:
@@ -328,6 +330,19 @@ class AdaptedLinear:
         self._weights = self.w.data_ptr(), self.w_scale.data_ptr()
         ws = self.workspace
         self._memory = (ws.buf.data_ptr(), ws.nbytes) if ws else (None, 0)
+
+    def errors(self) -> int:
+        """MXG_ERR_* bits of the calls since the last arming, the scratch's and
+        the workspace's (waits for the device)."""
+        bits = int(self.scratch[mx.WS_ERROR])
+        return bits | int(self.workspace.header()[mx.WS_ERROR]) if self.workspace else bits
+
+    def rearm(self, stream=None) -> None:
+        """Arms the scratch and the workspace again; no call may be in flight."""
+        handle = _on(self.device, stream)
+        mx.mxgemm_lora_scratch_init(self.scratch, self.scratch_bytes, handle)
+        if self.workspace:
+            mx.mxgemm_workspace_init(self.workspace.buf, self.workspace.nbytes, handle)
 
     def _call(self, mb, x, ids, x_scale, c_out, stream):
         dev = self.device

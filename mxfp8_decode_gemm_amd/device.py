@@ -254,7 +254,14 @@ class Experts:
     """The experts of one layer: MXFP8 weights packed once (w13 [experts,
     2 inter, hidden]: gate rows, then up rows; w2 [experts, hidden, inter];
     uint8 codes and scale bytes) and a workspace for ``max_pairs`` (token,
-    choice) pairs. Calls go one at a time, in order, on one stream."""
+    choice) pairs. Calls go one at a time, in order, on one stream. Its tensors
+    may be written, not replaced."""
+
+    w13 = property(lambda self: self._packed[0])
+    w13_scale = property(lambda self: self._packed[1])
+    w2 = property(lambda self: self._packed[2])
+    w2_scale = property(lambda self: self._packed[3])
+    workspace = property(lambda self: self._workspace)
 
     def __init__(self, w13: torch.Tensor, w13_scale: torch.Tensor, w2: torch.Tensor,
                  w2_scale: torch.Tensor, max_pairs: int = mx.MOE_MAX_PAIRS, stream=None) -> None:
@@ -266,11 +273,9 @@ class Experts:
         self.nbytes = mx.mxmoe_workspace_bytes(max_pairs, 1, self.experts, self.hidden, self.inter)
         if two % 2 or self.nbytes == 0:
             raise ValueError("w13, w2 or max_pairs: sizes that mxmoe_experts does not take")
-        self.w13, self.w13_scale = pack_experts(w13, w13_scale, stream)
-        self.w2, self.w2_scale = pack_experts(w2, w2_scale, stream)
-        self.workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
-        self._weights = (self.w13.data_ptr(), self.w13_scale.data_ptr(), self.w2.data_ptr(),
-                         self.w2_scale.data_ptr())
+        self._packed = (*pack_experts(w13, w13_scale, stream), *pack_experts(w2, w2_scale, stream))
+        self._workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
+        self._weights = tuple(t.data_ptr() for t in self._packed)
 
     def __call__(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
                  out: torch.Tensor = None, stream=None) -> torch.Tensor:
@@ -291,7 +296,7 @@ class Experts:
         code = _lib.mxmoe_experts(
             px, _address(ids, "ids", torch.int32, chosen, dev),
             _address(weights, "weights", torch.float32, chosen, dev), *self._weights, chosen[0],
-            chosen[1], self.experts, self.hidden, self.inter, self.workspace.data_ptr(),
+            chosen[1], self.experts, self.hidden, self.inter, self._workspace.data_ptr(),
             self.nbytes, out.data_ptr(), handle)
         if code:
             mx._check(code, "mxmoe_experts")
@@ -304,7 +309,32 @@ class AdaptedLinear:
     n, rank] in BF16, scale [adapters] in FP32. Owns the split-K workspace and
     the scratch; calls go one at a time, in order, on one stream. A result whose
     split-K exchange failed is NaN (or not published); ``errors`` names it, and
-    ``rearm`` makes the object good again."""
+    ``rearm`` makes the object good again.
+
+    ``a``, ``b`` and ``scale`` are the caller's tensors, read by every call as they
+    are then: they may be written, or replaced (a call after that looks at the new
+    ones; a captured graph keeps those it was captured with, which have to
+    live). ``scratch`` may be another armed one, as for projections that share
+    it. The packed weight and the workspace may be written, not replaced."""
+
+    w = property(lambda self: self._packed[0])
+    w_scale = property(lambda self: self._packed[1])
+    workspace = property(lambda self: self._workspace)
+    scratch = property(lambda self: self._scratch)
+    scratch_bytes = property(lambda self: self._scratch_bytes)
+
+    @scratch.setter
+    def scratch(self, t: torch.Tensor) -> None:
+        _refuse(t, "scratch", torch.int32, (None,), self.device)
+        if 4 * t.numel() < mx.mxgemm_lora_scratch_bytes(self.n):
+            raise ValueError(f"scratch: {4 * t.numel()} bytes are too few for n = {self.n}")
+        self._scratch, self._scratch_bytes = t, 4 * t.numel()
+
+    @scratch_bytes.setter
+    def scratch_bytes(self, nbytes: int) -> None:
+        if nbytes > 4 * self._scratch.numel():
+            raise ValueError(f"scratch_bytes: {nbytes} are more than the scratch has")
+        self._scratch_bytes = nbytes
 
     def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
                  scale: torch.Tensor, split_k: int = 1, stream=None) -> None:
@@ -313,23 +343,32 @@ class AdaptedLinear:
         dev = self.device = w.device
         handle = _on(dev, stream)
         _refuse(w_scale, "w_scale", torch.uint8, (self.n, self.k // 32), dev)
-        _refuse(a, "a", torch.bfloat16, (None, None, self.k), dev)
-        adapters, rank = a.shape[:2]
-        _refuse(b, "b", torch.bfloat16, (adapters, self.n, rank), dev)
-        _refuse(scale, "scale", torch.float32, (adapters,), dev)
-        self.scratch_bytes = mx.mxgemm_lora_scratch_bytes(self.n)
-        if self.scratch_bytes == 0 or adapters < 1 or rank % 8 or not 8 <= rank <= mx.LORA_MAX_RANK:
-            raise ValueError("w or a: sizes that mxgemm_lora does not take")
-        self.split_k = split_k
-        self.w, self.w_scale = pack_weight(w, w_scale, self.n, self.k, handle)
         self.a, self.b, self.scale = a, b, scale
-        self.workspace = Workspace(self.n, split_k, dev, handle) if split_k > 1 else None
-        self.scratch = torch.empty(self.scratch_bytes // 4, dtype=torch.int32, device=dev)
-        mx.mxgemm_lora_scratch_init(self.scratch, self.scratch_bytes, handle)
-        self.lora = mx.mxg_lora(a.data_ptr(), b.data_ptr(), scale.data_ptr(), None, adapters, rank)
-        self._weights = self.w.data_ptr(), self.w_scale.data_ptr()
-        ws = self.workspace
+        self._take_adapters()
+        nbytes = mx.mxgemm_lora_scratch_bytes(self.n)
+        if nbytes == 0:
+            raise ValueError("w: sizes that mxgemm_lora does not take")
+        self.split_k = split_k
+        self._packed = pack_weight(w, w_scale, self.n, self.k, handle)
+        self._workspace = Workspace(self.n, split_k, dev, handle) if split_k > 1 else None
+        self.scratch = torch.empty(nbytes // 4, dtype=torch.int32, device=dev)
+        mx.mxgemm_lora_scratch_init(self.scratch, nbytes, handle)
+        self._weights = tuple(t.data_ptr() for t in self._packed)
+        ws = self._workspace
         self._memory = (ws.buf.data_ptr(), ws.nbytes) if ws else (None, 0)
+
+    def _take_adapters(self) -> None:
+        """Looks at a, b and scale, and keeps them and their addresses."""
+        a, b, scale = self.a, self.b, self.scale
+        _refuse(a, "a", torch.bfloat16, (None, None, self.k), self.device)
+        adapters, rank = a.shape[:2]
+        _refuse(b, "b", torch.bfloat16, (adapters, self.n, rank), self.device)
+        _refuse(scale, "scale", torch.float32, (adapters,), self.device)
+        if adapters < 1 or rank % 8 or not 8 <= rank <= mx.LORA_MAX_RANK:
+            raise ValueError("a: sizes that mxgemm_lora does not take")
+        self._adapters = a, b, scale
+        self._places = a.data_ptr(), b.data_ptr(), scale.data_ptr()
+        self.lora = mx.mxg_lora(*self._places, None, adapters, rank)
 
     def errors(self) -> int:
         """MXG_ERR_* bits of the calls since the last arming, the scratch's and
@@ -355,6 +394,11 @@ class AdaptedLinear:
         else:
             form = (_address(x, "x", torch.uint8, (m, self.k), dev),
                     _address(x_scale, "x_scale", torch.uint8, (m, self.k // 32), dev), None)
+        a, b, scale = self.a, self.b, self.scale
+        was = self._adapters
+        if (a is not was[0] or b is not was[1] or scale is not was[2]
+                or (a.data_ptr(), b.data_ptr(), scale.data_ptr()) != self._places):
+            self._take_adapters()
         # (Read by the library within the call.)
         self.lora.ids = _address(ids, "ids", torch.int32, (m,), dev)
         pc = None
@@ -365,8 +409,8 @@ class AdaptedLinear:
             _keep(c_out, stream)
             pc = c_out.data_ptr()
         code = _lib.mxgemm_lora(mb, *self._weights, *form, m, self.n, self.k, self.split_k,
-                                *self._memory, self.lora, self.scratch.data_ptr(),
-                                self.scratch_bytes, pc, handle)
+                                *self._memory, self.lora, self._scratch.data_ptr(),
+                                self._scratch_bytes, pc, handle)
         if code:
             mx._check(code, "mxgemm_lora")
         return c_out

@@ -182,14 +182,56 @@ def _on(device: torch.device, stream):
         raise ValueError(f"tensors on {device}, but the current device is cuda:{_device()}")
     if stream is None:
         return _raw_stream(device.index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, int):
+        return stream
+    if stream.device != device:
+        raise ValueError(f"a stream of {stream.device} for tensors on {device}")
+    return stream.cuda_stream
 
 
-def _keep(t: torch.Tensor, stream) -> None:
-    """Keeps a fresh output's memory until a call on a stream other than the
-    one it was allocated on has ended."""
+# Memory and streams. A fresh tensor of a call on a given stream is allocated on that
+# stream: on the current one it could be memory that work queued there still uses.
+# The current stream, where the caller goes on, is noted for it. Tensors that a call
+# on a given stream is handed are noted as used there, so that memory the caller
+# drops is not given out while the call runs. A handle (an int) names a stream whose
+# end this module cannot see: nothing is noted for it, and what such a call uses has to
+# live until it has ended.
+
+
+def _stream(stream, device: torch.device):
+    """The given stream as torch's (None for the current one)."""
+    return torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream
+
+
+def _fresh(like: torch.Tensor, shape: tuple, dtype, stream) -> torch.Tensor:
+    """An output's memory, for a call on the given stream."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(_stream(stream, like.device)):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
+def _lend(stream, *tensors) -> None:
+    """Notes the tensors as used on the given stream."""
     if stream is not None and not isinstance(stream, int):
-        t.record_stream(stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+class _Home:
+    """The tensors an object owns, made on one stream: other streams it is used on are
+    noted for them."""
+
+    def __init__(self, handle: int, tensors: tuple) -> None:
+        self._seen, self._tensors = {handle}, tensors
+
+    def used(self, handle: int, stream) -> None:
+        if handle not in self._seen and not isinstance(stream, int):
+            self._seen.add(handle)
+            _lend(stream or torch.cuda.current_stream(self._tensors[0].device), *self._tensors)
 
 
 _SCORES = {"softmax": mx.ROUTE_SOFTMAX, "sigmoid": mx.ROUTE_SIGMOID}
@@ -218,13 +260,11 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
     handle = _on(dev, stream)
     out = (tokens, top_k if top_k > 0 else 0)
     if ids is None:
-        ids = logits.new_empty(out, dtype=torch.int32)
-        _keep(ids, stream)
+        ids = _fresh(logits, out, torch.int32, stream)
     else:
         _address(ids, "ids", torch.int32, out, dev)
     if weights is None:
-        weights = logits.new_empty(out, dtype=torch.float32)
-        _keep(weights, stream)
+        weights = _fresh(logits, out, torch.float32, stream)
     else:
         _address(weights, "weights", torch.float32, out, dev)
     router = mx.mxmoe_router(experts, top_k, _SCORES[score], groups, top_groups, group_best,
@@ -235,6 +275,8 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
         ids.data_ptr(), weights.data_ptr(), handle)
     if code:
         mx._check(code, "mxmoe_route")
+    if stream is not None:
+        _lend(stream, logits, bias, ids, weights)
     return ids, weights
 
 
@@ -244,9 +286,10 @@ def pack_experts(w: torch.Tensor, ws: torch.Tensor, stream=None):
     e, n, k = w.shape
     _refuse(ws, "w_scale", torch.uint8, (e, n, k // 32), w.device)
     handle = _on(w.device, stream)
-    wp = torch.empty(mx.mxmoe_packed_weight_bytes(e, n, k), dtype=torch.uint8, device=w.device)
-    wsp = torch.empty(mx.mxmoe_packed_scale_bytes(e, n, k), dtype=torch.uint8, device=w.device)
+    wp = _fresh(w, (mx.mxmoe_packed_weight_bytes(e, n, k),), torch.uint8, stream)
+    wsp = _fresh(w, (mx.mxmoe_packed_scale_bytes(e, n, k),), torch.uint8, stream)
     mx.mxmoe_pack_weight(w, ws, e, n, k, wp, wsp, handle)
+    _lend(stream, w, ws)
     return wp, wsp
 
 
@@ -274,8 +317,9 @@ class Experts:
         if two % 2 or self.nbytes == 0:
             raise ValueError("w13, w2 or max_pairs: sizes that mxmoe_experts does not take")
         self._packed = (*pack_experts(w13, w13_scale, stream), *pack_experts(w2, w2_scale, stream))
-        self._workspace = torch.empty(self.nbytes, dtype=torch.uint8, device=dev)
+        self._workspace = _fresh(w13, (self.nbytes,), torch.uint8, stream)
         self._weights = tuple(t.data_ptr() for t in self._packed)
+        self._home = _Home(_on(dev, stream), (*self._packed, self._workspace))
 
     def __call__(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
                  out: torch.Tensor = None, stream=None) -> torch.Tensor:
@@ -289,10 +333,10 @@ class Experts:
         rows = (chosen[0], self.hidden)
         px = _address(x, "x", torch.bfloat16, rows, dev)
         if out is None:
-            out = x.new_empty(rows)
-            _keep(out, stream)
+            out = _fresh(x, rows, torch.bfloat16, stream)
         else:
             _address(out, "out", torch.bfloat16, rows, dev)
+        self._home.used(handle, stream)
         code = _lib.mxmoe_experts(
             px, _address(ids, "ids", torch.int32, chosen, dev),
             _address(weights, "weights", torch.float32, chosen, dev), *self._weights, chosen[0],
@@ -300,6 +344,8 @@ class Experts:
             self.nbytes, out.data_ptr(), handle)
         if code:
             mx._check(code, "mxmoe_experts")
+        if stream is not None:
+            _lend(stream, x, ids, weights, out)
         return out
 
 
@@ -349,12 +395,15 @@ class AdaptedLinear:
         if nbytes == 0:
             raise ValueError("w: sizes that mxgemm_lora does not take")
         self.split_k = split_k
-        self._packed = pack_weight(w, w_scale, self.n, self.k, handle)
-        self._workspace = Workspace(self.n, split_k, dev, handle) if split_k > 1 else None
-        self.scratch = torch.empty(nbytes // 4, dtype=torch.int32, device=dev)
+        with torch.cuda.stream(_stream(stream, dev)):  # its memory is that stream's
+            self._packed = pack_weight(w, w_scale, self.n, self.k, handle)
+            self._workspace = Workspace(self.n, split_k, dev, handle) if split_k > 1 else None
+            self.scratch = torch.empty(nbytes // 4, dtype=torch.int32, device=dev)
         mx.mxgemm_lora_scratch_init(self.scratch, nbytes, handle)
+        _lend(stream, w, w_scale)
         self._weights = tuple(t.data_ptr() for t in self._packed)
         ws = self._workspace
+        self._home = _Home(handle, (*self._packed, self.scratch) + ((ws.buf,) if ws else ()))
         self._memory = (ws.buf.data_ptr(), ws.nbytes) if ws else (None, 0)
 
     def _take_adapters(self) -> None:
@@ -405,14 +454,16 @@ class AdaptedLinear:
         if c_out is not None:
             pc = _address(c_out, "c_out", torch.bfloat16, (m, self.n), dev)
         elif mb is None:
-            c_out = x.new_empty((m, self.n), dtype=torch.bfloat16)
-            _keep(c_out, stream)
+            c_out = _fresh(x, (m, self.n), torch.bfloat16, stream)
             pc = c_out.data_ptr()
+        self._home.used(handle, stream)
         code = _lib.mxgemm_lora(mb, *self._weights, *form, m, self.n, self.k, self.split_k,
                                 *self._memory, self.lora, self._scratch.data_ptr(),
                                 self._scratch_bytes, pc, handle)
         if code:
             mx._check(code, "mxgemm_lora")
+        if stream is not None:
+            _lend(stream, x, ids, x_scale, c_out, a, b, scale, self._scratch)
         return c_out
 
     def __call__(self, x: torch.Tensor, ids: torch.Tensor, x_scale: torch.Tensor = None,

@@ -145,6 +145,8 @@ def as_u16(t: torch.Tensor) -> np.ndarray:
 # ---------------------------------------------------------------------------
 
 
+# No operator here has a backward pass: a tensor that requires a gradient is refused
+# where one would be recorded.
 # A decode step's calls take a few microseconds on the GPU, so the checks below
 # are written to cost less than that on the host.
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -164,12 +166,19 @@ def _refuse(t, name: str, dtype, shape, device) -> None:
         raise ValueError(f"{name}: on {t.device}, not on {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
+    _refuse_gradient(t, name)
+
+
+def _refuse_gradient(t: torch.Tensor, name: str) -> None:
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name}: requires a gradient, and the decode operators have none "
+                         "(call them under torch.no_grad)")
 
 
 def _address(t, name: str, dtype, shape: tuple, device) -> int:
     """The address of a contiguous device tensor of this type and shape."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == device and t.is_contiguous()):
+            and t.device == device and t.is_contiguous() and not t.requires_grad):
         return t.data_ptr()
     _refuse(t, name, dtype, shape, device)
     return t.data_ptr()
@@ -248,6 +257,8 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
     kind = _LOGITS.get(logits.dtype) if isinstance(logits, torch.Tensor) else None
     if kind is None or logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits: a float32 or bfloat16 device tensor [tokens, experts] is needed")
+    if logits.requires_grad:
+        _refuse_gradient(logits, "logits")
     tokens, experts = logits.shape
     row_stride, step = logits.stride()
     if step != 1 and experts > 1:
@@ -446,7 +457,8 @@ class AdaptedLinear:
         a, b, scale = self.a, self.b, self.scale
         was = self._adapters
         if (a is not was[0] or b is not was[1] or scale is not was[2]
-                or (a.data_ptr(), b.data_ptr(), scale.data_ptr()) != self._places):
+                or (a.data_ptr(), b.data_ptr(), scale.data_ptr()) != self._places
+                or a.requires_grad or b.requires_grad or scale.requires_grad):
             self._take_adapters()
         # (Read by the library within the call.)
         self.lora.ids = _address(ids, "ids", torch.int32, (m,), dev)

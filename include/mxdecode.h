@@ -74,7 +74,7 @@ typedef struct mxmoe_router {
  *   logits      device, [tokens] rows of `experts` values, row t at
  *               logits + t * row_stride elements; type MXG_F32 or MXG_BF16,
  *               aligned to its element
- *   row_stride  elements, >= experts
+ *   row_stride  elements, from experts to 2^31
  *   bias        device or NULL: [experts] FP32
  *   tokens      rows, 1..2^24
  *   ids         device, [tokens][top_k] int32
@@ -104,7 +104,8 @@ int mxmoe_pack_weight(const uint8_t* w, const uint8_t* w_scale, int32_t experts,
 
 /* Bytes of workspace mxmoe_experts needs for these sizes; 0 on bad sizes. It
  * needs no arming, and holds nothing from one call to the next. A workspace
- * serves every call with as many pairs (tokens * top_k) or fewer. */
+ * serves every call of these experts, hidden and inter with as many pairs (tokens *
+ * top_k) or fewer. */
 size_t mxmoe_workspace_bytes(int32_t tokens, int32_t top_k, int32_t experts, int32_t hidden,
                              int32_t inter);
 
@@ -117,11 +118,12 @@ size_t mxmoe_workspace_bytes(int32_t tokens, int32_t top_k, int32_t experts, int
  * inter], and silu(v) = v / (1 + exp(-v)). An id outside 0..experts-1 adds
  * nothing; a row without any expert comes out as zeros. A row may name an
  * expert more than once. Products accumulate in FP32, h is held as the sum of
- * two BF16 values (about 17 bits; beyond BF16's range it is infinite), the sum
- * over j runs in FP32 in ascending order, and the result is rounded once to
- * BF16. A weight is the BF16 value
- * nearest to its code times its scale: exact for scale bytes 3..246 (255 is the
- * E8M0 NaN and not taken). Results are the same bits on every call.
+ * two BF16 values (to 2^-18 of itself or 2^-134; beyond BF16's range it is
+ * infinite), the sum over j runs in FP32 in ascending order, and the result is
+ * rounded once to BF16. A weight is the BF16 value nearest to its code times its
+ * scale: exact for scale bytes 3..246 (255 is the E8M0 NaN and not taken); one
+ * beyond BF16's range is infinite, and in w2 makes NaN of its column. Results are
+ * the same bits on every call.
  *
  *   x         device, [tokens, hidden] BF16, 16-B aligned
  *   ids       device, [tokens, top_k] int32
@@ -176,8 +178,9 @@ int mxgemm_lora_scratch_init(void* scratch, size_t scratch_bytes, void* stream);
  * The shared product is theirs (with BF16 x: of the quantized activation);
  * the adapter takes BF16 x as it is, MXFP8 x as the values it stands for.
  * Both products of the adapter accumulate in FP32, u = scale[i] A[i] x between
- * them is held as the sum of two BF16 values (about 17 bits), and the result is
- * added to the shared product before the one rounding to BF16.
+ * them is held as the sum of two BF16 values (to 2^-18 of itself or 2^-134; an
+ * infinity in B therefore makes NaN of its column), and the result is added to the
+ * shared product before the one rounding to BF16.
  *
  *   mb       a mailbox to publish C into (then collect it, as after
  *            mxgemm_publish), or NULL for the plain product into c_out

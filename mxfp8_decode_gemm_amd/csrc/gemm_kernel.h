@@ -374,12 +374,14 @@ __device__ __attribute__((noinline)) bool stage_rest(const uint8_t* x, const uin
 // ---- low-rank adapters (LORA) ---------------------------------------------
 // C[t] += scale[i] B[i] (A[i] x[t]), i = ids[t], beside the W stream:
 //   * u = scale A x is small (m * rank values) but reads A whole, so its dot
-//     products, cut into `parts` along K, are spread over the workgroups: the
-//     side wave of each computes its share while the workers stream W, and
-//     stores every partial as a (value, epoch) pair, as split-K does. A small N
-//     has few workgroups: up to one more per CU then joins them, all of whose
-//     waves compute u and nothing else (N=64/K=16384/m=8 rank 64 699 -> 32 us,
-//     N=1024/K=4096/m=8 rank 128 36 -> 16 us, no difference from 256 tiles on).
+//     products, cut into `parts` along K, are spread over the workgroups that run
+//     from the start: the side wave of each computes its share while the workers
+//     stream W, and stores every partial as a (value, epoch) pair, as split-K
+//     does. (Shares of workgroups that start later cost everyone u, see below:
+//     N=12288/K=4096/m=4 rank 64 663 instead of 22 us.) A small N has few
+//     workgroups: up to one more per CU then joins them, all of whose waves compute u
+//     and nothing else (N=64/K=16384/m=8 rank 64 699 -> 32 us, N=1024/K=4096/m=8
+//     rank 128 36 -> 16 us, no difference from 256 tiles on).
 //   * Each side wave then collects all pairs, sums the parts in ascending K
 //     order and leaves u in LDS as high and low BF16 parts (hi = bf16(u), lo =
 //     bf16(u - hi), together 17 bits).
@@ -598,7 +600,8 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
         // that comes too early costs a round trip behind the W stream. Without
         // the wait N=7168/K=8192/m=8/S=4 rank 16 took 15.4 us instead of 14.0,
         // N=7168/K=2048/m=4 rank 64 10.4 instead of 9.0, N=4096/K=16384/m=5/S=8
-        // rank 32 16.1 instead of 14.4; 48 was 0.5 us slower on the second.
+        // rank 32 16.1 instead of 14.4; 48 was 0.5 us slower on the second. (One W
+        // in turn, in the Infinity Cache; other shapes were not measured.)
         if (polls > 1)
           __builtin_amdgcn_s_sleep(1);
         else

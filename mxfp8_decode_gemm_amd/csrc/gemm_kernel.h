@@ -1347,14 +1347,11 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 || LORA ? 1 : 0)))
       fp |= row_down<1>(fp);
       fp |= row_down<2>(fp);
       fp |= row_down<4>(fp);
-      // With adapters c_out says so too: NaN.
-      const bool whole = fp == 0 && !ws_failed;
-      if (live && e == 0 && (whole || LORA)) {
-        uint4 raw = {pair, p1, p2, p3};
-        if (LORA && !whole) raw = uint4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
+      if (live && e == 0 && fp == 0 && !ws_failed) {
+        const uint4 raw = {pair, p1, p2, p3};
         const size_t off = ((size_t)t * N + row0 + 8 * jc) * 2;
         if (a.c_out) *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.c_out) + off) = raw;
-        if (a.slot && (whole || !LORA)) {
+        if (a.slot) {
           uint4 clean;
           clean.x = clear_negative_zero(raw.x);
           clean.y = clear_negative_zero(raw.y);
@@ -1362,6 +1359,11 @@ __global__ void __launch_bounds__(64 * (WN * WK + (SK > 1 || LORA ? 1 : 0)))
           clean.w = clear_negative_zero(raw.w);
           *reinterpret_cast<uint4*>(slot + off) = clean;
         }
+      }
+      if constexpr (LORA) {  // with adapters c_out says so: NaN
+        if (live && e == 0 && (fp != 0 || ws_failed) && a.c_out)
+          *reinterpret_cast<uint4*>(a.c_out + (size_t)t * N + row0 + 8 * jc) =
+              uint4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
       }
     }
   }

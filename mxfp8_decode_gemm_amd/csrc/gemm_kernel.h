@@ -600,8 +600,8 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
         // that comes too early costs a round trip behind the W stream. Without
         // the wait N=7168/K=8192/m=8/S=4 rank 16 took 15.4 us instead of 14.0,
         // N=7168/K=2048/m=4 rank 64 10.4 instead of 9.0, N=4096/K=16384/m=5/S=8
-        // rank 32 16.1 instead of 14.4; 48 was 0.5 us slower on the second. (One W
-        // in turn, in the Infinity Cache; other shapes were not measured.)
+        // rank 32 16.1 instead of 14.4; 48 was 0.5 us slower on the second. (With
+        // one W, in the Infinity Cache; other shapes were not measured.)
         if (polls > 1)
           __builtin_amdgcn_s_sleep(1);
         else

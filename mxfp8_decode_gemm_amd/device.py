@@ -3,7 +3,8 @@
 ``Mailbox`` owns the slot and state buffers of one mailbox; ``Workspace`` owns
 a split-K workspace; ``upload`` places MXFP8 operands in HBM; ``route``,
 ``Experts`` and ``AdaptedLinear`` are the operators whose weights are chosen
-per row, on torch tensors. Nothing here computes any part of an operator or of
+per row, on torch tensors (without a backward pass: tensors that require a
+gradient are taken under ``torch.no_grad`` only). Nothing here computes any part of an operator or of
 the mailbox protocol: every call goes through ``binding``.
 """
 
@@ -145,8 +146,6 @@ def as_u16(t: torch.Tensor) -> np.ndarray:
 # ---------------------------------------------------------------------------
 
 
-# No operator here has a backward pass: a tensor that requires a gradient is refused
-# where one would be recorded.
 # A decode step's calls take a few microseconds on the GPU, so the checks below
 # are written to cost less than that on the host.
 _raw_stream = torch._C._cuda_getCurrentRawStream

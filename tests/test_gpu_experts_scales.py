@@ -56,5 +56,6 @@ def test_scales_outside_the_exact_range(dv, s13, s2, top, e, tokens):
     x, ids, w = layer.inputs(7, tokens, 2)
     x = ((x & 0x8000) | ((((x >> 7) & 0xFF).astype(np.int32) + e).clip(1, 254) << 7).astype(
         np.uint16) | (x & 0x7F)).astype(np.uint16)
-    got = layer.check(x, ids, w)
+    with np.errstate(over="ignore"):  # (the oracle's exp of a large negative gate)
+        got = layer.check(x, ids, w)
     assert (np.abs(got) > 0).mean() > 0.5

@@ -4,8 +4,8 @@
 a split-K workspace; ``upload`` places MXFP8 operands in HBM; ``route``,
 ``Experts`` and ``AdaptedLinear`` are the operators whose weights are chosen
 per row, on torch tensors (without a backward pass: tensors that require a
-gradient are taken under ``torch.no_grad`` only). Nothing here computes any part of an operator or of
-the mailbox protocol: every call goes through ``binding``.
+gradient are taken under ``torch.no_grad`` only). Nothing here computes any part
+of an operator or of the mailbox protocol: every call goes through ``binding``.
 """
 
 from __future__ import annotations

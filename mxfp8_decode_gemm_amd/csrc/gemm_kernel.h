@@ -377,8 +377,7 @@ __device__ __attribute__((noinline)) bool stage_rest(const uint8_t* x, const uin
 //     products, cut into `parts` along K, are spread over the workgroups that run
 //     from the start: the side wave of each computes its share while the workers
 //     stream W, and stores every partial as a (value, epoch) pair, as split-K
-//     does. (Shares of workgroups that start later cost everyone u, see below:
-//     N=12288/K=4096/m=4 rank 64 663 instead of 22 us.) A small N has few
+//     does. A small N has few
 //     workgroups: up to one more per CU then joins them, all of whose waves compute u
 //     and nothing else (N=64/K=16384/m=8 rank 64 699 -> 32 us, N=1024/K=4096/m=8
 //     rank 128 36 -> 16 us, no difference from 256 tiles on).
@@ -391,12 +390,21 @@ __device__ __attribute__((noinline)) bool stage_rest(const uint8_t* x, const uin
 //     split-K slices and the waves along K, whose partials are summed anyway.
 //     A unit's product is added in the columns of its adapter's rows alone: an
 //     infinity or NaN in one adapter stays with its rows.
-// A pair not seen after kLoraPolls polls is computed by the wave that wants it,
-// to the same bits: no workgroup depends on another being resident. Workgroup 0
-// advances the epoch once every workgroup has read it; should that wait give up
-// (calls that overlap on one scratch), it marks the scratch, and from then on
-// every wave computes all of u itself until the scratch is armed again.
-constexpr uint32_t kLoraPolls = 256;
+// No workgroup depends on another being resident. Where pairs have not come after
+// kLoraFirstPolls polls (workgroups that do not run: another stream's kernel has
+// their CUs), the waves that wait deal all tasks among themselves, kLoraTicket at a
+// time by a counter in the scratch: a task so taken is a running wave's. Pairs
+// that have not come kLoraPolls polls after that are computed by the wave that wants
+// them. All to the same bits. (Without the second dealing every waiting wave
+// computed all of u: two projections of N=12288 and 11008, K=4096, m=8, rank 64
+// and 128 on two streams took 840-1830 us a pair; 94-110 now, 90 on one. With 16 first
+// polls two of 7168x2048, rank 64 took 33 instead of 23 us, with 64 the wide ones 135.)
+// Workgroup 0 advances the epoch once every workgroup has read it; should that wait
+// give up (calls that overlap on one scratch), it marks the scratch, and from
+// then on every wave computes all of u itself until the scratch is armed again.
+constexpr uint32_t kLoraFirstPolls = 32, kLoraPolls = 256;
+constexpr int kLoraTicket = 4;
+constexpr int kLoraCounter = 4;  // scratch header words 4 and 5: (tickets, epoch)
 // LDS area: [0] distinct adapters, [1 + j] adapter j, [9 + j] its rows' mask,
 // then u's high parts [m][rank], its low parts, the partials (FP32).
 constexpr int kLoraList = 80;
@@ -435,6 +443,22 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// The next ticket of this launch. The counter's upper half holds the epoch it
+// counts for: the first wave to want a ticket starts it.
+__device__ __forceinline__ int lora_ticket(uint32_t* hdr, uint32_t epoch, int lane) {
+  uint32_t t = 0;
+  if (lane == 0) {
+    uint64_t* const word = reinterpret_cast<uint64_t*>(hdr + kLoraCounter);
+    uint64_t v = ld_agent_u64(word);
+    if ((uint32_t)(v >> 32) != epoch)
+      __hip_atomic_compare_exchange_strong(word, &v, (uint64_t)epoch << 32, __ATOMIC_RELAXED,
+                                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    t = (uint32_t)__hip_atomic_fetch_add(word, (uint64_t)1, __ATOMIC_RELAXED,
+                                         __HIP_MEMORY_SCOPE_AGENT);
+  }
+  return __builtin_amdgcn_readfirstlane((int)t);
 }
 
 // The side wave of an adapter launch, from the kernel's start to its end: it
@@ -493,9 +517,10 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
 
   // ---- u's dot products --------------------------------------------------
   // Task q: the partial (row, rank, part), part fastest, in 512-value pieces.
-  // First this workgroup's tasks, into pairs, and a collection of all pairs;
-  // or all tasks, into LDS: where they are few, where the scratch is marked,
-  // and where a pair did not come.
+  // Pass 0: this workgroup's tasks, into pairs, and a collection of all pairs.
+  // Pass 1, where pairs did not come: tasks by tickets, into pairs, and a
+  // collection. Pass 2: all tasks, into LDS, where they are few, where the
+  // scratch is marked, and where pairs still did not come.
   const int ps = l.parts_log2;
   const int total = (nrows * rank) << ps;
   const int len = K >> ps;  // of a part: a multiple of 32
@@ -503,19 +528,27 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
   const uint32_t rinv = ((1u << 20) + rank - 1) / rank;  // item / rank for items < 1024
   constexpr int kPieces = 8;  // in flight
   bool before_barrier = !HELPS;
-  for (int pass = lerr != 0 || l.workers == 0 ? 1 : 0; pass < 2; ++pass) {
-    const int first =
-        pass != 0 ? 0
-                  : HELPS ? l.groups + ((int)blockIdx.x - l.groups) * (NW + 1) + wave
-                          : (int)blockIdx.x;
-    const int step = pass == 0 ? l.workers : 1;
-    int q = first < (pass == 0 ? step : 1) ? first : total, piece = 0;
+  int pass = lerr != 0 || l.workers == 0 ? 2 : 0, tickets = 0;
+  for (;;) {
+    int step = 1, q = 0, end = total;
+    if (pass == 0) {
+      step = l.workers;
+      q = HELPS ? l.groups + ((int)blockIdx.x - l.groups) * (NW + 1) + wave : (int)blockIdx.x;
+      if (q >= step) q = total;
+    } else if (pass == 1) {
+      q = kLoraTicket * lora_ticket(l.hdr, lepoch, lane);
+      end = q + kLoraTicket < total ? q + kLoraTicket : total;
+    }
+    // There may be more tickets. (No wave takes more than there are, whatever calls
+    // that overlap on one scratch make of the counter.)
+    const bool again = pass == 1 && q < total && ++tickets < kLoraMaxPairs / kLoraTicket;
+    int piece = 0;
     float sum = 0.f;
-    while (before_barrier || q < total) {
+    while (before_barrier || q < end) {
       uint4 av[kPieces], xv[kPieces];
       uint32_t sb[QX ? 1 : kPieces];
-      int ql = q < total ? q : 0, pl = piece;
-      if (q < total) {
+      int ql = q < end ? q : 0, pl = piece;
+      if (q < end) {
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
           const int item = ql >> ps;
@@ -535,7 +568,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
           }
           if (++pl == per) {
             pl = 0;
-            if (ql + step < total) ql += step;  // past the last task: it again, not used
+            if (ql + step < end) ql += step;  // past the last task: it again, not used
           }
         }
       }
@@ -552,7 +585,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
       }
       // All of one task; a helping wave, which has no LDS of its own and hardly
       // more than one task, leaves the pieces behind it out.
-      const bool one = q < total && (HELPS || per - piece >= kPieces);
+      const bool one = q < end && (HELPS || per - piece >= kPieces);
 #pragma unroll
       for (int j = 0; j < kPieces; ++j) {
         float d;
@@ -570,12 +603,12 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
       if (one) piece = HELPS && piece + kPieces > per ? per - 1 : piece + kPieces - 1;
       __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
 #pragma unroll 1
-      for (int j = one ? kPieces - 1 : 0; j < kPieces && q < total; ++j) {
+      for (int j = one ? kPieces - 1 : 0; j < kPieces && q < end; ++j) {
         if (!one && piece * 512 + 8 * lane < len) sum += stage[64 * j + lane];
         if (++piece == per) {
           sum = wave_sum63(sum);
           if (lane == 63) {
-            if (pass == 0)
+            if (pass < 2)
               st_agent_u64(l.pairs + q, (uint64_t)__float_as_uint(sum) | ((uint64_t)lepoch << 32));
             else
               part[q] = sum;
@@ -587,7 +620,9 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
       }
     }
     if (HELPS) return;
-    if (pass == 1) break;
+    if (again) continue;
+    if (pass == 2) break;
+    const uint32_t limit = pass == 0 ? kLoraFirstPolls : kLoraPolls;
     // All pairs, eight loads per lane in flight.
     constexpr int B = 8;
     bool missed = false;
@@ -595,7 +630,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
       uint64_t pv[B];
       uint32_t polls = 0;
       bool pending = true;
-      while (pending && polls++ < kLoraPolls) {
+      while (pending && polls++ < limit) {
         // The first look comes about 0.9 us after this workgroup's own stores: one
         // that comes too early costs a round trip behind the W stream. Without
         // the wait N=7168/K=8192/m=8/S=4 rank 16 took 15.4 us instead of 14.0,
@@ -623,6 +658,7 @@ __device__ __forceinline__ void lora_side(const GemmArgs& a, uint32_t* hdr, uint
         if (q0 + 64 * j + lane < total) part[q0 + 64 * j + lane] = __uint_as_float((uint32_t)pv[j]);
     }
     if (!missed) break;
+    ++pass;
   }
   __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
   for (int i0 = 0; i0 < nrows * rank; i0 += 64) {

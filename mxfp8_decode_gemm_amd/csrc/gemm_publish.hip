@@ -378,8 +378,9 @@ hipError_t launch_gemm_publish(const GemmArgs& a, const TileCfg& c, hipStream_t 
     // start, of at most 512, and where these are few, workgroups that only
     // help (up to one per CU: a small N leaves the rest of the device idle). They
     // come last in the grid. A workgroup that starts when others end can take
-    // no share: all of those would wait for it, then compute u alone (dealt to
-    // 512 where 256 ran, N=12288/K=4096/m=4 rank 64 took 663 us instead of 22).
+    // no share: those would wait for it until they deal its products out again
+    // (when each then computed all of u, N=12288/K=4096/m=4 rank 64, dealt to
+    // 512 where 256 ran, took 663 us instead of 22).
     constexpr int kShares = 512;
     const int groups = (int)grid.x, waves = (int)block.x / 64;
     const int started = c.started[a.xb != nullptr ? 1 : 0];

@@ -1,5 +1,5 @@
-"""ctypes binding of libmxgemm.so: the C ABI of include/mxgemm.h and
-include/mxdecode.h, same names.
+"""ctypes binding of libmxgemm.so: the C ABI of include/mxgemm.h,
+include/mxdecode.h and include/mxrows.h, same names.
 
 Argument marshalling only: every step of the hot path runs in the HIP
 library. Device buffers may be passed as torch tensors (their data_ptr is
@@ -20,6 +20,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MXG_LIBRARY") or os.path.join(_PKG, "lib", "libmxgemm.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mxgemm.h")
 DECODE_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mxdecode.h")
+ROWS_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "mxrows.h")
 
 OK = 0
 EINVAL = -1
@@ -53,6 +54,12 @@ ROUTE_MAX_TOP_K = 32
 MOE_MAX_EXPERTS = 1024
 MOE_MAX_PAIRS = 1024
 LORA_MAX_RANK = 128
+
+F16 = 2
+MXFP4, MXFP8 = 4, 8
+ROWS_MAX = 1 << 24
+ROWS_MAX_N = 1 << 20
+ROWS_MAX_K = 65536
 
 
 class MxgError(Exception):
@@ -111,6 +118,18 @@ class mxg_lora(ctypes.Structure):
     ]
 
 
+class mxrows_weight(ctypes.Structure):
+    _fields_ = [
+        ("w", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("format", ctypes.c_int32),
+        ("experts", ctypes.c_int32),
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("gated", ctypes.c_int32),
+    ]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -121,6 +140,7 @@ def _load() -> ctypes.CDLL:
     vp, i32, i64, sz, u32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                              ctypes.c_size_t, ctypes.c_uint32)
     mbp = ctypes.POINTER(mxg_mailbox)
+    rwp = ctypes.POINTER(mxrows_weight)
     sig = {
         "mxg_mailbox_slots_bytes": (sz, [i32, i64]),
         "mailbox_init": (ctypes.c_int, [mbp, vp, vp, i32, i32, i64, vp]),
@@ -166,6 +186,16 @@ def _load() -> ctypes.CDLL:
         "mxgemm_lora_scratch_init": (ctypes.c_int, [vp, sz, vp]),
         "mxgemm_lora": (ctypes.c_int, [mbp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, sz,
                                        ctypes.POINTER(mxg_lora), vp, sz, vp, vp]),
+        "mxfp4_quantize": (ctypes.c_int, [vp, i32, i64, i32, i32, vp, vp, vp]),
+        "mxfp4_dequantize": (ctypes.c_int, [vp, vp, i32, i32, i32, vp, vp]),
+        "mxrows_packed_weight_bytes": (sz, [i32, i32, i32, i32]),
+        "mxrows_packed_scale_bytes": (sz, [i32, i32, i32, i32]),
+        "mxrows_pack_weight": (ctypes.c_int, [i32, vp, vp, i32, i32, i32, vp, vp, vp]),
+        "mxrows_product": (ctypes.c_int, [rwp, i32, vp, vp, i32, vp, vp]),
+        "mxmoe_sort_workspace_bytes": (sz, [i32, i32, i32]),
+        "mxmoe_sort": (ctypes.c_int, [vp, i32, i32, i32, vp, sz, vp, vp, vp]),
+        "mxmoe_grouped": (ctypes.c_int, [rwp, i32, vp, vp, i32, vp, i32, i32, vp, i32, vp, vp]),
+        "mxmoe_combine": (ctypes.c_int, [vp, vp, vp, i32, i32, i32, i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -482,3 +512,60 @@ def mxgemm_lora(mb, w, w_scale, x, x_scale, x_bf16, m: int, n: int, k: int, spli
                             split_k, _ptr(workspace), workspace_bytes, ctypes.byref(lora),
                             _ptr(scratch), scratch_bytes, _ptr(c_out), _stream(stream)),
            "mxgemm_lora")
+
+
+# ---- include/mxrows.h -------------------------------------------------------
+
+
+def mxfp4_quantize(x, x_type: int, row_stride: int, rows: int, k: int, x_q, x_scale,
+                   stream=None) -> None:
+    _check(_lib.mxfp4_quantize(_ptr(x), x_type, row_stride, rows, k, _ptr(x_q), _ptr(x_scale),
+                               _stream(stream)), "mxfp4_quantize")
+
+
+def mxfp4_dequantize(x_q, x_scale, rows: int, k: int, y_type: int, y, stream=None) -> None:
+    _check(_lib.mxfp4_dequantize(_ptr(x_q), _ptr(x_scale), rows, k, y_type, _ptr(y),
+                                 _stream(stream)), "mxfp4_dequantize")
+
+
+def mxrows_packed_weight_bytes(format: int, experts: int, n: int, k: int) -> int:
+    return int(_lib.mxrows_packed_weight_bytes(format, experts, n, k))
+
+
+def mxrows_packed_scale_bytes(format: int, experts: int, n: int, k: int) -> int:
+    return int(_lib.mxrows_packed_scale_bytes(format, experts, n, k))
+
+
+def mxrows_pack_weight(format: int, w, w_scale, experts: int, n: int, k: int, w_packed, ws_packed,
+                       stream=None) -> None:
+    _check(_lib.mxrows_pack_weight(format, _ptr(w), _ptr(w_scale), experts, n, k, _ptr(w_packed),
+                                   _ptr(ws_packed), _stream(stream)), "mxrows_pack_weight")
+
+
+def mxrows_product(w: mxrows_weight, x_format: int, x, x_scale, rows: int, out,
+                   stream=None) -> None:
+    _check(_lib.mxrows_product(ctypes.byref(w), x_format, _ptr(x), _ptr(x_scale), rows, _ptr(out),
+                               _stream(stream)), "mxrows_product")
+
+
+def mxmoe_sort_workspace_bytes(tokens: int, top_k: int, experts: int) -> int:
+    return int(_lib.mxmoe_sort_workspace_bytes(tokens, top_k, experts))
+
+
+def mxmoe_sort(ids, tokens: int, top_k: int, experts: int, workspace, workspace_bytes: int, order,
+               offsets, stream=None) -> None:
+    _check(_lib.mxmoe_sort(_ptr(ids), tokens, top_k, experts, _ptr(workspace), workspace_bytes,
+                           _ptr(order), _ptr(offsets), _stream(stream)), "mxmoe_sort")
+
+
+def mxmoe_grouped(w: mxrows_weight, x_format: int, x, x_scale, x_rows: int, order, gather: int,
+                  scatter: int, offsets, rows: int, out, stream=None) -> None:
+    _check(_lib.mxmoe_grouped(ctypes.byref(w), x_format, _ptr(x), _ptr(x_scale), x_rows,
+                              _ptr(order), gather, scatter, _ptr(offsets), rows, _ptr(out),
+                              _stream(stream)), "mxmoe_grouped")
+
+
+def mxmoe_combine(y, ids, weights, tokens: int, top_k: int, experts: int, hidden: int, out,
+                  stream=None) -> None:
+    _check(_lib.mxmoe_combine(_ptr(y), _ptr(ids), _ptr(weights), tokens, top_k, experts, hidden,
+                              _ptr(out), _stream(stream)), "mxmoe_combine")

@@ -73,18 +73,6 @@ struct Plan {
   int order[N];
 };
 
-// The sum of v over this lane and the ones below.
-__device__ __forceinline__ int wave_scan(int v) {
-#define MXG_DPP_ADD(C, MASK) v += __builtin_amdgcn_update_dpp(0, v, C, MASK, 0xF, true)
-  MXG_DPP_ADD(0x111, 0xF);  // rows of 16, then across them
-  MXG_DPP_ADD(0x112, 0xF);
-  MXG_DPP_ADD(0x114, 0xF);
-  MXG_DPP_ADD(0x118, 0xF);
-  MXG_DPP_ADD(0x142, 0xA);
-  MXG_DPP_ADD(0x143, 0xC);
-#undef MXG_DPP_ADD
-  return v;
-}
 __device__ __forceinline__ int wave_prefix(int v) { return wave_scan(v) - v; }
 
 // Up to 64 pairs: one per lane, without a barrier. Every wave computes the

@@ -1,0 +1,236 @@
+// MXFP4 (gfx950): mxfp4_quantize, mxfp4_dequantize and mxrows_pack_weight of
+// include/mxrows.h.
+
+#include <hip/hip_runtime.h>
+
+#include "mx_device.h"
+#include "rows_internal.h"
+
+namespace mxg {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Eight consecutive values of a row as FP32.
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
+  if constexpr (TYPE == MXG_F32) {
+    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TYPE == MXG_BF16) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        v[2 * i] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i] & 0xFFFFu));
+        v[2 * i + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[i] >> 16));
+      }
+    }
+  }
+}
+
+// Maximum over the 4 lanes of a quad; all lanes active.
+__device__ __forceinline__ uint32_t quad_max_u32(uint32_t a) {
+  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xF, 0xF, true));
+  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x4E, 0xF, 0xF, true));
+  return a;
+}
+
+// The scale byte of a block whose largest magnitude has these FP32 bits: with
+// amax = (1 + f) 2^(E - 127), amax <= 6 2^e = 1.5 2^(e + 2) holds first at e = E -
+// 129 where f <= 1/2 and at E - 128 otherwise; never below -127. Subnormal FP32
+// magnitudes are below 6 2^-127.
+__device__ __forceinline__ uint32_t fp4_scale_byte(uint32_t amax) {
+  const int E = (int)(amax >> 23);
+  if (E == 0xFF) return 0xFFu;
+  const int s = E - 2 + ((amax & 0x7FFFFFu) > 0x400000u ? 1 : 0);
+  return (uint32_t)(s < 0 ? 0 : s);
+}
+
+// One lane per 8 values, the 4 lanes of a block side by side. Bound by HBM: 2 or
+// 4 bytes read, 17/32 written per value. v_cvt_scalef32_pk_fp4_f32 divides by
+// the scale (a power of two: exact) and rounds once, ties to even, for every
+// finite block (|v / 2^e| <= 6).
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads)
+    quantize4_kernel(const void* x, int64_t row_stride, int64_t chunks, int per_row, uint8_t* xq,
+                     uint8_t* xs) {
+  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  for (int64_t base = (int64_t)blockIdx.x * kThreads; base < chunks; base += stride) {
+    const int64_t c = base + threadIdx.x;
+    const int64_t cc = c < chunks ? c : chunks - 1;  // (chunks are a multiple of 4)
+    const int64_t row = cc / per_row;
+    float v[8];
+    load8<TYPE>(x, row * row_stride + 8 * (cc - row * per_row), v);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    const uint32_t sb = fp4_scale_byte(quad_max_u32(amax));
+    uint32_t codes = 0;
+    if (sb == 0xFFu) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        codes |= (7u | (__float_as_uint(v[i]) >> 28 & 8u)) << (4 * i);
+    } else {
+      const float s = e8m0_to_f32(sb);
+      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[0], v[1], s, 0);
+      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2], v[3], s, 1);
+      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[4], v[5], s, 2);
+      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[6], v[7], s, 3);
+    }
+    if (c < chunks) {
+      reinterpret_cast<uint32_t*>(xq)[c] = codes;
+      if ((c & 3) == 0) xs[c >> 2] = (uint8_t)sb;
+    }
+  }
+}
+
+// One lane per 8 codes. The FP32 product of an E2M1 value and a power of two is
+// exact up to FP32's range; the type's rounding follows.
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads)
+    dequantize4_kernel(const uint8_t* xq, const uint8_t* xs, int64_t chunks, void* y) {
+  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < chunks; c += stride) {
+    const uint32_t codes = reinterpret_cast<const uint32_t*>(xq)[c];
+    const uint32_t sb = xs[c >> 2];
+    const float s = sb == 0xFFu ? __uint_as_float(0x7FC00000u) : e8m0_to_f32(sb);
+    float v[8];
+#define MXG_FP4_PAIR(I)                                                            \
+  {                                                                                \
+    const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, I);        \
+    v[2 * I] = p[0] * s;                                                           \
+    v[2 * I + 1] = p[1] * s;                                                       \
+  }
+    MXG_FP4_PAIR(0)
+    MXG_FP4_PAIR(1)
+    MXG_FP4_PAIR(2)
+    MXG_FP4_PAIR(3)
+#undef MXG_FP4_PAIR
+    if constexpr (TYPE == MXG_F32) {
+      float4* q = reinterpret_cast<float4*>(y) + 2 * c;
+      q[0] = float4{v[0], v[1], v[2], v[3]};
+      q[1] = float4{v[4], v[5], v[6], v[7]};
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (TYPE == MXG_BF16)
+          w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+        else
+          w[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * i]) |
+                 (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * i + 1]) << 16;
+      }
+      reinterpret_cast<uint4*>(y)[c] = uint4{w[0], w[1], w[2], w[3]};
+    }
+  }
+}
+
+// One thread per 16 bytes of the packed codes (the layout of rows_internal.h);
+// K past the row's and rows past n are zeros.
+template <int FORMAT>
+__global__ void __launch_bounds__(kThreads)
+    pack_codes_kernel(const uint8_t* w, int n, int k, int64_t pieces, int64_t per_expert,
+                      uint4* wp) {
+  constexpr int kUnit = FORMAT == MXG_MXFP4 ? 128 : 256;  // pieces of a unit
+  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  const int kbs = (int)(2 * ((k + 255) / 256));
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < pieces; i += stride) {
+    const int64_t e = i / per_expert, u = (i - e * per_expert) / kUnit;
+    const int in = (int)(i % kUnit), lane = in & 63, q = in >> 6;
+    const int64_t rb = u / kbs;
+    const int kb = (int)(u - rb * kbs), g = lane >> 5;
+    const int64_t row = rb * 32 + (lane & 31);
+    uint4 v = {0u, 0u, 0u, 0u};
+    if (row < n && 128 * kb < k) {
+      const int64_t r = e * n + row;
+      if constexpr (FORMAT == MXG_MXFP4)  // q: the step
+        v = *reinterpret_cast<const uint4*>(w + r * (k / 2) + 64 * kb + 16 * (2 * g + q));
+      else                                // q: twice the step, the half
+        v = *reinterpret_cast<const uint4*>(w + r * k + 128 * kb +
+                                            16 * (4 * (q & 1) + 2 * (q >> 1) + g));
+    }
+    wp[i] = v;
+  }
+}
+
+// One thread per scale word.
+__global__ void __launch_bounds__(kThreads)
+    pack_scales_kernel(const uint8_t* ws, int n, int k, int64_t words, int64_t per_expert,
+                       uint32_t* wsp) {
+  const int64_t stride = (int64_t)gridDim.x * kThreads;
+  const int kp = (k + 255) / 256;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < words; i += stride) {
+    const int64_t e = i / per_expert, u = (i - e * per_expert) >> 6;
+    const int lane = (int)(i & 63), g = lane >> 5;
+    const int64_t rb = u / kp, row = rb * 32 + (lane & 31);
+    const int kb = 2 * (int)(u - rb * kp);
+    uint32_t v = 0x7F7F7F7Fu;
+    if (row < n) {
+      const uint8_t* p = ws + (e * n + row) * (k / 32) + 4 * kb + 2 * g;
+      v = p[0] | (uint32_t)p[1] << 8;
+      v |= 128 * (kb + 1) < k ? (uint32_t)p[4] << 16 | (uint32_t)p[5] << 24 : 0x7F7F0000u;
+    }
+    wsp[i] = v;
+  }
+}
+
+unsigned blocks_for(int64_t threads) {
+  const int64_t b = (threads + kThreads - 1) / kThreads;
+  return (unsigned)(b < 4096 ? b : 4096);
+}
+
+}  // namespace
+
+hipError_t launch_fp4_quantize(const void* x, int x_type, int64_t row_stride, int rows, int k,
+                               uint8_t* xq, uint8_t* xs, hipStream_t s) {
+  const int64_t chunks = (int64_t)rows * (k / 8);
+  const dim3 grid(blocks_for(chunks)), block(kThreads);
+  if (x_type == MXG_F32)
+    hipLaunchKernelGGL((quantize4_kernel<MXG_F32>), grid, block, 0, s, x, row_stride, chunks, k / 8,
+                       xq, xs);
+  else if (x_type == MXG_BF16)
+    hipLaunchKernelGGL((quantize4_kernel<MXG_BF16>), grid, block, 0, s, x, row_stride, chunks,
+                       k / 8, xq, xs);
+  else
+    hipLaunchKernelGGL((quantize4_kernel<MXG_F16>), grid, block, 0, s, x, row_stride, chunks, k / 8,
+                       xq, xs);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp4_dequantize(const uint8_t* xq, const uint8_t* xs, int rows, int k, int y_type,
+                                 void* y, hipStream_t s) {
+  const int64_t chunks = (int64_t)rows * (k / 8);
+  const dim3 grid(blocks_for(chunks)), block(kThreads);
+  if (y_type == MXG_F32)
+    hipLaunchKernelGGL((dequantize4_kernel<MXG_F32>), grid, block, 0, s, xq, xs, chunks, y);
+  else if (y_type == MXG_BF16)
+    hipLaunchKernelGGL((dequantize4_kernel<MXG_BF16>), grid, block, 0, s, xq, xs, chunks, y);
+  else
+    hipLaunchKernelGGL((dequantize4_kernel<MXG_F16>), grid, block, 0, s, xq, xs, chunks, y);
+  return hipGetLastError();
+}
+
+hipError_t launch_rows_pack(int format, const uint8_t* w, const uint8_t* ws, int experts, int n,
+                            int k, uint8_t* wp, uint8_t* wsp, hipStream_t s) {
+  const int64_t units = row_blocks(n) * kb_pairs(k) * 2;
+  const int64_t per = units * unit_bytes(format) / 16, words = units / 2 * 64;
+  const dim3 block(kThreads);
+  if (format == MXG_MXFP4)
+    hipLaunchKernelGGL((pack_codes_kernel<MXG_MXFP4>), dim3(blocks_for(per * experts)), block, 0, s,
+                       w, n, k, per * experts, per, reinterpret_cast<uint4*>(wp));
+  else
+    hipLaunchKernelGGL((pack_codes_kernel<MXG_MXFP8>), dim3(blocks_for(per * experts)), block, 0, s,
+                       w, n, k, per * experts, per, reinterpret_cast<uint4*>(wp));
+  hipLaunchKernelGGL(pack_scales_kernel, dim3(blocks_for(words * experts)), block, 0, s, ws, n, k,
+                     words * experts, words, reinterpret_cast<uint32_t*>(wsp));
+  return hipGetLastError();
+}
+
+}  // namespace mxg

@@ -55,6 +55,18 @@ template <int N>
 __device__ __forceinline__ uint32_t row_down(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x100 + N, 0xF, 0xF, true);
 }
+// The sum of v over this lane and the ones below.
+__device__ __forceinline__ int wave_scan(int v) {
+#define MXG_DPP_ADD(C, MASK) v += __builtin_amdgcn_update_dpp(0, v, C, MASK, 0xF, true)
+  MXG_DPP_ADD(0x111, 0xF);  // rows of 16, then across them
+  MXG_DPP_ADD(0x112, 0xF);
+  MXG_DPP_ADD(0x114, 0xF);
+  MXG_DPP_ADD(0x118, 0xF);
+  MXG_DPP_ADD(0x142, 0xA);
+  MXG_DPP_ADD(0x143, 0xC);
+#undef MXG_DPP_ADD
+  return v;
+}
 __device__ __forceinline__ uint32_t ld_agent_u32(const uint32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }

@@ -1,0 +1,237 @@
+// A router's (token, choice) pairs (gfx950): mxmoe_sort and mxmoe_combine of
+// include/mxrows.h.
+
+#include <hip/hip_runtime.h>
+
+#include "mx_device.h"
+#include "rows_internal.h"
+
+namespace mxg {
+namespace {
+
+// ---- sort --------------------------------------------------------------------
+//
+// A counting sort that keeps the order of equal keys, without atomics. Workgroups
+// take contiguous chunks of the pairs, waves contiguous parts of a chunk. Bucket e
+// < experts holds expert e's pairs, bucket `experts` those without one. A pair's
+// place is the sum of what lies before its bucket, of its bucket in earlier
+// workgroups, in earlier waves and in earlier pairs of its wave; the last comes
+// from matching the 64 keys of a round bit by bit.
+//
+// One workgroup does it in one launch. More of them count first, in a launch of
+// their own (a row of the workspace each), and each then sums the rows itself:
+// with at most kMostGroups of them that costs less than a third launch.
+
+constexpr int kSortWaves = 16;
+constexpr int kSortThreads = 64 * kSortWaves;
+constexpr int kBuckets = MXG_MOE_MAX_EXPERTS + 2;  // an even number
+constexpr int kChunk = 4096;                       // pairs of a workgroup, or more:
+constexpr int kMostGroups = 256;
+
+struct SortArgs {
+  const int32_t* ids;
+  int32_t pairs, experts, chunk, groups, stride;  // stride: words of a workspace row
+  uint32_t* counts;                               // [groups][stride]
+  int32_t *order, *offsets;
+};
+
+// The lanes whose key equals this lane's; bits: of the largest key.
+__device__ __forceinline__ uint64_t same_key(int key, int bits) {
+  uint64_t m = ~0ull;
+  for (int i = 0; i < bits; ++i) {
+    const bool one = key >> i & 1;
+    const uint64_t b = __ballot(one);
+    m &= one ? b : ~b;
+  }
+  return m;
+}
+
+// The bucket of pair p, or one past all of them for p >= end.
+__device__ __forceinline__ int bucket_of(const SortArgs& a, int p, int end) {
+  if (p >= end) return a.experts + 1;
+  const int e = a.ids[p];
+  return (unsigned)e < (unsigned)a.experts ? e : a.experts;
+}
+
+// Counts of a wave's pairs into its row of LDS.
+__device__ __forceinline__ void count_part(const SortArgs& a, int p0, int p1, int bits, int lane,
+                                           uint32_t* row) {
+  for (int p = p0; p < p1; p += 64) {
+    const int b = bucket_of(a, p + lane, p1);
+    const uint64_t m = same_key(b, bits);
+    if (b <= a.experts && __builtin_ctzll(m) == lane) row[b] += (uint32_t)__popcll(m);
+    __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
+  }
+}
+
+template <bool ONE>  // one workgroup: counts and places in this launch
+__global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a, int count_only) {
+  __shared__ uint32_t part[kSortWaves][kBuckets];
+  __shared__ uint32_t sums[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int used = a.experts + 1;
+  const int bits = 32 - __builtin_clz(a.experts + 1);
+  const int c0 = blockIdx.x * a.chunk, c1 = min(c0 + a.chunk, a.pairs);
+  const int per = ((c1 - c0 + kSortThreads - 1) / kSortThreads) * 64;  // pairs of a wave
+  const int p0 = min(c0 + wave * per, c1), p1 = min(p0 + per, c1);
+  for (int i = lane; i < used; i += 64) part[wave][i] = 0;
+  __builtin_amdgcn_wave_barrier();
+  count_part(a, p0, p1, bits, lane, part[wave]);
+  __syncthreads();
+
+  if (!ONE && count_only) {
+    for (int b = tid; b < a.stride; b += kSortThreads) {
+      uint32_t n = 0;
+      if (b < used)
+        for (int w = 0; w < kSortWaves; ++w) n += part[w][b];
+      a.counts[(int64_t)blockIdx.x * a.stride + b] = n;
+    }
+    return;
+  }
+
+  // Buckets 2 tid and 2 tid + 1: all their pairs, and those of earlier workgroups.
+  uint32_t all[2] = {0, 0}, before[2] = {0, 0};
+  if (2 * tid < used) {
+    if (ONE) {
+      for (int w = 0; w < kSortWaves; ++w) {
+        all[0] += part[w][2 * tid];
+        if (2 * tid + 1 < used) all[1] += part[w][2 * tid + 1];
+      }
+    } else {
+      const uint2* row = reinterpret_cast<const uint2*>(a.counts) + tid;
+#pragma unroll 8
+      for (int k = 0; k < a.groups; ++k) {
+        const uint2 n = row[(int64_t)k * (a.stride / 2)];
+        all[0] += n.x;
+        all[1] += n.y;
+        before[0] += k < (int)blockIdx.x ? n.x : 0;
+        before[1] += k < (int)blockIdx.x ? n.y : 0;
+      }
+    }
+  }
+  const int mine = (int)(all[0] + all[1]);
+  const int upto = wave_scan(mine);
+  if (lane == 63) sums[wave] = (uint32_t)upto;
+  __syncthreads();
+  uint32_t at = (uint32_t)(upto - mine);
+  for (int w = 0; w < wave; ++w) at += sums[w];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int b = 2 * tid + j;
+    if (b >= used) break;
+    if (blockIdx.x == 0) a.offsets[b] = (int32_t)at;
+    uint32_t to = at + before[j];
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t n = part[w][b];
+      part[w][b] = to;
+      to += n;
+    }
+    at += all[j];
+  }
+  __syncthreads();
+  uint32_t* row = part[wave];
+  for (int p = p0; p < p1; p += 64) {
+    const int b = bucket_of(a, p + lane, p1);
+    const uint64_t m = same_key(b, bits);
+    const uint32_t first = b <= a.experts ? row[b] : 0;
+    const uint32_t below = (uint32_t)__popcll(m & ((1ull << lane) - 1));
+    __builtin_amdgcn_wave_barrier();
+    if (b <= a.experts) {
+      a.order[first + below] = p + lane;
+      if (below == 0) row[b] = first + (uint32_t)__popcll(m);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+void sort_shape(int64_t pairs, int experts, int* chunk, int* groups, int* stride) {
+  int64_t c = kChunk;
+  if ((pairs + c - 1) / c > kMostGroups) c = (pairs + kMostGroups - 1) / kMostGroups;
+  *chunk = (int)c;
+  *groups = (int)((pairs + c - 1) / c);
+  *stride = (experts + 2) / 2 * 2;
+}
+
+// ---- combine ------------------------------------------------------------------
+//
+// Bound by the read of y. One thread per 8 columns of a token; a token's ids and
+// weights are the same for the whole workgroup (scalar loads), eight rows' loads in
+// flight.
+
+constexpr int kCombineThreads = 128;
+
+__global__ void __launch_bounds__(kCombineThreads)
+    combine_pairs_kernel(const uint4* y, const int32_t* ids, const float* weights, int top_k,
+                         int experts, int cols, uint4* out) {
+  const int c = blockIdx.y * kCombineThreads + threadIdx.x;
+  const int64_t t = blockIdx.x;
+  if (c >= cols) return;
+  float s[8] = {};
+  constexpr int B = 8;
+  for (int j0 = 0; j0 < top_k; j0 += B) {
+    uint4 v[B];
+    float w[B];
+    bool there[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const int64_t p = t * top_k + min(j0 + j, top_k - 1);
+      const int e = ids[p];
+      w[j] = weights[p];
+      there[j] = j0 + j < top_k && (unsigned)e < (unsigned)experts;
+      if (there[j]) v[j] = y[p * cols + c];
+    }
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      if (!there[j]) continue;
+      const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[2 * i] = fmaf(w[j], __uint_as_float(u[i] << 16), s[2 * i]);
+        s[2 * i + 1] = fmaf(w[j], __uint_as_float(u[i] & 0xFFFF0000u), s[2 * i + 1]);
+      }
+    }
+  }
+  out[t * cols + c] = uint4{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]), bf16_pair(s[4], s[5]),
+                            bf16_pair(s[6], s[7])};
+}
+
+}  // namespace
+
+size_t sort_workspace(int64_t pairs, int experts) {
+  int chunk, groups, stride;
+  sort_shape(pairs, experts, &chunk, &groups, &stride);
+  return ((size_t)groups * stride * 4 + 15) / 16 * 16;
+}
+
+hipError_t launch_sort(const int32_t* ids, int pairs, int experts, void* workspace, int32_t* order,
+                       int32_t* offsets, hipStream_t s) {
+  SortArgs a;
+  a.ids = ids;
+  a.pairs = pairs;
+  a.experts = experts;
+  sort_shape(pairs, experts, &a.chunk, &a.groups, &a.stride);
+  a.counts = static_cast<uint32_t*>(workspace);
+  a.order = order;
+  a.offsets = offsets;
+  const dim3 grid((unsigned)a.groups), block(kSortThreads);
+  if (a.groups == 1) {
+    hipLaunchKernelGGL((sort_pairs_kernel<true>), grid, block, 0, s, a, 0);
+  } else {
+    hipLaunchKernelGGL((sort_pairs_kernel<false>), grid, block, 0, s, a, 1);
+    hipLaunchKernelGGL((sort_pairs_kernel<false>), grid, block, 0, s, a, 0);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const uint16_t* y, const int32_t* ids, const float* weights, int tokens,
+                          int top_k, int experts, int hidden, uint16_t* out, hipStream_t s) {
+  const int cols = hidden / 8;
+  const dim3 grid((unsigned)tokens, (unsigned)((cols + kCombineThreads - 1) / kCombineThreads));
+  hipLaunchKernelGGL(combine_pairs_kernel, grid, dim3(kCombineThreads), 0, s,
+                     reinterpret_cast<const uint4*>(y), ids, weights, top_k, experts, cols,
+                     reinterpret_cast<uint4*>(out));
+  return hipGetLastError();
+}
+
+}  // namespace mxg

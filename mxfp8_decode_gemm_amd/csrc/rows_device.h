@@ -1,0 +1,106 @@
+// Device helpers shared by the kernels of the products of any number of rows
+// (gfx950): the scaled MFMA by format, where a tile of rows lies, the epilogue's
+// arithmetic.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mx_device.h"
+#include "rows_internal.h"
+
+namespace mxg {
+namespace {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// The operand of one MFMA step: 32 rows by 64 values of K, 16 or 32 bytes a lane.
+template <int FORMAT>
+struct Piece {
+  v4u lo, hi;
+};
+template <>
+struct Piece<MXG_MXFP4> {
+  v4u lo;
+};
+
+template <int FORMAT>
+__device__ __forceinline__ v8i operand(const Piece<FORMAT>& p) {
+  if constexpr (FORMAT == MXG_MXFP4)
+    return v8i{(int)p.lo.x, (int)p.lo.y, (int)p.lo.z, (int)p.lo.w, 0, 0, 0, 0};
+  else
+    return v8i{(int)p.lo.x, (int)p.lo.y, (int)p.lo.z, (int)p.lo.w,
+               (int)p.hi.x, (int)p.hi.y, (int)p.hi.z, (int)p.hi.w};
+}
+
+// acc[n][t] += sum over 64 K of W[n] x[t], byte BW of sw and byte BX of sx the
+// lane's scales. acc: lane l holds column t = l % 32 and the rows n = 8 (i / 4) +
+// 4 (l / 32) + i % 4.
+template <int FW, int FX, int BW, int BX>
+__device__ __forceinline__ v16f product(const Piece<FW>& w, uint32_t sw, const Piece<FX>& x,
+                                        uint32_t sx, v16f acc) {
+  constexpr int CW = FW == MXG_MXFP4 ? 4 : 0, CX = FX == MXG_MXFP4 ? 4 : 0;  // E2M1, e4m3
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand<FW>(w), operand<FX>(x), acc, CW,
+                                                         CX, BW, (int)sw, BX, (int)sx);
+}
+
+__device__ __forceinline__ float gated(float gate, float up) {
+  return gate / (1.f + expf(-gate)) * up;
+}
+
+// A tile of sorted rows of one expert: rows r0 .. r1 - 1; expert -1: no such tile.
+struct RowTile {
+  int expert, r0, r1;
+};
+
+// Tile number `at` of TILE rows, counted over the experts in turn. Every lane of
+// the wave takes part; the result is wave-uniform.
+template <int TILE>
+__device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int experts, int rows, int at,
+                                             int lane) {
+  const int per = (experts + 63) >> 6;  // consecutive experts of a lane
+  int own = 0;
+  for (int j = 0; j < per; ++j) {
+    const int e = lane * per + j;
+    if (e < experts) {
+      const int a = max(offsets[e], 0), b = min(offsets[e + 1], rows);
+      own += b > a ? (b - a + TILE - 1) / TILE : 0;
+    }
+  }
+  const int end = wave_scan(own);
+  const uint64_t past = __ballot(end > at);
+  if (past == 0) return RowTile{-1, 0, 0};
+  const int who = __builtin_ctzll(past);
+  int left = at - __builtin_amdgcn_readlane(end - own, who);
+  for (int j = 0; j < per; ++j) {
+    const int e = who * per + j;
+    if (e >= experts) break;
+    const int a = max(__builtin_amdgcn_readfirstlane(offsets[e]), 0);
+    const int b = min(__builtin_amdgcn_readfirstlane(offsets[e + 1]), rows);
+    const int tiles = b > a ? (b - a + TILE - 1) / TILE : 0;
+    if (left < tiles) {
+      const int r0 = a + left * TILE;
+      return RowTile{e, r0, min(r0 + TILE, b)};
+    }
+    left -= tiles;
+  }
+  return RowTile{-1, 0, 0};
+}
+
+// The row of x that sorted row i takes.
+__device__ __forceinline__ int source_row(const RowsArgs& a, int i) {
+  if (a.gather == 0) return i;
+  const int r = (int)((uint32_t)a.order[i] / (uint32_t)a.gather);
+  return min(max(r, 0), a.x_rows - 1);
+}
+
+// The row of out that sorted row i goes to, -1 for none.
+__device__ __forceinline__ int target_row(const RowsArgs& a, int i) {
+  if (!a.scatter) return i;
+  const int r = a.order[i];
+  return (unsigned)r < (unsigned)a.rows ? r : -1;
+}
+
+}  // namespace
+}  // namespace mxg

@@ -1,0 +1,169 @@
+// Products of few rows (gfx950): mxrows_product and mxmoe_grouped of
+// include/mxrows.h where a weight is read for at most a few dozen rows.
+//
+// What bounds it: the read of the active weights. A workgroup takes 32 rows of W
+// (gated: 32 gate rows and the up rows beside them) and up to 32 RX rows of x; its
+// waves divide K, so that even a narrow weight has many waves reading. Each wave
+// streams its units (1 KiB contiguous per instruction) and the rows' codes (in
+// L2) into registers and feeds both to the scaled MFMA as they are; the partial
+// tiles meet in LDS and are summed in ascending K order.
+
+#include <hip/hip_runtime.h>
+
+#include "rows_device.h"
+
+namespace mxg {
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kThreads = 64 * kWaves;
+
+template <int FW, int FX, int RX, bool GATED>
+__global__ void __launch_bounds__(kThreads) rows_stream_kernel(RowsArgs a) {
+  constexpr int RW = GATED ? 2 : 1;
+  constexpr int kTile = 32 * RX;
+  __shared__ float red[kWaves][RW][RX][16][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r32 = lane & 31, g = lane >> 5;
+  const int ct = blockIdx.y, rt = blockIdx.x;
+  RowTile tile{0, rt * kTile, min(rt * kTile + kTile, a.rows)};
+  if (a.offsets) {
+    tile = find_tile<kTile>(a.offsets, a.experts, a.rows, rt, lane);
+    if (tile.expert < 0) return;
+  }
+
+  // This lane's rows of x (those past the end: the last one again).
+  const int x_row = FX == MXG_MXFP4 ? a.k / 2 : a.k;
+  const uint8_t* xr[RX];
+  const uint8_t* xsr[RX];
+#pragma unroll
+  for (int t = 0; t < RX; ++t) {
+    const int64_t row = source_row(a, min(tile.r0 + 32 * t + r32, tile.r1 - 1));
+    xr[t] = a.x + row * x_row;
+    xsr[t] = a.xs + row * (a.k >> 5);
+  }
+  constexpr int kUnit = FW == MXG_MXFP4 ? 2048 : 4096;
+  const uint8_t* w[RW];
+  const uint32_t* ws[RW];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    const int rb = ct + i * (a.nb / 2);
+    w[i] = a.w + tile.expert * a.w_bytes + (int64_t)rb * a.kp * 2 * kUnit + 16 * lane;
+    ws[i] = reinterpret_cast<const uint32_t*>(a.ws + tile.expert * a.ws_bytes) +
+            (int64_t)rb * a.kp * 64 + lane;
+  }
+
+  v16f acc[RW][RX];
+#pragma unroll
+  for (int i = 0; i < RW; ++i)
+#pragma unroll
+    for (int t = 0; t < RX; ++t)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][t][q] = 0.f;
+
+  const int kbs = a.k >> 7;
+  const int p0 = wave * a.kp / kWaves, p1 = (wave + 1) * a.kp / kWaves;
+  for (int p = p0; p < p1; ++p) {
+    uint32_t sw[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) sw[i] = ws[i][p * 64];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // A kb past K (the packed codes there are zeros): the row's last one again.
+      const int kb = min(2 * p + h, kbs - 1);
+      uint32_t sx[RX];
+      Piece<FX> xp[RX][2];
+      Piece<FW> wp[RW][2];
+#pragma unroll
+      for (int t = 0; t < RX; ++t) {
+        sx[t] = *reinterpret_cast<const uint16_t*>(xsr[t] + 4 * kb + 2 * g);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if constexpr (FX == MXG_MXFP4) {
+            xp[t][s].lo =
+                *reinterpret_cast<const v4u*>(xr[t] + 64 * kb + 16 * (2 * g + s));
+          } else {
+            xp[t][s].lo = *reinterpret_cast<const v4u*>(xr[t] + 128 * kb + 16 * (2 * s + g));
+            xp[t][s].hi = *reinterpret_cast<const v4u*>(xr[t] + 128 * kb + 64 + 16 * (2 * s + g));
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        const uint8_t* u = w[i] + (int64_t)(2 * p + h) * kUnit;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if constexpr (FW == MXG_MXFP4) {
+            wp[i][s].lo = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(u + 1024 * s));
+          } else {
+            wp[i][s].lo = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(u + 2048 * s));
+            wp[i][s].hi =
+                __builtin_nontemporal_load(reinterpret_cast<const v4u*>(u + 2048 * s + 1024));
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int t = 0; t < RX; ++t) {
+          const uint32_t s = h ? sw[i] >> 16 : sw[i];
+          acc[i][t] = product<FW, FX, 0, 0>(wp[i][0], s, xp[t][0], sx[t], acc[i][t]);
+          acc[i][t] = product<FW, FX, 1, 1>(wp[i][1], s, xp[t][1], sx[t], acc[i][t]);
+        }
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < RW; ++i)
+#pragma unroll
+    for (int t = 0; t < RX; ++t)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) red[wave][i][t][q][lane] = acc[i][t][q];
+  __syncthreads();
+  // One thread per row and pair of neighbouring columns.
+  for (int u = tid; u < kTile * 16; u += kThreads) {
+    const int row = u % kTile, c = 2 * (u / kTile);
+    const int t = row >> 5, l = (row & 31) + 32 * ((c >> 2) & 1), q = 4 * (c >> 3) + (c & 3);
+    if (tile.r0 + row >= tile.r1 || 32 * ct + c >= a.out_n) continue;
+    const int to = target_row(a, tile.r0 + row);
+    if (to < 0) continue;
+    float v[RW][2] = {};
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) {
+        v[i][0] += red[k][i][t][q][l];
+        v[i][1] += red[k][i][t][q + 1][l];
+      }
+    if constexpr (GATED) {
+      v[0][0] = gated(v[0][0], v[1][0]);
+      v[0][1] = gated(v[0][1], v[1][1]);
+    }
+    *reinterpret_cast<uint32_t*>(a.out + (int64_t)to * a.out_n + 32 * ct + c) =
+        bf16_pair(v[0][0], v[0][1]);
+  }
+}
+
+template <int FW, int FX, int RX>
+hipError_t launch(const RowsArgs& a, hipStream_t s) {
+  const int64_t tile = 32 * RX;
+  const int64_t most = a.rows / tile + (a.experts < a.rows ? a.experts : a.rows);
+  const dim3 grid((unsigned)(a.offsets ? most : (a.rows + tile - 1) / tile),
+                  (unsigned)(a.gated ? a.nb / 2 : a.nb));
+  if (a.gated)
+    hipLaunchKernelGGL((rows_stream_kernel<FW, FX, RX, true>), grid, dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((rows_stream_kernel<FW, FX, RX, false>), grid, dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rows(const RowsArgs& a, int w_format, int x_format, hipStream_t s) {
+  if (x_format == MXG_MXFP4) return launch<MXG_MXFP4, MXG_MXFP4, 1>(a, s);
+  if (w_format == MXG_MXFP4) return launch<MXG_MXFP4, MXG_MXFP8, 1>(a, s);
+  return launch<MXG_MXFP8, MXG_MXFP8, 1>(a, s);
+}
+
+}  // namespace mxg

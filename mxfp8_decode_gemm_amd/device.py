@@ -488,3 +488,295 @@ class AdaptedLinear:
                 x_scale: torch.Tensor = None, c_out: torch.Tensor = None, stream=None) -> None:
         """The same into the mailbox (then collect it)."""
         self._call(mailbox.mb, x, ids, x_scale, c_out, stream)
+
+
+# ---------------------------------------------------------------------------
+# products of any number of rows (include/mxrows.h)
+# ---------------------------------------------------------------------------
+
+_TYPES = {torch.float32: mx.F32, torch.bfloat16: mx.BF16, torch.float16: mx.F16}
+_FORMATS = {"mxfp4": mx.MXFP4, "mxfp8": mx.MXFP8}
+
+
+def _matrix(t, name: str) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name}: a device tensor of two dimensions is needed")
+    return t
+
+
+def quantize4(x: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor = None,
+              stream=None):
+    """One mxfp4_quantize call on [rows, k] float32, bfloat16 or float16 values (rows of
+    any stride that is a multiple of 16 bytes): (codes uint8 [rows, k/2], scales uint8
+    [rows, k/32])."""
+    kind = _TYPES.get(_matrix(x, "x").dtype)
+    if kind is None:
+        raise ValueError(f"x: {x.dtype} instead of one of {sorted(map(str, _TYPES))}")
+    if x.requires_grad:
+        _refuse_gradient(x, "x")
+    rows, k = x.shape
+    row_stride, step = x.stride()
+    if step != 1:
+        raise ValueError("x: a row's values have to be contiguous")
+    if rows == 1:
+        row_stride = k
+    dev = x.device
+    handle = _on(dev, stream)
+    if codes is None:
+        codes = _fresh(x, (rows, k // 2), torch.uint8, stream)
+    else:
+        _address(codes, "codes", torch.uint8, (rows, k // 2), dev)
+    if scales is None:
+        scales = _fresh(x, (rows, k // 32), torch.uint8, stream)
+    else:
+        _address(scales, "scales", torch.uint8, (rows, k // 32), dev)
+    code = _lib.mxfp4_quantize(x.data_ptr(), kind, row_stride, rows, k, codes.data_ptr(),
+                               scales.data_ptr(), handle)
+    if code:
+        mx._check(code, "mxfp4_quantize")
+    if stream is not None:
+        _lend(stream, x, codes, scales)
+    return codes, scales
+
+
+def dequantize4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
+                out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """One mxfp4_dequantize call: the values of codes [rows, k/2] and scales [rows, k/32]
+    as float32, bfloat16 or float16 [rows, k]."""
+    rows, half = _matrix(codes, "codes").shape
+    dev = codes.device
+    handle = _on(dev, stream)
+    pc = _address(codes, "codes", torch.uint8, (rows, half), dev)
+    ps = _address(scales, "scales", torch.uint8, (rows, half // 16), dev)
+    if dtype not in _TYPES:
+        raise ValueError(f"dtype: {dtype} instead of one of {sorted(map(str, _TYPES))}")
+    if out is None:
+        out = _fresh(codes, (rows, 2 * half), dtype, stream)
+    else:
+        _address(out, "out", dtype, (rows, 2 * half), dev)
+    code = _lib.mxfp4_dequantize(pc, ps, rows, 2 * half, _TYPES[dtype], out.data_ptr(), handle)
+    if code:
+        mx._check(code, "mxfp4_dequantize")
+    if stream is not None:
+        _lend(stream, codes, scales, out)
+    return out
+
+
+def quantize8(x: torch.Tensor, stream=None):
+    """One mxfp8_quantize call on contiguous [rows, k] bfloat16 values: (codes uint8 [rows,
+    k], scales uint8 [rows, k/32])."""
+    rows, k = _matrix(x, "x").shape
+    handle = _on(x.device, stream)
+    px = _address(x, "x", torch.bfloat16, (rows, k), x.device)
+    codes = _fresh(x, (rows, k), torch.uint8, stream)
+    scales = _fresh(x, (rows, k // 32), torch.uint8, stream)
+    code = _lib.mxfp8_quantize(px, rows, k, codes.data_ptr(), scales.data_ptr(), handle)
+    if code:
+        mx._check(code, "mxfp8_quantize")
+    if stream is not None:
+        _lend(stream, x, codes, scales)
+    return codes, scales
+
+
+_QUANTIZE = {mx.MXFP4: quantize4, mx.MXFP8: quantize8}
+
+
+class _RowsWeight:
+    """A stack of weights packed once for the products of any number of rows:
+    uint8 codes [experts, n, k/2] (MXFP4) or [experts, n, k] (MXFP8) and scale bytes
+    [experts, n, k/32], which say the format. Its tensors may be written, not
+    replaced; calls keep nothing in it, so they may run at once."""
+
+    w = property(lambda self: self._packed[0])
+    w_scale = property(lambda self: self._packed[1])
+
+    def _pack(self, w, w_scale, gated, activation, stream) -> None:
+        _refuse(w, "w", torch.uint8, (None, None, None), None)
+        e, n, width = w.shape
+        dev = self.device = w.device
+        blocks = w_scale.shape[-1] if isinstance(w_scale, torch.Tensor) and w_scale.dim() else 0
+        self.format = mx.MXFP4 if width == 16 * blocks else mx.MXFP8
+        self.experts, self.n, self.k = e, n, 32 * blocks
+        if width not in (16 * blocks, 32 * blocks):
+            raise ValueError("w: 16 (MXFP4) or 32 (MXFP8) bytes for each scale byte are needed")
+        _refuse(w_scale, "w_scale", torch.uint8, (e, n, blocks), dev)
+        nbytes = mx.mxrows_packed_weight_bytes(self.format, e, n, self.k)
+        if nbytes == 0 or (gated and n % 64):
+            raise ValueError("w: sizes that the products of any number of rows do not take")
+        if activation is not None and activation not in _FORMATS:
+            raise ValueError(f"activation: {activation!r} instead of one of {sorted(_FORMATS)}")
+        self.activation = _FORMATS[activation] if activation else self.format
+        if (self.format, self.activation) == (mx.MXFP8, mx.MXFP4):
+            raise ValueError("activation: an MXFP8 weight takes MXFP8 activations")
+        self.gated, self.out_n = bool(gated), n // 2 if gated else n
+        handle = _on(dev, stream)
+        wp = _fresh(w, (nbytes,), torch.uint8, stream)
+        wsp = _fresh(w, (mx.mxrows_packed_scale_bytes(self.format, e, n, self.k),), torch.uint8,
+                     stream)
+        mx.mxrows_pack_weight(self.format, w, w_scale, e, n, self.k, wp, wsp, handle)
+        _lend(stream, w, w_scale)
+        self._packed = wp, wsp
+        self._weight = mx.mxrows_weight(wp.data_ptr(), wsp.data_ptr(), self.format, e, n, self.k,
+                                        int(self.gated))
+        self._home = _Home(handle, self._packed)
+
+    def _codes(self, x, x_scale, rows, stream):
+        """x as codes: (format, codes, scales, their addresses); BF16 x is quantized."""
+        dev, k = self.device, self.k
+        if x_scale is None:
+            _address(x, "x", torch.bfloat16, (rows, k), dev)
+            x, x_scale = _QUANTIZE[self.activation](x, stream=stream)
+            return self.activation, x, x_scale, x.data_ptr(), x_scale.data_ptr()
+        kind = mx.MXFP4 if 2 * x.shape[1] == k else mx.MXFP8
+        px = _address(x, "x", torch.uint8, (rows, k // 2 if kind == mx.MXFP4 else k), dev)
+        return kind, x, x_scale, px, _address(x_scale, "x_scale", torch.uint8, (rows, k // 32), dev)
+
+
+class Linear(_RowsWeight):
+    """A projection [n, k] in MXFP4 or MXFP8, packed once, for any number of rows
+    (``Operands`` and ``publish`` are the projection of at most 8). gated: the rows are
+    [gate; up], and a result is silu(gate) * up of them. activation ("mxfp4" or "mxfp8",
+    by default the weight's format): what BF16 rows are quantized to."""
+
+    def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, gated: bool = False,
+                 activation: str = None, stream=None) -> None:
+        _refuse(w, "w", torch.uint8, (None, None), None)
+        if not isinstance(w_scale, torch.Tensor) or w_scale.dim() != 2:
+            raise ValueError("w_scale: a device tensor [n, k/32] is needed")
+        self._pack(w.unsqueeze(0), w_scale.unsqueeze(0), gated, activation, stream)
+
+    def __call__(self, x: torch.Tensor, x_scale: torch.Tensor = None, out: torch.Tensor = None,
+                 stream=None) -> torch.Tensor:
+        """One mxrows_product call: uint8 codes [rows, k/2] or [rows, k] with x_scale
+        [rows, k/32], or BF16 [rows, k], quantized first; BF16 [rows, n] (gated: n/2)."""
+        dev = self.device
+        handle = _on(dev, stream)
+        rows = _matrix(x, "x").shape[0]
+        kind, x, x_scale, px, ps = self._codes(x, x_scale, rows, stream)
+        if out is None:
+            out = _fresh(x, (rows, self.out_n), torch.bfloat16, stream)
+        else:
+            _address(out, "out", torch.bfloat16, (rows, self.out_n), dev)
+        self._home.used(handle, stream)
+        code = _lib.mxrows_product(self._weight, kind, px, ps, rows, out.data_ptr(), handle)
+        if code:
+            mx._check(code, "mxrows_product")
+        if stream is not None:
+            _lend(stream, x, x_scale, out)
+        return out
+
+
+def sort_pairs(ids: torch.Tensor, experts: int, order: torch.Tensor = None,
+               offsets: torch.Tensor = None, stream=None):
+    """One mxmoe_sort call on a router's ids [tokens, top_k]: (order int32 [tokens *
+    top_k], offsets int32 [experts + 1])."""
+    tokens, top_k = _matrix(ids, "ids").shape
+    dev = ids.device
+    handle = _on(dev, stream)
+    pi = _address(ids, "ids", torch.int32, (tokens, top_k), dev)
+    if order is None:
+        order = _fresh(ids, (tokens * top_k,), torch.int32, stream)
+    else:
+        _address(order, "order", torch.int32, (tokens * top_k,), dev)
+    if offsets is None:
+        offsets = _fresh(ids, (max(experts, 0) + 1,), torch.int32, stream)
+    else:
+        _address(offsets, "offsets", torch.int32, (experts + 1,), dev)
+    nbytes = _lib.mxmoe_sort_workspace_bytes(tokens, top_k, experts)
+    workspace = _fresh(ids, (nbytes,), torch.uint8, stream)
+    code = _lib.mxmoe_sort(pi, tokens, top_k, experts, workspace.data_ptr(), nbytes,
+                           order.data_ptr(), offsets.data_ptr(), handle)
+    if code:
+        mx._check(code, "mxmoe_sort")
+    if stream is not None:
+        _lend(stream, ids, order, offsets, workspace)
+    return order, offsets
+
+
+class GroupedLinear(_RowsWeight):
+    """Every expert's projection in MXFP4 or MXFP8 (uint8 codes [experts, n, k/2] or
+    [experts, n, k], scale bytes [experts, n, k/32]), packed once, on the rows of its
+    pairs. gated and activation: as ``Linear``."""
+
+    def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, gated: bool = False,
+                 activation: str = None, stream=None) -> None:
+        self._pack(w, w_scale, gated, activation, stream)
+
+    def __call__(self, x: torch.Tensor, x_scale, offsets: torch.Tensor,
+                 order: torch.Tensor = None, gather: int = 0, scatter: bool = False,
+                 out: torch.Tensor = None, stream=None) -> torch.Tensor:
+        """One mxmoe_grouped call. x, x_scale: codes, or BF16 rows and None; offsets and
+        order: of ``sort_pairs``. gather (a router's top_k): sorted row i is x[order[i] //
+        gather], else x[i]; scatter: its result is row order[i], else row i. BF16 [rows, n]
+        (gated: n/2), a row for each of order's, or of x without one; rows without an
+        expert are left as they were."""
+        dev = self.device
+        handle = _on(dev, stream)
+        x_rows = _matrix(x, "x").shape[0]
+        rows = x_rows
+        po = None
+        if order is not None:
+            rows = order.numel() if isinstance(order, torch.Tensor) else None
+            po = _address(order, "order", torch.int32, (rows,), dev)
+        poff = _address(offsets, "offsets", torch.int32, (self.experts + 1,), dev)
+        kind, x, x_scale, px, ps = self._codes(x, x_scale, x_rows, stream)
+        if out is None:
+            out = _fresh(x, (rows, self.out_n), torch.bfloat16, stream)
+        else:
+            _address(out, "out", torch.bfloat16, (rows, self.out_n), dev)
+        self._home.used(handle, stream)
+        code = _lib.mxmoe_grouped(self._weight, kind, px, ps, x_rows, po, gather, int(scatter),
+                                  poff, rows, out.data_ptr(), handle)
+        if code:
+            mx._check(code, "mxmoe_grouped")
+        if stream is not None:
+            _lend(stream, x, x_scale, offsets, order, out)
+        return out
+
+
+def combine(y: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, experts: int,
+            out: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """One mxmoe_combine call: BF16 y [tokens * top_k, hidden] (a row for each pair), ids
+    and weights as ``route`` returns them; BF16 [tokens, hidden]."""
+    tokens, top_k = _matrix(ids, "ids").shape
+    hidden = _matrix(y, "y").shape[1]
+    dev = y.device
+    handle = _on(dev, stream)
+    py = _address(y, "y", torch.bfloat16, (tokens * top_k, hidden), dev)
+    pi = _address(ids, "ids", torch.int32, (tokens, top_k), dev)
+    pw = _address(weights, "weights", torch.float32, (tokens, top_k), dev)
+    if out is None:
+        out = _fresh(y, (tokens, hidden), torch.bfloat16, stream)
+    else:
+        _address(out, "out", torch.bfloat16, (tokens, hidden), dev)
+    code = _lib.mxmoe_combine(py, pi, pw, tokens, top_k, experts, hidden, out.data_ptr(), handle)
+    if code:
+        mx._check(code, "mxmoe_combine")
+    if stream is not None:
+        _lend(stream, y, ids, weights, out)
+    return out
+
+
+class PromptExperts:
+    """The experts of one layer on a prompt's rows, where ``Experts`` takes a decode step's
+    (at most 1024 pairs): w13 [experts, 2 inter, hidden] (gate rows, then up rows) and w2
+    [experts, hidden, inter] in MXFP4 or MXFP8, packed once. activation ("mxfp4" or "mxfp8",
+    by default each weight's format): what the rows of both products are quantized to."""
+
+    def __init__(self, w13: torch.Tensor, w13_scale: torch.Tensor, w2: torch.Tensor,
+                 w2_scale: torch.Tensor, activation: str = None, stream=None) -> None:
+        self.up = GroupedLinear(w13, w13_scale, gated=True, activation=activation, stream=stream)
+        self.down = GroupedLinear(w2, w2_scale, activation=activation, stream=stream)
+        self.experts, self.hidden, self.inter = self.up.experts, self.up.k, self.up.out_n
+        if (self.down.experts, self.down.n, self.down.k) != (self.experts, self.hidden, self.inter):
+            raise ValueError("w2: [experts, hidden, inter] of w13 is needed")
+
+    def __call__(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                 out: torch.Tensor = None, stream=None) -> torch.Tensor:
+        """BF16 x [tokens, hidden], ids and weights as ``route`` returns them; BF16 [tokens,
+        hidden]: sort_pairs, both products with the rows quantized before each, combine."""
+        tokens, top_k = _matrix(ids, "ids").shape
+        order, offsets = sort_pairs(ids, self.experts, stream=stream)
+        h = self.up(x, None, offsets, order, gather=top_k, stream=stream)
+        y = self.down(h, None, offsets, order, scatter=True, stream=stream)
+        return combine(y, ids, weights, self.experts, out, stream)

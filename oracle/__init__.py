@@ -21,6 +21,9 @@ computes, in float64 / exact integer arithmetic:
                    word publish and fused all-gather; the all-reduce collect.
 * ``decode``    -- the operators whose weights are chosen per row: expert
                    routing, the chosen experts' products, low-rank adapters.
+* ``rows``      -- MXFP4 and the products of any number of rows: the quantizer,
+                   dense and grouped products, a router's pairs sorted and
+                   combined.
 * ``tolerance`` -- the BF16 acceptance bound used by every parity test.
 
 Page citations in this package name the four API pages by module:
@@ -30,6 +33,6 @@ Page citations in this package name the four API pages by module:
   "sync page"            = vllm.models.deepseek_v41.amd.mono.common.sync
 """
 
-from . import codecs, decode, gemm, mailbox, quant, tolerance  # noqa: F401
+from . import codecs, decode, gemm, mailbox, quant, rows, tolerance  # noqa: F401
 
-__all__ = ["codecs", "decode", "gemm", "mailbox", "quant", "tolerance"]
+__all__ = ["codecs", "decode", "gemm", "mailbox", "quant", "rows", "tolerance"]

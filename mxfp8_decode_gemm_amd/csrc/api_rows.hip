@@ -66,7 +66,10 @@ int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const 
   a.out_n = w->gated ? w->n / 2 : w->n;
   a.nb = (int32_t)row_blocks(w->n);
   a.kp = (int32_t)kb_pairs(w->k);
-  return hip_code(launch_rows(a, w->format, x_format, static_cast<hipStream_t>(stream)));
+  const int32_t groups = offsets ? (w->experts < rows ? w->experts : rows) : 1;
+  const bool many = rows / groups > 32;
+  return hip_code((many ? launch_rows_tile : launch_rows_stream)(a, w->format, x_format,
+                                                                static_cast<hipStream_t>(stream)));
 }
 }  // namespace
 

@@ -37,7 +37,8 @@ struct RowsArgs {
   int32_t out_n, nb, kp;  // columns of out; row blocks of a weight, pairs of kb
 };
 
-hipError_t launch_rows(const RowsArgs& a, int w_format, int x_format, hipStream_t s);
+hipError_t launch_rows_stream(const RowsArgs& a, int w_format, int x_format, hipStream_t s);
+hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, hipStream_t s);
 
 hipError_t launch_rows_pack(int format, const uint8_t* w, const uint8_t* ws, int experts, int n,
                             int k, uint8_t* wp, uint8_t* wsp, hipStream_t s);

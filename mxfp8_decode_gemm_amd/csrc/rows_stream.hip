@@ -160,7 +160,7 @@ hipError_t launch(const RowsArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_rows(const RowsArgs& a, int w_format, int x_format, hipStream_t s) {
+hipError_t launch_rows_stream(const RowsArgs& a, int w_format, int x_format, hipStream_t s) {
   if (x_format == MXG_MXFP4) return launch<MXG_MXFP4, MXG_MXFP4, 1>(a, s);
   if (w_format == MXG_MXFP4) return launch<MXG_MXFP4, MXG_MXFP8, 1>(a, s);
   return launch<MXG_MXFP8, MXG_MXFP8, 1>(a, s);

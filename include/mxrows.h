@@ -99,6 +99,11 @@ typedef struct mxrows_weight {
 
 /* ---- the product ----------------------------------------------------------- */
 
+/* Bytes of workspace mxrows_product needs for `rows` rows of this weight (its
+ * pointers are not looked at): 0 where K is not divided among workgroups, at most
+ * 32 MiB, and 0 on bad sizes. It needs no arming. */
+size_t mxrows_workspace_bytes(const mxrows_weight* w, int32_t x_format, int32_t rows);
+
 /* out[t] = W x[t] for t in 0..rows-1, rounded once to BF16; gated:
  * silu(Wg x[t]) * (Wu x[t]), formed in FP32 before the rounding. A row is out_n =
  * n (gated: n/2) values.
@@ -118,11 +123,14 @@ typedef struct mxrows_weight {
  *   x_format  MXG_MXFP4 (with an MXFP4 weight) or MXG_MXFP8
  *   x, x_scale  device, [rows, k] codes (16-B aligned), [rows, k/32] (4-B)
  *   rows      1..MXG_ROWS_MAX
+ *   workspace device, at least mxrows_workspace_bytes(), 16-B aligned; one call at
+ *             a time per workspace. NULL where that is 0
  *   out       device, [rows, out_n] BF16, 16-B aligned
- * Errors: MXG_EINVAL, MXG_EALIGN, MXG_EUNSUPPORTED (an MXFP8 weight on MXFP4 x),
- * MXG_EHIP. */
+ * Errors: MXG_EINVAL, MXG_EALIGN, MXG_EWORKSPACE, MXG_EUNSUPPORTED (an MXFP8
+ * weight on MXFP4 x), MXG_EHIP. */
 int mxrows_product(const mxrows_weight* w, int32_t x_format, const uint8_t* x,
-                   const uint8_t* x_scale, int32_t rows, uint16_t* out, void* stream);
+                   const uint8_t* x_scale, int32_t rows, void* workspace, size_t workspace_bytes,
+                   uint16_t* out, void* stream);
 
 /* ---- a router's pairs by expert -------------------------------------------- */
 
@@ -167,7 +175,7 @@ int mxmoe_sort(const int32_t* ids, int32_t tokens, int32_t top_k, int32_t expert
  *   offsets   device, [experts + 1] int32, ascending, within 0..rows; parts
  *             outside are passed over
  *   rows      1..MXG_ROWS_MAX: rows of order and of out
- * Other arguments and errors as mxrows_product. */
+ * Other arguments and errors as mxrows_product (no workspace). */
 int mxmoe_grouped(const mxrows_weight* w, int32_t x_format, const uint8_t* x,
                   const uint8_t* x_scale, int32_t x_rows, const int32_t* order, int32_t gather,
                   int32_t scatter, const int32_t* offsets, int32_t rows, uint16_t* out,

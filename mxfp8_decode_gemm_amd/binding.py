@@ -191,7 +191,8 @@ def _load() -> ctypes.CDLL:
         "mxrows_packed_weight_bytes": (sz, [i32, i32, i32, i32]),
         "mxrows_packed_scale_bytes": (sz, [i32, i32, i32, i32]),
         "mxrows_pack_weight": (ctypes.c_int, [i32, vp, vp, i32, i32, i32, vp, vp, vp]),
-        "mxrows_product": (ctypes.c_int, [rwp, i32, vp, vp, i32, vp, vp]),
+        "mxrows_workspace_bytes": (sz, [rwp, i32, i32]),
+        "mxrows_product": (ctypes.c_int, [rwp, i32, vp, vp, i32, vp, sz, vp, vp]),
         "mxmoe_sort_workspace_bytes": (sz, [i32, i32, i32]),
         "mxmoe_sort": (ctypes.c_int, [vp, i32, i32, i32, vp, sz, vp, vp, vp]),
         "mxmoe_grouped": (ctypes.c_int, [rwp, i32, vp, vp, i32, vp, i32, i32, vp, i32, vp, vp]),
@@ -542,10 +543,15 @@ def mxrows_pack_weight(format: int, w, w_scale, experts: int, n: int, k: int, w_
                                    _ptr(ws_packed), _stream(stream)), "mxrows_pack_weight")
 
 
-def mxrows_product(w: mxrows_weight, x_format: int, x, x_scale, rows: int, out,
-                   stream=None) -> None:
-    _check(_lib.mxrows_product(ctypes.byref(w), x_format, _ptr(x), _ptr(x_scale), rows, _ptr(out),
-                               _stream(stream)), "mxrows_product")
+def mxrows_workspace_bytes(w: mxrows_weight, x_format: int, rows: int) -> int:
+    return int(_lib.mxrows_workspace_bytes(ctypes.byref(w), x_format, rows))
+
+
+def mxrows_product(w: mxrows_weight, x_format: int, x, x_scale, rows: int, workspace,
+                   workspace_bytes: int, out, stream=None) -> None:
+    _check(_lib.mxrows_product(ctypes.byref(w), x_format, _ptr(x), _ptr(x_scale), rows,
+                               _ptr(workspace), workspace_bytes, _ptr(out), _stream(stream)),
+           "mxrows_product")
 
 
 def mxmoe_sort_workspace_bytes(tokens: int, top_k: int, experts: int) -> int:

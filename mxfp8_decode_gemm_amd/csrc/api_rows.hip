@@ -32,27 +32,15 @@ int64_t packed_expert_bytes(int32_t format, int32_t n, int32_t k) {
 }
 int64_t packed_expert_scale_bytes(int32_t n, int32_t k) { return row_blocks(n) * kb_pairs(k) * 256; }
 
-int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const uint8_t* x_scale,
-              int32_t x_rows, const int32_t* order, int32_t gather, int32_t scatter,
-              const int32_t* offsets, int32_t rows, uint16_t* out, void* stream) {
-  if (!w || !w->w || !w->scale || !x || !x_scale || !out) return MXG_EINVAL;
-  if (!weight_ok(w->format, w->experts, w->n, w->k) || !format_ok(x_format)) return MXG_EINVAL;
-  if ((w->gated != 0 && w->gated != 1) || (w->gated && w->n % 64)) return MXG_EINVAL;
-  if (!rows_ok(rows)) return MXG_EINVAL;
-  if (!aligned(w->w, 16) || !aligned(w->scale, 16) || !aligned(x, 16) || !aligned(x_scale, 4) ||
-      !aligned(out, 16))
-    return MXG_EALIGN;
-  if (w->format == MXG_MXFP8 && x_format == MXG_MXFP4) return MXG_EUNSUPPORTED;
-  const int64_t x_row = x_format == MXG_MXFP4 ? w->k / 2 : w->k;
-  if (gather && (int64_t)x_rows * x_row >= ((int64_t)1 << 32)) return MXG_EUNSUPPORTED;
+bool weight_shape_ok(const mxrows_weight* w) {
+  return w && weight_ok(w->format, w->experts, w->n, w->k) && (w->gated == 0 || w->gated == 1) &&
+         !(w->gated && w->n % 64);
+}
+
+// Sizes of a call (the pointers are the caller's to set).
+RowsArgs rows_args(const mxrows_weight* w, int32_t rows, const int32_t* offsets) {
   RowsArgs a = {};
-  a.w = w->w;
-  a.ws = w->scale;
-  a.x = x;
-  a.xs = x_scale;
-  a.out = out;
   a.offsets = offsets;
-  a.order = order;
   a.w_bytes = packed_expert_bytes(w->format, w->n, w->k);
   a.ws_bytes = packed_expert_scale_bytes(w->n, w->k);
   a.experts = w->experts;
@@ -60,16 +48,49 @@ int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const 
   a.k = w->k;
   a.gated = w->gated;
   a.rows = rows;
-  a.x_rows = x_rows;
-  a.gather = gather;
-  a.scatter = scatter;
   a.out_n = w->gated ? w->n / 2 : w->n;
   a.nb = (int32_t)row_blocks(w->n);
   a.kp = (int32_t)kb_pairs(w->k);
-  const int32_t groups = offsets ? (w->experts < rows ? w->experts : rows) : 1;
-  const bool many = rows / groups > 32;
-  return hip_code((many ? launch_rows_tile : launch_rows_stream)(a, w->format, x_format,
-                                                                static_cast<hipStream_t>(stream)));
+  return a;
+}
+
+// Whether a call runs by tiles of many rows or streams W for few.
+bool by_tiles(const RowsArgs& a) {
+  const int32_t groups = a.offsets ? (a.experts < a.rows ? a.experts : a.rows) : 1;
+  return a.rows / groups > 32;
+}
+
+int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const uint8_t* x_scale,
+              int32_t x_rows, const int32_t* order, int32_t gather, int32_t scatter,
+              const int32_t* offsets, int32_t rows, void* workspace, size_t workspace_bytes,
+              uint16_t* out, void* stream) {
+  if (!w || !w->w || !w->scale || !x || !x_scale || !out) return MXG_EINVAL;
+  if (!weight_shape_ok(w) || !format_ok(x_format) || !rows_ok(rows)) return MXG_EINVAL;
+  if (!aligned(w->w, 16) || !aligned(w->scale, 16) || !aligned(x, 16) || !aligned(x_scale, 4) ||
+      !aligned(out, 16))
+    return MXG_EALIGN;
+  if (w->format == MXG_MXFP8 && x_format == MXG_MXFP4) return MXG_EUNSUPPORTED;
+  const int64_t x_row = x_format == MXG_MXFP4 ? w->k / 2 : w->k;
+  if (gather && (int64_t)x_rows * x_row >= ((int64_t)1 << 32)) return MXG_EUNSUPPORTED;
+  RowsArgs a = rows_args(w, rows, offsets);
+  a.w = w->w;
+  a.ws = w->scale;
+  a.x = x;
+  a.xs = x_scale;
+  a.out = out;
+  a.order = order;
+  a.x_rows = x_rows;
+  a.gather = gather;
+  a.scatter = scatter;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!by_tiles(a)) return hip_code(launch_rows_stream(a, w->format, x_format, s));
+  const size_t needed = rows_tile_workspace(a);
+  if (needed) {
+    if (!workspace || workspace_bytes < needed) return MXG_EWORKSPACE;
+    if (!aligned(workspace, 16)) return MXG_EALIGN;
+    a.partial = static_cast<float*>(workspace);
+  }
+  return hip_code(launch_rows_tile(a, w->format, x_format, s));
 }
 }  // namespace
 
@@ -116,10 +137,18 @@ int mxrows_pack_weight(int32_t format, const uint8_t* w, const uint8_t* w_scale,
                                    static_cast<hipStream_t>(stream)));
 }
 
+size_t mxrows_workspace_bytes(const mxrows_weight* w, int32_t x_format, int32_t rows) {
+  if (!weight_shape_ok(w) || w->experts != 1 || !format_ok(x_format) || !rows_ok(rows)) return 0;
+  const RowsArgs a = rows_args(w, rows, nullptr);
+  return by_tiles(a) ? rows_tile_workspace(a) : 0;
+}
+
 int mxrows_product(const mxrows_weight* w, int32_t x_format, const uint8_t* x,
-                   const uint8_t* x_scale, int32_t rows, uint16_t* out, void* stream) {
+                   const uint8_t* x_scale, int32_t rows, void* workspace, size_t workspace_bytes,
+                   uint16_t* out, void* stream) {
   if (w && w->experts != 1) return MXG_EINVAL;
-  return rows_call(w, x_format, x, x_scale, rows, nullptr, 0, 0, nullptr, rows, out, stream);
+  return rows_call(w, x_format, x, x_scale, rows, nullptr, 0, 0, nullptr, rows, workspace,
+                   workspace_bytes, out, stream);
 }
 
 size_t mxmoe_sort_workspace_bytes(int32_t tokens, int32_t top_k, int32_t experts) {
@@ -147,8 +176,8 @@ int mxmoe_grouped(const mxrows_weight* w, int32_t x_format, const uint8_t* x,
   if ((gather || scatter) && !order) return MXG_EINVAL;
   if (!rows_ok(x_rows) || (!gather && x_rows != rows)) return MXG_EINVAL;
   if (!aligned(offsets, 4) || !aligned(order, 4)) return MXG_EALIGN;
-  return rows_call(w, x_format, x, x_scale, x_rows, order, gather, scatter, offsets, rows, out,
-                   stream);
+  return rows_call(w, x_format, x, x_scale, x_rows, order, gather, scatter, offsets, rows, nullptr,
+                   0, out, stream);
 }
 
 int mxmoe_combine(const uint16_t* y, const int32_t* ids, const float* weights, int32_t tokens,

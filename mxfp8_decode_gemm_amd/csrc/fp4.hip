@@ -151,10 +151,9 @@ __global__ void __launch_bounds__(kThreads)
     if (row < n && 128 * kb < k) {
       const int64_t r = e * n + row;
       if constexpr (FORMAT == MXG_MXFP4)  // q: the step
-        v = *reinterpret_cast<const uint4*>(w + r * (k / 2) + 64 * kb + 16 * (2 * g + q));
+        v = *reinterpret_cast<const uint4*>(w + r * (k / 2) + 64 * kb + 16 * (2 * q + g));
       else                                // q: twice the step, the half
-        v = *reinterpret_cast<const uint4*>(w + r * k + 128 * kb +
-                                            16 * (4 * (q & 1) + 2 * (q >> 1) + g));
+        v = *reinterpret_cast<const uint4*>(w + r * k + 128 * kb + 16 * (2 * q + g));
     }
     wp[i] = v;
   }
@@ -173,9 +172,9 @@ __global__ void __launch_bounds__(kThreads)
     const int kb = 2 * (int)(u - rb * kp);
     uint32_t v = 0x7F7F7F7Fu;
     if (row < n) {
-      const uint8_t* p = ws + (e * n + row) * (k / 32) + 4 * kb + 2 * g;
-      v = p[0] | (uint32_t)p[1] << 8;
-      v |= 128 * (kb + 1) < k ? (uint32_t)p[4] << 16 | (uint32_t)p[5] << 24 : 0x7F7F0000u;
+      const uint8_t* p = ws + (e * n + row) * (k / 32) + 4 * kb + g;
+      v = p[0] | (uint32_t)p[2] << 8;
+      v |= 128 * (kb + 1) < k ? (uint32_t)p[4] << 16 | (uint32_t)p[6] << 24 : 0x7F7F0000u;
     }
     wsp[i] = v;
   }

@@ -49,6 +49,25 @@ __device__ __forceinline__ float gated(float gate, float up) {
   return gate / (1.f + expf(-gate)) * up;
 }
 
+// Eight neighbouring columns 8 (q + g) .. of lane l's row l % 32 of a product, in
+// BF16: a lane's four meet those of the lane 32 on. q: 0 or 2.
+__device__ __forceinline__ uint4 eight_columns(const v16f& v, int q) {
+  const auto lo = __builtin_amdgcn_permlane32_swap(bf16_pair(v[4 * q], v[4 * q + 1]),
+                                                   bf16_pair(v[4 * q + 4], v[4 * q + 5]), false,
+                                                   false);
+  const auto hi = __builtin_amdgcn_permlane32_swap(bf16_pair(v[4 * q + 2], v[4 * q + 3]),
+                                                   bf16_pair(v[4 * q + 6], v[4 * q + 7]), false,
+                                                   false);
+  return uint4{lo[0], hi[0], lo[1], hi[1]};
+}
+
+__device__ __forceinline__ v16f gated(const v16f& gate, const v16f& up) {
+  v16f h;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) h[q] = gated(gate[q], up[q]);
+  return h;
+}
+
 // A tile of sorted rows of one expert: rows r0 .. r1 - 1; expert -1: no such tile.
 struct RowTile {
   int expert, r0, r1;

@@ -13,15 +13,13 @@ namespace mxg {
 // The packed weight (mxrows_pack_weight). Unit (rb, kb): 32 rows by 128 values
 // of K, two MFMA steps s of 64. Lane l of a wave holds row l % 32; with g = l /
 // 32, step s takes from it
-//   MXFP4: the 16 bytes of K block 2 g + s               at s 1024 + 16 l
-//   MXFP8: the 16-byte pieces 2 s + g and 4 + 2 s + g    at s 2048 + 16 l, + 1024
-// (of the unit's four 32-wide blocks, eight pieces). Either way lane group g's
-// scale of step s is that of block 2 g + s: x, row-major, is read in the same
-// order, and its scale bytes of both steps lie side by side. Which K an
-// instruction sums first is all that this choice changes.
-// Units lie [row block][kb], 2048 or 4096 bytes each; scales [row block][kb / 2]
-// [lane] as words: bytes 2 (kb % 2) + s. kb runs to an even number, rows to 32:
-// zeros with scale byte 127.
+//   MXFP4: the 16 bytes of K block 2 s + g               at s 1024 + 16 l
+//   MXFP8: the 16-byte pieces 4 s + g and 4 s + 2 + g    at s 2048 + 16 l, + 1024
+// (of the unit's four 32-wide blocks, eight pieces), and as its scale that of
+// block 2 s + g either way: the instruction's own order of K. Units lie [row
+// block][kb], 2048 or 4096 bytes each; scales [row block][kb / 2][lane] as words,
+// byte 2 (kb % 2) + s. kb runs to an even number, rows to 32: zeros with scale
+// byte 127.
 inline int unit_bytes(int format) { return format == MXG_MXFP4 ? 2048 : 4096; }
 inline int64_t row_blocks(int64_t n) { return (n + 31) / 32; }
 inline int64_t kb_pairs(int64_t k) { return (k + 255) / 256; }
@@ -35,9 +33,12 @@ struct RowsArgs {
   int64_t w_bytes, ws_bytes;  // of one expert
   int32_t experts, n, k, gated, rows, x_rows, gather, scatter;
   int32_t out_n, nb, kp;  // columns of out; row blocks of a weight, pairs of kb
+  float* partial;         // workspace of a split K (one weight, all rows), or null
 };
 
 hipError_t launch_rows_stream(const RowsArgs& a, int w_format, int x_format, hipStream_t s);
+// Bytes of a.partial that launch_rows_tile wants for these sizes (0: none).
+size_t rows_tile_workspace(const RowsArgs& a);
 hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, hipStream_t s);
 
 hipError_t launch_rows_pack(int format, const uint8_t* w, const uint8_t* ws, int experts, int n,

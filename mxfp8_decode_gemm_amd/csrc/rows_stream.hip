@@ -77,15 +77,15 @@ __global__ void __launch_bounds__(kThreads) rows_stream_kernel(RowsArgs a) {
       Piece<FW> wp[RW][2];
 #pragma unroll
       for (int t = 0; t < RX; ++t) {
-        sx[t] = *reinterpret_cast<const uint16_t*>(xsr[t] + 4 * kb + 2 * g);
+        sx[t] = *reinterpret_cast<const uint32_t*>(xsr[t] + 4 * kb) >> (8 * g);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if constexpr (FX == MXG_MXFP4) {
             xp[t][s].lo =
-                *reinterpret_cast<const v4u*>(xr[t] + 64 * kb + 16 * (2 * g + s));
+                *reinterpret_cast<const v4u*>(xr[t] + 64 * kb + 16 * (2 * s + g));
           } else {
-            xp[t][s].lo = *reinterpret_cast<const v4u*>(xr[t] + 128 * kb + 16 * (2 * s + g));
-            xp[t][s].hi = *reinterpret_cast<const v4u*>(xr[t] + 128 * kb + 64 + 16 * (2 * s + g));
+            xp[t][s].lo = *reinterpret_cast<const v4u*>(xr[t] + 128 * kb + 64 * s + 16 * g);
+            xp[t][s].hi = *reinterpret_cast<const v4u*>(xr[t] + 128 * kb + 64 * s + 32 + 16 * g);
           }
         }
       }
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) rows_stream_kernel(RowsArgs a) {
         for (int t = 0; t < RX; ++t) {
           const uint32_t s = h ? sw[i] >> 16 : sw[i];
           acc[i][t] = product<FW, FX, 0, 0>(wp[i][0], s, xp[t][0], sx[t], acc[i][t]);
-          acc[i][t] = product<FW, FX, 1, 1>(wp[i][1], s, xp[t][1], sx[t], acc[i][t]);
+          acc[i][t] = product<FW, FX, 1, 2>(wp[i][1], s, xp[t][1], sx[t], acc[i][t]);
         }
     }
   }

@@ -39,25 +39,42 @@ __device__ __forceinline__ void copy_words(uint32_t to, const uint8_t* base, uin
                ::"s"(to), "v"(off), "s"(base) : "memory");
 }
 
+// A tile's geometry. A stage is 64 bytes of each row of x (128 values in MXFP4: two
+// MFMA steps, 64 in MXFP8: one) with the same K of W; a ring of four of them lies in
+// LDS. Scales come by pairs of kb (four steps), two pairs.
+// RX: the most 32-row blocks of x of a wave; a tile of fewer rows runs with fewer.
 template <int FW, int FX, int RW, int RX, int WW, int WX>
 struct Tile {
   static constexpr int kWaves = WW * WX, kThreads = 64 * kWaves;
-  static constexpr int kKb = FX == MXG_MXFP4 ? 2 : 1;  // of a stage: 128 bytes of a row of x
-  static constexpr int kSteps = 2 * kKb;
-  static constexpr int kWBlock = (FW == MXG_MXFP4 ? 2048 : 4096) * kKb, kXBlock = 4096;
+  static constexpr int kPer = FX == MXG_MXFP4 ? 2 : 1;  // steps of a stage
+  static constexpr int kStages = 4 / kPer;              // of a pair
+  static constexpr int kStepW = FW == MXG_MXFP4 ? 1024 : 2048;
+  static constexpr int kWBlock = kStepW * kPer, kXBlock = 2048;
   static constexpr int kNW = WW * RW, kNX = WX * RX;  // blocks of 32 rows
   static constexpr int kRows = 32 * kNX;
-  static constexpr int kX = kNW * kWBlock, kWS = kX + kNX * kXBlock, kXS = kWS + kNW * 256;
-  static constexpr int kStage = kXS + kNX * 256;
-  static constexpr int kCopyW = kNW / kWaves, kCopyX = kNX / kWaves;
-  static_assert(kNW % kWaves == 0 && kNX % kWaves == 0 && RW % 2 == 0, "");
+  static constexpr int kX = kNW * kWBlock, kSlot = kX + kNX * kXBlock, kRing = 4;
+  static constexpr int kScales = kRing * kSlot, kPair = (kNW + kNX) * 256;
+  static constexpr int kLds = kScales + 2 * kPair;
+  static constexpr int kCopyW = kNW / kWaves;  // blocks that a wave copies
+  static constexpr bool kSplits = RW == 2;     // K may be divided among workgroups
+  // What the epilogue lays out at once: 32 rows of a wave's columns, a row's 16 bytes
+  // longer than they are, so that eight rows meet no bank twice.
+  static constexpr int kOutRow = 64 * RW + 16;
+  static_assert(kNW % kWaves == 0 && RW % 2 == 0 && kLds <= 160 * 1024, "");
+  static_assert(kWaves * 32 * kOutRow <= kScales, "");
 };
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
 
 template <int FW, int FX, int RW, int RX, int WW, int WX>
 __global__ void __launch_bounds__(64 * WW * WX) __attribute__((amdgpu_waves_per_eu(1)))
-rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles) {
+rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
   using T = Tile<FW, FX, RW, RX, WW, WX>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * T::kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ww = wave % WW, wx = wave / WW;
@@ -67,18 +84,25 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles) {
   constexpr int kRun = 32;
   const int bid = blockIdx.x;
   const int at = bid / (8 * kRun) * (8 * kRun) + (bid & 7) * kRun + (bid >> 3) % kRun;
-  if (at >= row_tiles * col_tiles) return;
+  if (at >= row_tiles * col_tiles * split) return;
+  // The tiles of one part of K after the other: those of a run share its rows of x.
+  const int tiles = row_tiles * col_tiles;
+  const int part = at / tiles, number = at - part * tiles;
   // Eight row tiles side by side down the columns, so that a run shares W and x.
   constexpr int kGroup = 8;
-  const int group = at / (kGroup * col_tiles);
+  const int group = number / (kGroup * col_tiles);
   const int high = min(kGroup, row_tiles - group * kGroup);
-  const int in = at - group * kGroup * col_tiles;
+  const int in = number - group * kGroup * col_tiles;
   const int ct = in / high, rt = group * kGroup + in % high;
   RowTile tile{0, rt * T::kRows, min(rt * T::kRows + T::kRows, a.rows)};
   if (a.offsets) {
     tile = find_tile<T::kRows>(a.offsets, a.experts, a.rows, rt, lane);
     if (tile.expert < 0) return;
   }
+
+  // Its pairs of kb.
+  const int pair0 = part * a.kp / split, kp = (part + 1) * a.kp / split - pair0;
+  const int kbs = min((a.k >> 7) - 2 * pair0, 2 * kp);
 
   // ---- what this wave copies ---------------------------------------------------
   const uint8_t *wb[T::kCopyW], *wsb[T::kCopyW];
@@ -90,245 +114,413 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles) {
       rb = min(ct * (T::kNW / 2) + (b >> 1), a.nb / 2 - 1) + (b & 1) * (a.nb / 2);
     else
       rb = min(ct * T::kNW + b, a.nb - 1);
-    wb[i] = a.w + tile.expert * a.w_bytes + (int64_t)rb * a.kp * (FW == MXG_MXFP4 ? 4096 : 8192);
-    wsb[i] = a.ws + tile.expert * a.ws_bytes + (int64_t)rb * a.kp * 256;
+    const int64_t unit = (int64_t)rb * a.kp + pair0;
+    wb[i] = a.w + tile.expert * a.w_bytes + unit * (4 * T::kStepW);
+    wsb[i] = a.ws + tile.expert * a.ws_bytes + unit * 256;
   }
-  // Rows of x: a wave instruction takes 8 rows of 128 bytes, lane l the piece
-  // (l ^ l / 8) % 8 of row l / 8, so that a row r holds piece p at p ^ r % 8 and the
-  // lanes of an operand read meet no bank twice. Rows past the end: the last one.
   const int x_row = FX == MXG_MXFP4 ? a.k >> 1 : a.k;
   const int64_t base_row = a.gather ? 0 : tile.r0;
-  const uint8_t* xb = a.x + base_row * x_row;
-  const uint8_t* xsb = a.xs + base_row * (a.k >> 5);
-  const int piece = (lane ^ (lane >> 3)) & 7;
-  uint32_t xo[T::kCopyX][4], xso[T::kCopyX];
-#pragma unroll
-  for (int i = 0; i < T::kCopyX; ++i) {
-    const int b = wave + i * T::kWaves;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = min(tile.r0 + 32 * b + 8 * j + (lane >> 3), tile.r1 - 1);
-      xo[i][j] = (uint32_t)(source_row(a, row) - base_row) * (uint32_t)x_row + 16 * piece;
-    }
-    const int row = min(tile.r0 + 32 * b + r32, tile.r1 - 1);
-    xso[i] = (uint32_t)(source_row(a, row) - base_row) * (uint32_t)(a.k >> 5) +
-             (FX == MXG_MXFP4 ? 4 * g : 0);
-  }
+  const uint8_t* xb = a.x + base_row * x_row + (int64_t)pair0 * (256 / T::kPer);
+  const uint8_t* xsb = a.xs + base_row * (a.k >> 5) + (int64_t)pair0 * 8;
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  const int kbs = a.k >> 7;
-  const int stages = (kbs + T::kKb - 1) / T::kKb;
+  const int last = kbs * (2 / T::kPer) - 1;  // the last stage that x has
 
-  // Copies of a stage, numbered: kCopyW times (codes, scales), kCopyX times (four of
-  // codes, scales).
-  constexpr int kCopies = 2 * T::kCopyW + 5 * T::kCopyX;
-  auto copy = [&](int n, int stage, uint32_t buf) __attribute__((always_inline)) {
-    const uint32_t to = base + buf;
-    if (n < 2 * T::kCopyW) {
-      const int i = n >> 1, b = wave + i * T::kWaves;
-      if ((n & 1) == 0)
-        copy_kib<T::kWBlock / 1024>(to + b * T::kWBlock, wb[i] + (int64_t)stage * T::kWBlock,
-                                    16 * lane);
-      else
-        copy_words(to + T::kWS + b * 256, wsb[i] + (stage * T::kKb >> 1) * 256, 4 * lane);
-    } else {
-      const int i = (n - 2 * T::kCopyW) / 5, j = (n - 2 * T::kCopyW) % 5, b = wave + i * T::kWaves;
-      // A stage of which K has only the first half: its codes again (W's are zero).
-      const bool half = FX == MXG_MXFP4 && 2 * stage + 2 > kbs;
-      if (j < 4)
-        copy_kib<1>(to + T::kX + b * T::kXBlock + 1024 * j, xb + (int64_t)stage * 128,
-                    xo[i][j < 4 ? j : 0] - (half ? 16 * (piece & 4) : 0));
-      else
-        copy_words(to + T::kXS + b * 256, xsb + stage * 4 * T::kKb, xso[i] - (half ? 4 * g : 0));
+  // The tile with NX blocks of 32 rows of x for each wave: block t of wave column wx
+  // is the tile's block t * WX + wx, so that a tile of few rows is shared evenly.
+  auto run = [&](auto blocks) __attribute__((always_inline)) {
+    constexpr int NX = decltype(blocks)::value;
+    constexpr int kBlocks = WX * NX;
+    constexpr int kCopyX = (kBlocks + T::kWaves - 1) / T::kWaves;
+    // Instructions of a wave's copies of a stage and of a pair's scales, which go with
+    // the pair's first stage.
+    constexpr int kWLoads = T::kWBlock / 1024;
+    constexpr int kCopies = T::kCopyW + 2 * kCopyX;
+    constexpr auto loads = [](int stage) constexpr {
+      return T::kCopyW * kWLoads + 2 * kCopyX + (stage % T::kStages == 0 ? T::kCopyW + kCopyX : 0);
+    };
+
+    // Rows of x: a wave instruction takes 64 bytes of 16 rows, lane l the piece (l ^ l /
+    // 8) % 4 of row l / 4, so that row r holds piece p at p ^ (r / 2) % 4 and the lanes of
+    // an operand read meet no bank twice. Rows past the end: the last one again. (Where
+    // the blocks do not go round, two waves copy the same one.)
+    uint32_t xo[kCopyX][2], xso[kCopyX];
+    int xblock[kCopyX];
+#pragma unroll
+    for (int i = 0; i < kCopyX; ++i) {
+      const int b = xblock[i] = (wave + i * T::kWaves) % kBlocks;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = min(tile.r0 + 32 * b + 16 * j + (lane >> 2), tile.r1 - 1);
+        xo[i][j] = (uint32_t)(source_row(a, row) - base_row) * (uint32_t)x_row +
+                   16 * ((lane ^ (lane >> 3)) & 3);
+      }
+      const int row = min(tile.r0 + 32 * b + r32, tile.r1 - 1);
+      xso[i] = (uint32_t)(source_row(a, row) - base_row) * (uint32_t)(a.k >> 5) + 4 * g;
     }
-  };
 
-  // ---- what it computes -----------------------------------------------------------
-  v16f acc[RW][RX];
-#pragma unroll
-  for (int i = 0; i < RW; ++i)
-#pragma unroll
-    for (int t = 0; t < RX; ++t)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][t][q] = 0.f;
-  struct Operands {
-    Piece<FW> w[RW];
-    Piece<FX> x[RX];
-  } op[2];
-  uint32_t sw[RW], sx[RX];
-
-  const uint32_t w_at = ww * RW * T::kWBlock + 16 * lane;
-  const uint32_t x_at = T::kX + wx * RX * T::kXBlock + 128 * r32 +
-                        16 * ((FX == MXG_MXFP4 ? 2 * g : g) ^ (r32 & 7));
-  auto lds16 = [&](uint32_t at) __attribute__((always_inline)) {
-    return *reinterpret_cast<const v4u*>(lds + at);
-  };
-  // The n-th operand of a step: W's, then x's. buf: the buffer's offset.
-  auto fetch = [&](Operands& o, int n, auto step, uint32_t buf) __attribute__((always_inline)) {
-    constexpr int S = decltype(step)::value;
-    if (n < RW) {
-      const uint32_t p = buf + w_at + n * T::kWBlock + S * (FW == MXG_MXFP4 ? 1024 : 2048);
-      o.w[n].lo = lds16(p);
-      if constexpr (FW == MXG_MXFP8) o.w[n].hi = lds16(p + 1024);
-    } else {
-      const int t = n - RW;
-      if constexpr (FX == MXG_MXFP4) {
-        o.x[t].lo = lds16(buf + t * T::kXBlock + (x_at ^ (16 * (4 * (S >> 1) + (S & 1)))));
+    // Copy n of a stage: W's blocks, x's (two each), with a pair's first stage its
+    // scales. Where K ends with a pair's first half, W is zero in the second, and x's
+    // codes and scales before it are taken again.
+    auto copy = [&](int n, int stage) __attribute__((always_inline)) {
+      const uint32_t to = base + (stage & 3) * T::kSlot;
+      const int pair = stage / T::kStages;
+      const uint32_t sto = base + T::kScales + (pair & 1) * T::kPair;
+      if (n < T::kCopyW) {
+        copy_kib<kWLoads>(to + (wave + n * T::kWaves) * T::kWBlock,
+                          wb[n] + (int64_t)stage * T::kWBlock, 16 * lane);
+      } else if (n < kCopies) {
+        const int i = (n - T::kCopyW) >> 1, j = (n - T::kCopyW) & 1;
+        copy_kib<1>(to + T::kX + xblock[i] * T::kXBlock + 1024 * j,
+                    xb + (int64_t)min(stage, last) * 64, xo[i][j]);
+      } else if (n < kCopies + T::kCopyW) {
+        const int i = n - kCopies;
+        copy_words(sto + (wave + i * T::kWaves) * 256, wsb[i] + (int64_t)pair * 256, 4 * lane);
       } else {
-        o.x[t].lo = lds16(buf + t * T::kXBlock + (x_at ^ (32 * S)));
-        o.x[t].hi = lds16(buf + t * T::kXBlock + (x_at ^ (64 + 32 * S)));
-      }
-    }
-  };
-  // A stage's scales, byte S of a word that of step S.
-  auto fetch_scales = [&](uint32_t (&w)[RW], uint32_t (&x)[RX], int stage, uint32_t buf)
-                          __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < RW; ++i) {
-      w[i] = *reinterpret_cast<const uint32_t*>(lds + buf + T::kWS + (ww * RW + i) * 256 + 4 * lane);
-      if constexpr (FX == MXG_MXFP8) w[i] >>= 16 * (stage & 1);
-    }
-#pragma unroll
-    for (int t = 0; t < RX; ++t) {
-      const uint8_t* p = lds + buf + T::kXS + (wx * RX + t) * 256 + 4 * r32;
-      const uint32_t d0 = *reinterpret_cast<const uint32_t*>(p);
-      if constexpr (FX == MXG_MXFP4) {
-        const uint32_t d1 = *reinterpret_cast<const uint32_t*>(p + 128);
-        x[t] = __builtin_amdgcn_perm(d1, d0, g ? 0x07060302u : 0x05040100u);
-      } else {
-        x[t] = d0 >> (16 * g);
-      }
-    }
-  };
-
-  // One step of stage `stage` in the buffer at buf: its products, between them the
-  // next step's operands (kNext) and, in a stage's last one, the copies of the stage
-  // after the next (kCopy).
-  auto step = [&](auto number, auto next, auto copies, int stage, uint32_t buf)
-                  __attribute__((always_inline)) {
-    constexpr int S = decltype(number)::value, kM = RW * RX, kCur = S & 1;
-    constexpr bool kLast = S == T::kSteps - 1;
-    constexpr bool kNext = !kLast || decltype(next)::value, kCopy = kLast && decltype(copies)::value;
-    const uint32_t other = T::kStage - buf;
-    uint32_t nw[RW], nx[RX];
-    if constexpr (kLast && kNext) {
-      // The next stage has landed, every wave is done reading this one.
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      fetch_scales(nw, nx, stage + 1, other);
-    }
-#pragma unroll
-    for (int m = 0; m < kM; ++m) {
-      const int i = m % RW, t = m / RW;
-      acc[i][t] = product<FW, FX, S, S>(op[kCur].w[i], sw[i], op[kCur].x[t], sx[t], acc[i][t]);
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (kNext) {
-#pragma unroll
-        for (int n = m * (RW + RX) / kM; n < (m + 1) * (RW + RX) / kM; ++n)
-          fetch(op[kCur ^ 1], n, Int<kLast ? 0 : S + 1>(), kLast ? other : buf);
-      }
-      if constexpr (kCopy) {
-#pragma unroll
-        for (int n = m * kCopies / kM; n < (m + 1) * kCopies / kM; ++n) copy(n, stage + 2, buf);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if constexpr (kLast && kNext) {
-#pragma unroll
-      for (int i = 0; i < RW; ++i) sw[i] = nw[i];
-#pragma unroll
-      for (int t = 0; t < RX; ++t) sx[t] = nx[t];
-    }
-  };
-  auto whole = [&](auto next, auto copies, int stage, uint32_t buf) __attribute__((always_inline)) {
-    step(Int<0>(), next, copies, stage, buf);
-    step(Int<1>(), next, copies, stage, buf);
-    if constexpr (T::kSteps == 4) {
-      step(Int<2>(), next, copies, stage, buf);
-      step(Int<3>(), next, copies, stage, buf);
-    }
-  };
-
-#pragma unroll
-  for (int n = 0; n < kCopies; ++n) copy(n, 0, 0);
-  if (stages > 1) {
-#pragma unroll
-    for (int n = 0; n < kCopies; ++n) copy(n, 1, T::kStage);
-  }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  fetch_scales(sw, sx, 0, 0);
-#pragma unroll
-  for (int n = 0; n < RW + RX; ++n) fetch(op[0], n, Int<0>(), 0);
-  uint32_t buf = 0;
-  int s = 0;
-  for (; s + 2 < stages; ++s) {
-    whole(Int<1>(), Int<1>(), s, buf);
-    buf = T::kStage - buf;
-  }
-  if (stages > 1) {
-    whole(Int<1>(), Int<0>(), s, buf);
-    buf = T::kStage - buf;
-    ++s;
-  }
-  whole(Int<0>(), Int<0>(), s, buf);
-
-  // ---- epilogue ---------------------------------------------------------------------
-  // A lane's four neighbouring columns meet those of the lane 32 on: 16 bytes.
-#pragma unroll
-  for (int t = 0; t < RX; ++t) {
-    const int i0 = tile.r0 + 32 * (wx * RX + t) + r32;
-    const int to = i0 < tile.r1 ? target_row(a, i0) : -1;
-    uint16_t* row = a.out + (int64_t)max(to, 0) * a.out_n;
-    auto store = [&](const v16f& v, int col) __attribute__((always_inline)) {
-#pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        const auto lo = __builtin_amdgcn_permlane32_swap(bf16_pair(v[4 * q], v[4 * q + 1]),
-                                                         bf16_pair(v[4 * q + 4], v[4 * q + 5]),
-                                                         false, false);
-        const auto hi = __builtin_amdgcn_permlane32_swap(bf16_pair(v[4 * q + 2], v[4 * q + 3]),
-                                                         bf16_pair(v[4 * q + 6], v[4 * q + 7]),
-                                                         false, false);
-        const int c = col + 8 * (q + g);
-        if (to >= 0 && c < a.out_n)
-          *reinterpret_cast<uint4*>(row + c) = uint4{lo[0], hi[0], lo[1], hi[1]};
+        const int i = n - kCopies - T::kCopyW;
+        copy_words(sto + (T::kNW + xblock[i]) * 256, xsb + (int64_t)pair * 8,
+                   xso[i] - (2 * pair + 1 < kbs ? 0 : 4 * g));
       }
     };
-    if (a.gated) {
+    // Part `part` of `parts` of a stage's copies.
+    auto copy_part = [&](int stage, bool scales, int part, int parts)
+                         __attribute__((always_inline)) {
+      const int all = kCopies + (scales ? T::kCopyW + kCopyX : 0);
 #pragma unroll
-      for (int i = 0; i < RW; i += 2) {
-        v16f h;
+      for (int n = part * all / parts; n < (part + 1) * all / parts; ++n) copy(n, stage);
+    };
+
+    // The first four stages (with two steps a stage, the last one's second half comes in
+    // the first step).
 #pragma unroll
-        for (int q = 0; q < 16; ++q) h[q] = gated(acc[i][t][q], acc[i + 1][t][q]);
-        store(h, 32 * (ct * (T::kNW / 2) + (ww * RW + i) / 2));
+    for (int j = 0; j < 4; ++j)
+      if (j < T::kStages || kp > 1) copy_part(j, j % T::kStages == 0, 0, j == 3 ? T::kPer : 1);
+
+    v16f acc[RW][NX];
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+      for (int t = 0; t < NX; ++t) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][t][q] = 0.f;
+        asm volatile("" : "+a"(acc[i][t]));  // here, under the loads' latency
       }
-    } else {
+    // Operands of this and the next step; W's of the next one take the registers of
+    // this one's where MFMAs are long enough (MXFP8: 64 cycles) to hide the reads after
+    // the last use (two sets of both are more registers than there are).
+    constexpr int kSetsW = FX == MXG_MXFP8 ? 1 : 2;
+    Piece<FW> opw[kSetsW][RW];
+    Piece<FX> opx[2][NX];
+    uint32_t sw[RW], sx[NX];
+
+    const uint32_t w_at = ww * RW * T::kWBlock + 16 * lane;
+    const uint32_t x_at = T::kX + wx * T::kXBlock + 64 * r32 + 16 * (g ^ ((r32 >> 1) & 3));
+    auto lds16 = [&](uint32_t at) __attribute__((always_inline)) {
+      return *reinterpret_cast<const v4u*>(lds + at);
+    };
+    // The n-th operand of step S of a pair whose first stage is `first`: W's, then x's.
+    auto fetch = [&](int n, auto step, int first) __attribute__((always_inline)) {
+      constexpr int S = decltype(step)::value;
+      Piece<FW>* const w = opw[S % kSetsW];
+      Piece<FX>* const x = opx[S & 1];
+      const uint32_t slot = ((first + S / T::kPer) & 3) * T::kSlot;
+      if (n < RW) {
+        const uint32_t p = slot + w_at + n * T::kWBlock + (S % T::kPer) * T::kStepW;
+        w[n].lo = lds16(p);
+        if constexpr (FW == MXG_MXFP8) w[n].hi = lds16(p + 1024);
+      } else {
+        const int t = n - RW;
+        const uint32_t p = slot + t * WX * T::kXBlock;
+        x[t].lo = lds16(p + (x_at ^ (32 * (S % T::kPer))));
+        if constexpr (FX == MXG_MXFP8) x[t].hi = lds16(p + (x_at ^ 32));
+      }
+    };
+    // A pair's scales, byte S of a word that of step S.
+    auto fetch_scales = [&](uint32_t (&w)[RW], uint32_t (&x)[NX], int pair)
+                            __attribute__((always_inline)) {
+      const uint8_t* p = lds + T::kScales + (pair & 1) * T::kPair;
 #pragma unroll
-      for (int i = 0; i < RW; ++i) store(acc[i][t], 32 * (ct * T::kNW + ww * RW + i));
+      for (int i = 0; i < RW; ++i)
+        w[i] = *reinterpret_cast<const uint32_t*>(p + (ww * RW + i) * 256 + 4 * lane);
+#pragma unroll
+      for (int t = 0; t < NX; ++t) {
+        const uint32_t* q =
+            reinterpret_cast<const uint32_t*>(p + (T::kNW + wx + t * WX) * 256 + 4 * r32);
+        x[t] = __builtin_amdgcn_perm(q[32], q[0], g ? 0x07050301u : 0x06040200u);
+      }
+    };
+
+    // One step of a pair: its products, between them the next step's operands and
+    // copies. LEFT: the pairs there are after this one (2: or more). Before a stage's
+    // last step its operands are in registers in every wave that has passed the barrier,
+    // so its slot takes the stage four on; there the next stage has to have landed,
+    // younger loads may still fly.
+    auto step = [&](auto number, auto left, int pair) __attribute__((always_inline)) {
+      constexpr int S = decltype(number)::value, kLeft = decltype(left)::value;
+      constexpr int kM = RW * NX, P = T::kPer;
+      constexpr bool kEdge = P == 1 || S % 2 == 1;  // a stage's last step
+      constexpr bool kNext = S < 3 || kLeft > 0;
+      constexpr int J = S / P;                      // its stage of the pair
+      const int first = pair * T::kStages;
+      // Whether stage q, counted from this pair's first one, exists: q < kThere.
+      constexpr int kThere = kLeft == 2 ? 99 : (kLeft + 1) * T::kStages;
+      uint32_t nw[RW], nx[NX];
+      if constexpr (kEdge && kNext) {
+        constexpr int kYounger = (J + 2 < kThere ? loads(J + 2) : 0) +
+                                 (J + 3 < kThere ? loads(J + 3) : 0);
+        wait_loads<kYounger>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if constexpr (S == 3) fetch_scales(nw, nx, pair + 1);
+      }
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        // Neighbouring products share an operand, which costs less energy.
+        const int t = m / RW;
+        const bool back = t % 2 == 1 && (kSetsW == 2 || t < NX - 1);
+        const int i = back ? RW - 1 - m % RW : m % RW;
+        acc[i][t] = product<FW, FX, S, S>(opw[S % kSetsW][i], sw[i], opx[S & 1][t], sx[t],
+                                          acc[i][t]);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (kNext) {
+          const int then = first + (S == 3 ? T::kStages : 0);
+          if (kSetsW == 2) {
+#pragma unroll
+            for (int n = m * (RW + NX) / kM; n < (m + 1) * (RW + NX) / kM; ++n)
+              fetch(n, Int<(S + 1) % 4>(), then);
+          } else {
+            // x's under the products before W's last uses (of one block: with the first).
+            constexpr int kBefore = NX > 1 ? kM - RW : 1;
+            if (m >= kM - RW) fetch(i, Int<(S + 1) % 4>(), then);
+#pragma unroll
+            for (int n = m * NX / kBefore; n < (m + 1) * NX / kBefore && n < NX; ++n)
+              fetch(RW + n, Int<(S + 1) % 4>(), then);
+          }
+        }
+        // Stage J + 4: with two steps a stage, half in its last one, half in the next.
+        constexpr int kTo = kEdge ? J + 4 : J + 3;
+        if constexpr (kTo < kThere)
+          copy_part(first + kTo, kTo % T::kStages == 0, P == 1 || kEdge ? m : kM + m, kM * P);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (S == 3 && kNext) {
+#pragma unroll
+        for (int i = 0; i < RW; ++i) sw[i] = nw[i];
+#pragma unroll
+        for (int t = 0; t < NX; ++t) sx[t] = nx[t];
+      }
+    };
+    auto whole = [&](auto left, int pair) __attribute__((always_inline)) {
+      step(Int<0>(), left, pair);
+      step(Int<1>(), left, pair);
+      step(Int<2>(), left, pair);
+      step(Int<3>(), left, pair);
+    };
+
+    // The first stage is there; of the others as many instructions may be in flight as
+    // were issued.
+    constexpr int kRest3 = [] {  // of the part of stage 3
+      int n = 0;
+      const int all = kCopies + (3 % T::kStages == 0 ? T::kCopyW + kCopyX : 0);
+      for (int c = 0; c < all / T::kPer; ++c) n += c < T::kCopyW ? kWLoads : 1;
+      return n;
+    }();
+    if (kp > 1 || T::kStages == 4)
+      wait_loads<loads(1) + loads(2) + kRest3>();
+    else
+      wait_loads<loads(1)>();
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    fetch_scales(sw, sx, 0);
+#pragma unroll
+    for (int n = 0; n < RW + NX; ++n) fetch(n, Int<0>(), 0);
+    int pair = 0;
+    for (; pair + 2 < kp; ++pair) whole(Int<2>(), pair);
+    if (pair + 1 < kp) whole(Int<1>(), pair++);
+    whole(Int<0>(), pair);
+
+    // ---- epilogue
+    if (T::kSplits && split > 1) {  // sums as they lie, 1 KiB a store, for join_kernel
+      float4* to = reinterpret_cast<float4*>(a.partial) +
+                   ((int64_t)(number * split + part) * T::kWaves + wave) * (RW * RX * 256) + lane;
+#pragma unroll
+      for (int t = 0; t < NX; ++t)
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            to[(t * RW + i) * 256 + 64 * q] =
+                float4{acc[i][t][4 * q], acc[i][t][4 * q + 1], acc[i][t][4 * q + 2],
+                       acc[i][t][4 * q + 3]};
+      return;
+    }
+    // 32 rows of the wave's columns meet in LDS and go out by whole lines.
+    __syncthreads();  // (the ring is read out)
+    uint8_t* const mine = lds + wave * 32 * T::kOutRow;
+    const bool two = a.gated != 0;
+    const int width = two ? 16 * RW : 32 * RW;  // columns of the wave
+    const int col = ct * (two ? 16 : 32) * T::kNW + ww * width;
+    const int lg = two ? (RW == 4 ? 3 : 2) : (RW == 4 ? 4 : 3);  // lanes of 16 bytes for a row
+#pragma unroll
+    for (int t = 0; t < NX; ++t) {
+      auto lay = [&](const v16f& v, int block) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < 4; q += 2)
+          *reinterpret_cast<uint4*>(mine + r32 * T::kOutRow + 64 * block + 16 * (q + g)) =
+              eight_columns(v, q);
+      };
+      if (two) {
+#pragma unroll
+        for (int i = 0; i < RW; i += 2) lay(gated(acc[i][t], acc[i + 1][t]), i / 2);
+      } else {
+#pragma unroll
+        for (int i = 0; i < RW; ++i) lay(acc[i][t], i);
+      }
+      __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
+      const int row0 = tile.r0 + 32 * (t * WX + wx);
+      for (int u = lane; u < 32 << lg; u += 64) {
+        const int r = u >> lg, c = 8 * (u & ((1 << lg) - 1));
+        const uint4 v = *reinterpret_cast<const uint4*>(mine + r * T::kOutRow + 2 * c);
+        if (row0 + r < tile.r1 && col + c < a.out_n) {
+          const int to = target_row(a, row0 + r);
+          if (to >= 0) *reinterpret_cast<uint4*>(a.out + (int64_t)to * a.out_n + col + c) = v;
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+  };
+  static_assert(RX == 4, "");
+  const int n = (tile.r1 - tile.r0 + 32 * WX - 1) / (32 * WX);
+  if (n == 4)
+    run(Int<4>());
+  else if (n == 3)
+    run(Int<3>());
+  else if (n == 2)
+    run(Int<2>());
+  else
+    run(Int<1>());
+}
+
+// Adds up the parts of a split K in ascending order, one wave per 32 rows of x of a
+// wave of a tile.
+template <int RW, int RX, int WW, int WX>
+__global__ void __launch_bounds__(64) join_kernel(RowsArgs a, int row_tiles, int col_tiles,
+                                                  int split) {
+  constexpr int kWaves = WW * WX, kNW = WW * RW, kTileRows = 32 * WX * RX;
+  const int lane = threadIdx.x, r32 = lane & 31, g = lane >> 5;
+  const int t = blockIdx.x % RX, wave = blockIdx.x / RX % kWaves;
+  const int number = blockIdx.x / (RX * kWaves);
+  const int ww = wave % WW, wx = wave / WW;
+  // (As rows_tile_kernel numbers them.)
+  constexpr int kGroup = 8;
+  const int group = number / (kGroup * col_tiles);
+  const int high = min(kGroup, row_tiles - group * kGroup);
+  const int in = number - group * kGroup * col_tiles;
+  const int ct = in / high, rt = group * kGroup + in % high;
+  const int row = rt * kTileRows + 32 * (t * WX + wx);
+  if (row >= a.rows) return;
+  const float4* from = reinterpret_cast<const float4*>(a.partial) +
+                       ((int64_t)number * split * kWaves + wave) * (RW * RX * 256) + t * RW * 256 +
+                       lane;
+  v16f acc[RW] = {};
+  constexpr int B = 4;  // parts in flight
+  for (int p0 = 0; p0 < split; p0 += B) {
+    float4 v[B][RW][4];
+#pragma unroll
+    for (int p = 0; p < B; ++p)
+#pragma unroll
+      for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          v[p][i][q] = from[(int64_t)min(p0 + p, split - 1) * (kWaves * RW * RX * 256) + i * 256 +
+                            64 * q];
+#pragma unroll
+    for (int p = 0; p < B; ++p) {
+      if (p0 + p >= split) break;
+#pragma unroll
+      for (int i = 0; i < RW; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          acc[i][4 * q] += v[p][i][q].x;
+          acc[i][4 * q + 1] += v[p][i][q].y;
+          acc[i][4 * q + 2] += v[p][i][q].z;
+          acc[i][4 * q + 3] += v[p][i][q].w;
+        }
+    }
+  }
+  if (row + r32 >= a.rows) return;  // (a row's two lanes together)
+  uint16_t* out = a.out + (int64_t)(row + r32) * a.out_n;
+  auto store = [&](const v16f& v, int col) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      const uint4 u = eight_columns(v, q);
+      const int c = col + 8 * (q + g);
+      if (c < a.out_n) *reinterpret_cast<uint4*>(out + c) = u;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < RW; i += 2) {
+    if (a.gated) {
+      store(gated(acc[i], acc[i + 1]), 16 * (ct * kNW + ww * RW + i));
+    } else {
+      store(acc[i], 32 * (ct * kNW + ww * RW + i));
+      store(acc[i + 1], 32 * (ct * kNW + ww * RW + i + 1));
     }
   }
 }
 
+// What a launch is cut into.
+struct Shape {
+  bool wide;      // 256 rows of W a tile, or 128
+  int64_t row_tiles, col_tiles;
+  int split;
+};
+
+constexpr int kTileRows = 256;  // rows of x
+
+Shape shape_of(const RowsArgs& a) {
+  Shape s;
+  const int64_t most = a.rows / kTileRows + (a.experts < a.rows ? a.experts : a.rows);
+  s.row_tiles = a.offsets ? most : (a.rows + kTileRows - 1) / kTileRows;
+  s.col_tiles = (a.nb + 7) / 8;
+  s.wide = s.row_tiles * s.col_tiles >= 192;
+  if (!s.wide) s.col_tiles = (a.nb + 3) / 4;
+  s.split = 1;
+  if (!a.offsets && !s.wide) {
+    while (s.split < 16 && s.row_tiles * s.col_tiles * s.split * 2 <= 256 &&
+           a.kp >= 8 * s.split)
+      s.split *= 2;
+  }
+  return s;
+}
+
 template <int FW, int FX, int RW, int RX, int WW, int WX>
-hipError_t launch(const RowsArgs& a, hipStream_t s) {
+hipError_t launch(const RowsArgs& a, const Shape& h, hipStream_t s) {
   using T = Tile<FW, FX, RW, RX, WW, WX>;
-  const int64_t most = a.rows / T::kRows + (a.experts < a.rows ? a.experts : a.rows);
-  const int64_t rt = a.offsets ? most : (a.rows + T::kRows - 1) / T::kRows;
-  const int64_t ct = (a.nb + T::kNW - 1) / T::kNW;
-  const int64_t grid = (rt * ct + 255) / 256 * 256;
+  static_assert(T::kRows == kTileRows, "");
+  const int64_t grid = (h.row_tiles * h.col_tiles * h.split + 255) / 256 * 256;
   if (grid * T::kThreads > UINT32_MAX) return hipErrorInvalidValue;
   hipLaunchKernelGGL((rows_tile_kernel<FW, FX, RW, RX, WW, WX>), dim3((unsigned)grid),
-                     dim3(T::kThreads), 0, s, a, (int)rt, (int)ct);
+                     dim3(T::kThreads), 0, s, a, (int)h.row_tiles, (int)h.col_tiles, h.split);
+  if constexpr (T::kSplits)
+    if (h.split > 1)
+      hipLaunchKernelGGL((join_kernel<RW, RX, WW, WX>),
+                         dim3((unsigned)(h.row_tiles * h.col_tiles * T::kWaves * RX)), dim3(64), 0,
+                         s, a, (int)h.row_tiles, (int)h.col_tiles, h.split);
   return hipGetLastError();
 }
 
 template <int FW, int FX>
 hipError_t by_size(const RowsArgs& a, hipStream_t s) {
-  return launch<FW, FX, 4, 4, 2, 2>(a, s);
+  const Shape h = shape_of(a);
+  return h.wide ? launch<FW, FX, 4, 4, 2, 2>(a, h, s) : launch<FW, FX, 2, 4, 2, 2>(a, h, s);
 }
 
 }  // namespace
+
+size_t rows_tile_workspace(const RowsArgs& a) {
+  const Shape h = shape_of(a);
+  return h.split > 1 ? (size_t)(h.row_tiles * h.col_tiles) * h.split * 4 * 128 * kTileRows : 0;
+}
 
 hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, hipStream_t s) {
   if (x_format == MXG_MXFP4) return by_size<MXG_MXFP4, MXG_MXFP4>(a, s);

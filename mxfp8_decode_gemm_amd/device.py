@@ -658,11 +658,15 @@ class Linear(_RowsWeight):
         else:
             _address(out, "out", torch.bfloat16, (rows, self.out_n), dev)
         self._home.used(handle, stream)
-        code = _lib.mxrows_product(self._weight, kind, px, ps, rows, out.data_ptr(), handle)
+        nbytes = _lib.mxrows_workspace_bytes(self._weight, kind, rows)
+        workspace = _fresh(x, (nbytes,), torch.uint8, stream) if nbytes else None
+        code = _lib.mxrows_product(self._weight, kind, px, ps, rows,
+                                   workspace.data_ptr() if nbytes else None, nbytes,
+                                   out.data_ptr(), handle)
         if code:
             mx._check(code, "mxrows_product")
         if stream is not None:
-            _lend(stream, x, x_scale, out)
+            _lend(stream, x, x_scale, out, workspace)
         return out
 
 

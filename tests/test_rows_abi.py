@@ -24,7 +24,7 @@ def test_exports_every_declared_function(mx):
     names = mx.header_functions(mx.ROWS_HEADER_PATH)
     assert names == ["mxfp4_dequantize", "mxfp4_quantize", "mxmoe_combine", "mxmoe_grouped", "mxmoe_sort",
                      "mxmoe_sort_workspace_bytes", "mxrows_pack_weight", "mxrows_packed_scale_bytes",
-                     "mxrows_packed_weight_bytes", "mxrows_product"]
+                     "mxrows_packed_weight_bytes", "mxrows_product", "mxrows_workspace_bytes"]
     assert not [n for n in names if not hasattr(mx.library(), n) or not hasattr(mx, n)]
 
 
@@ -98,11 +98,31 @@ BAD_WEIGHTS = [
     (dict(rows=(1 << 24) + 1), -1), (dict(out=None), -1), (dict(x=4104), -2), (dict(xs=4098), -2), (dict(out=4104), -2),
 ]] + [(dict(experts=2), {}, -1)])
 def test_product_refusals(mx, wkw, kw, code):
-    a = dict(weight=True, f=4, x=4096, xs=4096, rows=2, out=4096)
+    a = dict(weight=True, f=4, x=4096, xs=4096, rows=2, ws=None, nbytes=0, out=4096)
     a.update(kw)
     w = mx.mxrows_weight(*{**WEIGHT, **wkw}.values())
     a["weight"] = ctypes.byref(w) if a["weight"] else None
     assert mx.library().mxrows_product(*a.values(), None) == code
+
+
+def test_product_workspace(mx):
+    w = mx.mxrows_weight(*{**WEIGHT, "n": 4096, "k": 16384}.values())
+    assert mx.mxrows_workspace_bytes(w, 4, 8) == 0 and mx.mxrows_workspace_bytes(w, 4, 65536) == 0
+    need = mx.mxrows_workspace_bytes(w, 4, 203)
+    assert 203 * 4096 * 4 * 2 <= need <= 32 << 20
+    most = 0
+    for rows in (33, 64, 65, 200, 256, 257, 1000, 5000):
+        for n in (8, 64, 1000, 8192, 1 << 20):
+            for k in (128, 2048, 65536):
+                v = mx.mxrows_weight(*{**WEIGHT, "n": n, "k": k}.values())
+                most = max(most, mx.mxrows_workspace_bytes(v, 4, rows))
+    assert 0 < most <= 32 << 20
+    lib = mx.library()
+    for ws, nbytes, code in ((None, need, -4), (4096, need - 1, -4), (4104, need, -2)):
+        assert lib.mxrows_product(ctypes.byref(w), 4, 4096, 4096, 203, ws, nbytes, 4096, None) == code
+    for bad in (dict(experts=2), dict(n=12), dict(gated=3), dict(format=1)):
+        assert mx.mxrows_workspace_bytes(mx.mxrows_weight(*{**WEIGHT, **bad}.values()), 4, 203) == 0
+    assert mx.mxrows_workspace_bytes(w, 5, 203) == 0 and mx.mxrows_workspace_bytes(w, 4, 0) == 0
 
 
 @pytest.mark.parametrize("wkw,kw,code", [(w, {}, c) for w, c in BAD_WEIGHTS] + [({}, kw, c) for kw, c in [

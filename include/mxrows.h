@@ -158,8 +158,8 @@ int mxmoe_sort(const int32_t* ids, int32_t tokens, int32_t top_k, int32_t expert
 
 /* out[o(i)] = W[e] x[r(i)] for the sorted rows i in offsets[e] ..
  * offsets[e + 1] - 1 of every expert e, with the arithmetic of mxrows_product;
- *   r(i) = order[i] / gather with gather >= 1 (a router's tokens: its top_k),
- *          i with gather 0;
+ *   r(i) = order[i] / gather with gather from 1 to MXG_ROUTE_MAX_TOP_K (a router's
+ *          tokens: its top_k), i with gather 0;
  *   o(i) = order[i] with scatter 1, i with scatter 0.
  * An expert may have no rows. Rows of out that no i leads to (the pairs without
  * an expert) are left as they were.

@@ -81,6 +81,7 @@ int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const 
   a.order = order;
   a.x_rows = x_rows;
   a.gather = gather;
+  a.gather_inv = gather > 1 ? (uint32_t)(((uint64_t)1 << 32) / gather + 1) : 0;
   a.scatter = scatter;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (!by_tiles(a)) return hip_code(launch_rows_stream(a, w->format, x_format, s));
@@ -172,7 +173,7 @@ int mxmoe_grouped(const mxrows_weight* w, int32_t x_format, const uint8_t* x,
                   const uint8_t* x_scale, int32_t x_rows, const int32_t* order, int32_t gather,
                   int32_t scatter, const int32_t* offsets, int32_t rows, uint16_t* out,
                   void* stream) {
-  if (!offsets || gather < 0 || (scatter != 0 && scatter != 1)) return MXG_EINVAL;
+  if (!offsets || gather < 0 || gather > MXG_ROUTE_MAX_TOP_K || (scatter != 0 && scatter != 1)) return MXG_EINVAL;
   if ((gather || scatter) && !order) return MXG_EINVAL;
   if (!rows_ok(x_rows) || (!gather && x_rows != rows)) return MXG_EINVAL;
   if (!aligned(offsets, 4) || !aligned(order, 4)) return MXG_EALIGN;

@@ -53,81 +53,107 @@ __device__ __forceinline__ uint32_t fp4_scale_byte(uint32_t amax) {
   return (uint32_t)(s < 0 ? 0 : s);
 }
 
-// One lane per 8 values, the 4 lanes of a block side by side. Bound by HBM: 2 or
-// 4 bytes read, 17/32 written per value. v_cvt_scalef32_pk_fp4_f32 divides by
-// the scale (a power of two: exact) and rounds once, ties to even, for every
-// finite block (|v / 2^e| <= 6).
+// Codes and scale byte of a lane's 8 values; the 4 lanes of a block side by side.
+// v_cvt_scalef32_pk_fp4_f32 divides by the scale (a power of two: exact) and rounds
+// once, ties to even, for every finite block (|v / 2^e| <= 6).
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t* scale) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  const uint32_t sb = *scale = fp4_scale_byte(quad_max_u32(amax));
+  uint32_t codes = 0;
+  if (sb == 0xFFu) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) codes |= (7u | (__float_as_uint(v[i]) >> 28 & 8u)) << (4 * i);
+  } else {
+    const float s = e8m0_to_f32(sb);
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[0], v[1], s, 0);
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2], v[3], s, 1);
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[4], v[5], s, 2);
+    codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[6], v[7], s, 3);
+  }
+  return codes;
+}
+
+// One lane per 8 values ("chunk"), kFlight chunks of a lane in flight. Bound by HBM: 2
+// or 4 bytes read, 17/32 written per value. Rows without a gap are one long row
+// (rows == 1); otherwise blockIdx.y counts the rows.
+constexpr int kFlight = 4;
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads)
-    quantize4_kernel(const void* x, int64_t row_stride, int64_t chunks, int per_row, uint8_t* xq,
+    quantize4_kernel(const void* x, int64_t row_stride, int rows, int64_t chunks, uint8_t* xq,
                      uint8_t* xs) {
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  for (int64_t base = (int64_t)blockIdx.x * kThreads; base < chunks; base += stride) {
-    const int64_t c = base + threadIdx.x;
-    const int64_t cc = c < chunks ? c : chunks - 1;  // (chunks are a multiple of 4)
-    const int64_t row = cc / per_row;
-    float v[8];
-    load8<TYPE>(x, row * row_stride + 8 * (cc - row * per_row), v);
-    uint32_t amax = 0;
+  const int64_t stride = (int64_t)gridDim.x * kThreads * kFlight;
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    for (int64_t base = (int64_t)blockIdx.x * kThreads * kFlight; base < chunks; base += stride) {
+      float v[kFlight][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    const uint32_t sb = fp4_scale_byte(quad_max_u32(amax));
-    uint32_t codes = 0;
-    if (sb == 0xFFu) {
+      for (int j = 0; j < kFlight; ++j) {  // (past the end: the last chunk; chunks % 4 == 0)
+        const int64_t c = base + j * kThreads + threadIdx.x;
+        load8<TYPE>(x, row * row_stride + 8 * (c < chunks ? c : chunks - 1), v[j]);
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        codes |= (7u | (__float_as_uint(v[i]) >> 28 & 8u)) << (4 * i);
-    } else {
-      const float s = e8m0_to_f32(sb);
-      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[0], v[1], s, 0);
-      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[2], v[3], s, 1);
-      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[4], v[5], s, 2);
-      codes = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(codes, v[6], v[7], s, 3);
-    }
-    if (c < chunks) {
-      reinterpret_cast<uint32_t*>(xq)[c] = codes;
-      if ((c & 3) == 0) xs[c >> 2] = (uint8_t)sb;
+      for (int j = 0; j < kFlight; ++j) {
+        const int64_t c = base + j * kThreads + threadIdx.x;
+        uint32_t sb;
+        const uint32_t codes = codes8(v[j], &sb);
+        if (c < chunks) {
+          const int64_t to = row * chunks + c;
+          reinterpret_cast<uint32_t*>(xq)[to] = codes;
+          if ((c & 3) == 0) xs[to >> 2] = (uint8_t)sb;
+        }
+      }
     }
   }
 }
 
-// One lane per 8 codes. The FP32 product of an E2M1 value and a power of two is
-// exact up to FP32's range; the type's rounding follows.
+// One lane per 8 codes, kFlight in flight. The FP32 product of an E2M1 value and a
+// power of two is exact up to FP32's range; the type's rounding follows.
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads)
     dequantize4_kernel(const uint8_t* xq, const uint8_t* xs, int64_t chunks, void* y) {
-  const int64_t stride = (int64_t)gridDim.x * kThreads;
-  for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < chunks; c += stride) {
-    const uint32_t codes = reinterpret_cast<const uint32_t*>(xq)[c];
-    const uint32_t sb = xs[c >> 2];
-    const float s = sb == 0xFFu ? __uint_as_float(0x7FC00000u) : e8m0_to_f32(sb);
-    float v[8];
-#define MXG_FP4_PAIR(I)                                                            \
-  {                                                                                \
-    const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.f, I);        \
-    v[2 * I] = p[0] * s;                                                           \
-    v[2 * I + 1] = p[1] * s;                                                       \
-  }
-    MXG_FP4_PAIR(0)
-    MXG_FP4_PAIR(1)
-    MXG_FP4_PAIR(2)
-    MXG_FP4_PAIR(3)
-#undef MXG_FP4_PAIR
-    if constexpr (TYPE == MXG_F32) {
-      float4* q = reinterpret_cast<float4*>(y) + 2 * c;
-      q[0] = float4{v[0], v[1], v[2], v[3]};
-      q[1] = float4{v[4], v[5], v[6], v[7]};
-    } else {
-      uint32_t w[4];
+  const int64_t stride = (int64_t)gridDim.x * kThreads * kFlight;
+  for (int64_t base = (int64_t)blockIdx.x * kThreads * kFlight; base < chunks; base += stride) {
+    uint32_t codes[kFlight], sb[kFlight];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (TYPE == MXG_BF16)
-          w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
-        else
-          w[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * i]) |
-                 (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * i + 1]) << 16;
+    for (int j = 0; j < kFlight; ++j) {
+      const int64_t c = base + j * kThreads + threadIdx.x, cc = c < chunks ? c : chunks - 1;
+      codes[j] = reinterpret_cast<const uint32_t*>(xq)[cc];
+      sb[j] = xs[cc >> 2];
+    }
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      const int64_t c = base + j * kThreads + threadIdx.x;
+      if (c >= chunks) break;
+      const float s = sb[j] == 0xFFu ? __uint_as_float(0x7FC00000u) : e8m0_to_f32(sb[j]);
+      float v[8];
+#define MXG_FP4_PAIR(I)                                                        \
+  {                                                                            \
+    const auto p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes[j], 1.f, I); \
+    v[2 * I] = p[0] * s;                                                       \
+    v[2 * I + 1] = p[1] * s;                                                   \
+  }
+      MXG_FP4_PAIR(0)
+      MXG_FP4_PAIR(1)
+      MXG_FP4_PAIR(2)
+      MXG_FP4_PAIR(3)
+#undef MXG_FP4_PAIR
+      if constexpr (TYPE == MXG_F32) {
+        float4* q = reinterpret_cast<float4*>(y) + 2 * c;
+        q[0] = float4{v[0], v[1], v[2], v[3]};
+        q[1] = float4{v[4], v[5], v[6], v[7]};
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (TYPE == MXG_BF16)
+            w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+          else
+            w[i] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * i]) |
+                   (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v[2 * i + 1]) << 16;
+        }
+        reinterpret_cast<uint4*>(y)[c] = uint4{w[0], w[1], w[2], w[3]};
       }
-      reinterpret_cast<uint4*>(y)[c] = uint4{w[0], w[1], w[2], w[3]};
     }
   }
 }
@@ -189,16 +215,22 @@ unsigned blocks_for(int64_t threads) {
 
 hipError_t launch_fp4_quantize(const void* x, int x_type, int64_t row_stride, int rows, int k,
                                uint8_t* xq, uint8_t* xs, hipStream_t s) {
-  const int64_t chunks = (int64_t)rows * (k / 8);
-  const dim3 grid(blocks_for(chunks)), block(kThreads);
+  int64_t chunks = k / 8;
+  if (row_stride == k) {
+    chunks *= rows;
+    rows = 1;
+  }
+  const dim3 grid(blocks_for((chunks + kFlight - 1) / kFlight),
+                  (unsigned)(rows < 16384 ? rows : 16384)),
+      block(kThreads);
   if (x_type == MXG_F32)
-    hipLaunchKernelGGL((quantize4_kernel<MXG_F32>), grid, block, 0, s, x, row_stride, chunks, k / 8,
+    hipLaunchKernelGGL((quantize4_kernel<MXG_F32>), grid, block, 0, s, x, row_stride, rows, chunks,
                        xq, xs);
   else if (x_type == MXG_BF16)
-    hipLaunchKernelGGL((quantize4_kernel<MXG_BF16>), grid, block, 0, s, x, row_stride, chunks,
-                       k / 8, xq, xs);
+    hipLaunchKernelGGL((quantize4_kernel<MXG_BF16>), grid, block, 0, s, x, row_stride, rows, chunks,
+                       xq, xs);
   else
-    hipLaunchKernelGGL((quantize4_kernel<MXG_F16>), grid, block, 0, s, x, row_stride, chunks, k / 8,
+    hipLaunchKernelGGL((quantize4_kernel<MXG_F16>), grid, block, 0, s, x, row_stride, rows, chunks,
                        xq, xs);
   return hipGetLastError();
 }
@@ -206,7 +238,7 @@ hipError_t launch_fp4_quantize(const void* x, int x_type, int64_t row_stride, in
 hipError_t launch_fp4_dequantize(const uint8_t* xq, const uint8_t* xs, int rows, int k, int y_type,
                                  void* y, hipStream_t s) {
   const int64_t chunks = (int64_t)rows * (k / 8);
-  const dim3 grid(blocks_for(chunks)), block(kThreads);
+  const dim3 grid(blocks_for((chunks + kFlight - 1) / kFlight)), block(kThreads);
   if (y_type == MXG_F32)
     hipLaunchKernelGGL((dequantize4_kernel<MXG_F32>), grid, block, 0, s, xq, xs, chunks, y);
   else if (y_type == MXG_BF16)

@@ -11,7 +11,8 @@ namespace {
 
 // ---- sort --------------------------------------------------------------------
 //
-// A counting sort that keeps the order of equal keys, without atomics. Workgroups
+// A counting sort that keeps the order of equal keys (the only atomics add whole
+// numbers in LDS). Workgroups
 // take contiguous chunks of the pairs, waves contiguous parts of a chunk. Bucket e
 // < experts holds expert e's pairs, bucket `experts` those without one. A pair's
 // place is the sum of what lies before its bucket, of its bucket in earlier
@@ -25,7 +26,8 @@ namespace {
 constexpr int kSortWaves = 16;
 constexpr int kSortThreads = 64 * kSortWaves;
 constexpr int kBuckets = MXG_MOE_MAX_EXPERTS + 2;  // an even number
-constexpr int kChunk = 4096;                       // pairs of a workgroup, or more:
+constexpr int kOne = 4096;    // most pairs of a single workgroup
+constexpr int kChunk = 1024;  // pairs of each of several, or more:
 constexpr int kMostGroups = 256;
 
 struct SortArgs {
@@ -68,6 +70,7 @@ template <bool ONE>  // one workgroup: counts and places in this launch
 __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a, int count_only) {
   __shared__ uint32_t part[kSortWaves][kBuckets];
   __shared__ uint32_t sums[kSortWaves];
+  __shared__ uint32_t total[2][ONE ? 1 : kBuckets];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int used = a.experts + 1;
@@ -92,21 +95,42 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a, in
 
   // Buckets 2 tid and 2 tid + 1: all their pairs, and those of earlier workgroups.
   uint32_t all[2] = {0, 0}, before[2] = {0, 0};
-  if (2 * tid < used) {
-    if (ONE) {
+  if (ONE) {
+    if (2 * tid < used) {
       for (int w = 0; w < kSortWaves; ++w) {
         all[0] += part[w][2 * tid];
         if (2 * tid + 1 < used) all[1] += part[w][2 * tid + 1];
       }
-    } else {
-      const uint2* row = reinterpret_cast<const uint2*>(a.counts) + tid;
+    }
+  } else {
+    // Teams of threads, one for each pair of buckets, take the workspace's rows in turn.
+    const int half = a.stride / 2, teams = kSortThreads / half;
+    const int team = tid / half, pair = tid - team * half;
+    for (int b = tid; b < 2 * kBuckets; b += kSortThreads) total[b / kBuckets][b % kBuckets] = 0;
+    __syncthreads();
+    if (team < teams) {
+      const uint2* row = reinterpret_cast<const uint2*>(a.counts) + pair;
+      uint2 sum = {0, 0}, low = {0, 0};
 #pragma unroll 8
-      for (int k = 0; k < a.groups; ++k) {
-        const uint2 n = row[(int64_t)k * (a.stride / 2)];
-        all[0] += n.x;
-        all[1] += n.y;
-        before[0] += k < (int)blockIdx.x ? n.x : 0;
-        before[1] += k < (int)blockIdx.x ? n.y : 0;
+      for (int k = team; k < a.groups; k += teams) {
+        const uint2 n = row[(int64_t)k * half];
+        const bool earlier = k < (int)blockIdx.x;
+        sum.x += n.x;
+        sum.y += n.y;
+        low.x += earlier ? n.x : 0;
+        low.y += earlier ? n.y : 0;
+      }
+      atomicAdd(&total[0][2 * pair], sum.x);
+      atomicAdd(&total[0][2 * pair + 1], sum.y);
+      atomicAdd(&total[1][2 * pair], low.x);
+      atomicAdd(&total[1][2 * pair + 1], low.y);
+    }
+    __syncthreads();
+    if (2 * tid < used) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        all[j] = total[0][2 * tid + j];
+        before[j] = total[1][2 * tid + j];
       }
     }
   }
@@ -146,7 +170,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_pairs_kernel(SortArgs a, in
 }
 
 void sort_shape(int64_t pairs, int experts, int* chunk, int* groups, int* stride) {
-  int64_t c = kChunk;
+  int64_t c = pairs <= kOne ? kOne : kChunk;
   if ((pairs + c - 1) / c > kMostGroups) c = (pairs + kMostGroups - 1) / kMostGroups;
   *chunk = (int)c;
   *groups = (int)((pairs + c - 1) / c);
@@ -169,26 +193,33 @@ __global__ void __launch_bounds__(kCombineThreads)
   if (c >= cols) return;
   float s[8] = {};
   constexpr int B = 8;
+  const int64_t p0 = t * top_k;
   for (int j0 = 0; j0 < top_k; j0 += B) {
-    uint4 v[B];
+    // A pair without an expert takes the row of the first one that has one: every load
+    // is issued, without a branch, and none of a row that is not asked for.
+    int any = 0;
     float w[B];
     bool there[B];
 #pragma unroll
-    for (int j = 0; j < B; ++j) {
-      const int64_t p = t * top_k + min(j0 + j, top_k - 1);
-      const int e = ids[p];
-      w[j] = weights[p];
+    for (int j = B - 1; j >= 0; --j) {
+      const int at = min(j0 + j, top_k - 1), e = ids[p0 + at];
+      w[j] = weights[p0 + at];
       there[j] = j0 + j < top_k && (unsigned)e < (unsigned)experts;
-      if (there[j]) v[j] = y[p * cols + c];
+      any = there[j] ? j + 1 : any;
     }
+    if (any == 0) continue;
+    uint4 v[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) v[j] = y[(p0 + j0 + (there[j] ? j : any - 1)) * cols + c];
 #pragma unroll
     for (int j = 0; j < B; ++j) {
-      if (!there[j]) continue;
       const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[2 * i] = fmaf(w[j], __uint_as_float(u[i] << 16), s[2 * i]);
-        s[2 * i + 1] = fmaf(w[j], __uint_as_float(u[i] & 0xFFFF0000u), s[2 * i + 1]);
+        const float a = fmaf(w[j], __uint_as_float(u[i] << 16), s[2 * i]);
+        const float b = fmaf(w[j], __uint_as_float(u[i] & 0xFFFF0000u), s[2 * i + 1]);
+        s[2 * i] = there[j] ? a : s[2 * i];
+        s[2 * i + 1] = there[j] ? b : s[2 * i + 1];
       }
     }
   }

@@ -45,13 +45,23 @@ __device__ __forceinline__ v16f product(const Piece<FW>& w, uint32_t sw, const P
                                                          CX, BW, (int)sw, BX, (int)sx);
 }
 
+// silu(gate) * up. With E = exp(-|gate|), silu is gate / (1 + E) for a gate from zero
+// on and gate E / (1 + E) below: the reciprocal's argument lies in 1..2, and E as the
+// square of exp2(-|gate| log2(e) / 2) is right down to FP32's subnormals. E is off by
+// |gate| 2^-23 and a few 2^-24 of itself (the exponent's rounding), far below the
+// result's BF16 rounding; expf and a division took twice the time of a tile's
+// epilogue.
 __device__ __forceinline__ float gated(float gate, float up) {
-  return gate / (1.f + expf(-gate)) * up;
+  const float q = __builtin_amdgcn_exp2f(fabsf(gate) * -0.72134752f);
+  const float e = q * q;
+  return gate * (gate < 0.f ? e : 1.f) * __builtin_amdgcn_rcpf(1.f + e) * up;
 }
 
-// Eight neighbouring columns 8 (q + g) .. of lane l's row l % 32 of a product, in
-// BF16: a lane's four meet those of the lane 32 on. q: 0 or 2.
-__device__ __forceinline__ uint4 eight_columns(const v16f& v, int q) {
+// Eight neighbouring columns of lane l's row l % 32 in BF16, from the values that it
+// holds of 16: v[0..3] are columns 4 (l / 32) .. and v[4..7] those 8 on; a lane's four
+// meet those of the lane 32 on, and lane group l / 32 gets columns 8 (l / 32) ...
+template <typename V>
+__device__ __forceinline__ uint4 eight_columns(const V& v, int q = 0) {
   const auto lo = __builtin_amdgcn_permlane32_swap(bf16_pair(v[4 * q], v[4 * q + 1]),
                                                    bf16_pair(v[4 * q + 4], v[4 * q + 5]), false,
                                                    false);
@@ -110,7 +120,8 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int experts
 // The row of x that sorted row i takes.
 __device__ __forceinline__ int source_row(const RowsArgs& a, int i) {
   if (a.gather == 0) return i;
-  const int r = (int)((uint32_t)a.order[i] / (uint32_t)a.gather);
+  const uint32_t o = (uint32_t)a.order[i];
+  const int r = (int)(a.gather == 1 ? o : __umulhi(o, a.gather_inv));
   return min(max(r, 0), a.x_rows - 1);
 }
 

@@ -33,6 +33,9 @@ struct RowsArgs {
   int64_t w_bytes, ws_bytes;  // of one expert
   int32_t experts, n, k, gated, rows, x_rows, gather, scatter;
   int32_t out_n, nb, kp;  // columns of out; row blocks of a weight, pairs of kb
+  // floor(2^32 / gather) + 1: o / gather is the high word of its product with o, for o
+  // below 2^24 and gather from 2 to 32 (the product's excess is below o 2^-32).
+  uint32_t gather_inv;
   float* partial;         // workspace of a split K (one weight, all rows), or null
 };
 

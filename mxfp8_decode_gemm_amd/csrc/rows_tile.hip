@@ -64,6 +64,18 @@ struct Tile {
   static_assert(kWaves * 32 * kOutRow <= kScales, "");
 };
 
+// Tile `number` of a launch: eight row tiles side by side down the columns, so that
+// neighbours share W and x.
+__device__ __forceinline__ void tile_at(int number, int row_tiles, int col_tiles, int* ct,
+                                        int* rt) {
+  constexpr int kGroup = 8;
+  const int group = row_tiles <= kGroup ? 0 : number / (kGroup * col_tiles);
+  const int high = min(kGroup, row_tiles - group * kGroup);
+  const int in = number - group * kGroup * col_tiles;
+  *ct = high == kGroup ? in / kGroup : in / high;
+  *rt = group * kGroup + (in - *ct * high);
+}
+
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   static_assert(N < 64, "");
@@ -87,13 +99,9 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
   if (at >= row_tiles * col_tiles * split) return;
   // The tiles of one part of K after the other: those of a run share its rows of x.
   const int tiles = row_tiles * col_tiles;
-  const int part = at / tiles, number = at - part * tiles;
-  // Eight row tiles side by side down the columns, so that a run shares W and x.
-  constexpr int kGroup = 8;
-  const int group = number / (kGroup * col_tiles);
-  const int high = min(kGroup, row_tiles - group * kGroup);
-  const int in = number - group * kGroup * col_tiles;
-  const int ct = in / high, rt = group * kGroup + in % high;
+  const int part = split > 1 ? at / tiles : 0, number = at - part * tiles;
+  int ct, rt;
+  tile_at(number, row_tiles, col_tiles, &ct, &rt);
   RowTile tile{0, rt * T::kRows, min(rt * T::kRows + T::kRows, a.rows)};
   if (a.offsets) {
     tile = find_tile<T::kRows>(a.offsets, a.experts, a.rows, rt, lane);
@@ -356,37 +364,49 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
     // 32 rows of the wave's columns meet in LDS and go out by whole lines.
     __syncthreads();  // (the ring is read out)
     uint8_t* const mine = lds + wave * 32 * T::kOutRow;
-    const bool two = a.gated != 0;
-    const int width = two ? 16 * RW : 32 * RW;  // columns of the wave
-    const int col = ct * (two ? 16 : 32) * T::kNW + ww * width;
-    const int lg = two ? (RW == 4 ? 3 : 2) : (RW == 4 ? 4 : 3);  // lanes of 16 bytes for a row
+    auto emit = [&](auto gate) __attribute__((always_inline)) {
+      constexpr bool kTwo = decltype(gate)::value;
+      constexpr int kWidth = (kTwo ? 16 : 32) * RW;  // columns of the wave
+      constexpr int kLanes = kWidth / 8;             // of 16 bytes, for a row
+      const int col = ct * (kTwo ? 16 : 32) * T::kNW + ww * kWidth + 8 * (lane % kLanes);
 #pragma unroll
-    for (int t = 0; t < NX; ++t) {
-      auto lay = [&](const v16f& v, int block) __attribute__((always_inline)) {
+      for (int t = 0; t < NX; ++t) {
+        auto lay = [&](const v16f& v, int block) __attribute__((always_inline)) {
 #pragma unroll
-        for (int q = 0; q < 4; q += 2)
-          *reinterpret_cast<uint4*>(mine + r32 * T::kOutRow + 64 * block + 16 * (q + g)) =
-              eight_columns(v, q);
-      };
-      if (two) {
+          for (int q = 0; q < 4; q += 2)
+            *reinterpret_cast<uint4*>(mine + r32 * T::kOutRow + 64 * block + 16 * (q + g)) =
+                eight_columns(v, q);
+        };
+        if constexpr (kTwo) {
 #pragma unroll
-        for (int i = 0; i < RW; i += 2) lay(gated(acc[i][t], acc[i + 1][t]), i / 2);
-      } else {
+          for (int i = 0; i < RW; i += 2) lay(gated(acc[i][t], acc[i + 1][t]), i / 2);
+        } else {
 #pragma unroll
-        for (int i = 0; i < RW; ++i) lay(acc[i][t], i);
-      }
-      __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
-      const int row0 = tile.r0 + 32 * (t * WX + wx);
-      for (int u = lane; u < 32 << lg; u += 64) {
-        const int r = u >> lg, c = 8 * (u & ((1 << lg) - 1));
-        const uint4 v = *reinterpret_cast<const uint4*>(mine + r * T::kOutRow + 2 * c);
-        if (row0 + r < tile.r1 && col + c < a.out_n) {
-          const int to = target_row(a, row0 + r);
-          if (to >= 0) *reinterpret_cast<uint4*>(a.out + (int64_t)to * a.out_n + col + c) = v;
+          for (int i = 0; i < RW; ++i) lay(acc[i][t], i);
         }
+        __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
+        constexpr int kTimes = 32 * kLanes / 64;
+        const int row0 = tile.r0 + 32 * (t * WX + wx) + lane / kLanes;
+        int to[kTimes];
+        uint4 v[kTimes];
+#pragma unroll
+        for (int u = 0; u < kTimes; ++u) {
+          const int row = row0 + u * (64 / kLanes);
+          to[u] = row < tile.r1 ? target_row(a, row) : -1;
+          v[u] = *reinterpret_cast<const uint4*>(
+              mine + (lane / kLanes + u * (64 / kLanes)) * T::kOutRow + 16 * (lane % kLanes));
+        }
+#pragma unroll
+        for (int u = 0; u < kTimes; ++u)
+          if (to[u] >= 0 && col < a.out_n)
+            *reinterpret_cast<uint4*>(a.out + (int64_t)to[u] * a.out_n + col) = v[u];
+        __builtin_amdgcn_wave_barrier();
       }
-      __builtin_amdgcn_wave_barrier();
-    }
+    };
+    if (a.gated)
+      emit(Int<1>());
+    else
+      emit(Int<0>());
   };
   static_assert(RX == 4, "");
   const int n = (tile.r1 - tile.r0 + 32 * WX - 1) / (32 * WX);
@@ -400,72 +420,59 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
     run(Int<1>());
 }
 
-// Adds up the parts of a split K in ascending order, one wave per 32 rows of x of a
-// wave of a tile.
-template <int RW, int RX, int WW, int WX>
+// Adds up the parts of a split K in ascending order. A wave takes 16 columns of 32
+// rows of x (gated: of gate and up): a quarter of a block pair, so that there are
+// enough waves for the memory.
+template <int RW, int RX, int WW, int WX, bool GATED>
 __global__ void __launch_bounds__(64) join_kernel(RowsArgs a, int row_tiles, int col_tiles,
                                                   int split) {
   constexpr int kWaves = WW * WX, kNW = WW * RW, kTileRows = 32 * WX * RX;
+  constexpr int kN = GATED ? 2 : 1;
   const int lane = threadIdx.x, r32 = lane & 31, g = lane >> 5;
   const int t = blockIdx.x % RX, wave = blockIdx.x / RX % kWaves;
   const int number = blockIdx.x / (RX * kWaves);
+  const int half = blockIdx.y % 2, block = blockIdx.y / 2;
   const int ww = wave % WW, wx = wave / WW;
-  // (As rows_tile_kernel numbers them.)
-  constexpr int kGroup = 8;
-  const int group = number / (kGroup * col_tiles);
-  const int high = min(kGroup, row_tiles - group * kGroup);
-  const int in = number - group * kGroup * col_tiles;
-  const int ct = in / high, rt = group * kGroup + in % high;
+  int ct, rt;
+  tile_at(number, row_tiles, col_tiles, &ct, &rt);
   const int row = rt * kTileRows + 32 * (t * WX + wx);
   if (row >= a.rows) return;
   const float4* from = reinterpret_cast<const float4*>(a.partial) +
-                       ((int64_t)number * split * kWaves + wave) * (RW * RX * 256) + t * RW * 256 +
-                       lane;
-  v16f acc[RW] = {};
-  constexpr int B = 4;  // parts in flight
+                       ((int64_t)number * split * kWaves + wave) * (RW * RX * 256) +
+                       (t * RW + block * kN) * 256 + 128 * half + lane;
+  float s[kN][8] = {};
+  constexpr int B = 8;  // parts in flight
   for (int p0 = 0; p0 < split; p0 += B) {
-    float4 v[B][RW][4];
+    float4 v[B][kN][2];
 #pragma unroll
     for (int p = 0; p < B; ++p)
 #pragma unroll
-      for (int i = 0; i < RW; ++i)
+      for (int i = 0; i < kN; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < 2; ++q)
           v[p][i][q] = from[(int64_t)min(p0 + p, split - 1) * (kWaves * RW * RX * 256) + i * 256 +
                             64 * q];
 #pragma unroll
     for (int p = 0; p < B; ++p) {
       if (p0 + p >= split) break;
 #pragma unroll
-      for (int i = 0; i < RW; ++i)
+      for (int i = 0; i < kN; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          acc[i][4 * q] += v[p][i][q].x;
-          acc[i][4 * q + 1] += v[p][i][q].y;
-          acc[i][4 * q + 2] += v[p][i][q].z;
-          acc[i][4 * q + 3] += v[p][i][q].w;
+        for (int q = 0; q < 2; ++q) {
+          s[i][4 * q] += v[p][i][q].x;
+          s[i][4 * q + 1] += v[p][i][q].y;
+          s[i][4 * q + 2] += v[p][i][q].z;
+          s[i][4 * q + 3] += v[p][i][q].w;
         }
     }
   }
-  if (row + r32 >= a.rows) return;  // (a row's two lanes together)
-  uint16_t* out = a.out + (int64_t)(row + r32) * a.out_n;
-  auto store = [&](const v16f& v, int col) __attribute__((always_inline)) {
+  float h[8];
 #pragma unroll
-    for (int q = 0; q < 4; q += 2) {
-      const uint4 u = eight_columns(v, q);
-      const int c = col + 8 * (q + g);
-      if (c < a.out_n) *reinterpret_cast<uint4*>(out + c) = u;
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < RW; i += 2) {
-    if (a.gated) {
-      store(gated(acc[i], acc[i + 1]), 16 * (ct * kNW + ww * RW + i));
-    } else {
-      store(acc[i], 32 * (ct * kNW + ww * RW + i));
-      store(acc[i + 1], 32 * (ct * kNW + ww * RW + i + 1));
-    }
-  }
+  for (int q = 0; q < 8; ++q) h[q] = GATED ? gated(s[0][q], s[kN - 1][q]) : s[0][q];
+  const uint4 u = eight_columns(h);
+  const int c = 32 * ((ct * kNW + ww * RW) / kN + block) + 16 * half + 8 * g;
+  if (row + r32 < a.rows && c < a.out_n)
+    *reinterpret_cast<uint4*>(a.out + (int64_t)(row + r32) * a.out_n + c) = u;
 }
 
 // What a launch is cut into.
@@ -502,10 +509,15 @@ hipError_t launch(const RowsArgs& a, const Shape& h, hipStream_t s) {
   hipLaunchKernelGGL((rows_tile_kernel<FW, FX, RW, RX, WW, WX>), dim3((unsigned)grid),
                      dim3(T::kThreads), 0, s, a, (int)h.row_tiles, (int)h.col_tiles, h.split);
   if constexpr (T::kSplits)
-    if (h.split > 1)
-      hipLaunchKernelGGL((join_kernel<RW, RX, WW, WX>),
-                         dim3((unsigned)(h.row_tiles * h.col_tiles * T::kWaves * RX)), dim3(64), 0,
-                         s, a, (int)h.row_tiles, (int)h.col_tiles, h.split);
+    if (h.split > 1) {
+      const dim3 joins((unsigned)(h.row_tiles * h.col_tiles * T::kWaves * RX), a.gated ? RW : 2 * RW);
+      if (a.gated)
+        hipLaunchKernelGGL((join_kernel<RW, RX, WW, WX, true>), joins, dim3(64), 0, s, a,
+                           (int)h.row_tiles, (int)h.col_tiles, h.split);
+      else
+        hipLaunchKernelGGL((join_kernel<RW, RX, WW, WX, false>), joins, dim3(64), 0, s, a,
+                           (int)h.row_tiles, (int)h.col_tiles, h.split);
+    }
   return hipGetLastError();
 }
 

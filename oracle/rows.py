@@ -8,8 +8,9 @@ return how far a result may be off before its rounding to BF16; ``bf16_bound`` a
   waves meet, each off by no more than 2^-23 of the sum of magnitudes;
 * with MXFP8 on either side the matrix instruction drops, of eight products at aligned K, what lies below 2^-13 of
   the largest: at most 7 * 2^-13 of it. The largest magnitudes of the eight of W and of x bound that product;
-* silu and its product in FP32: 10 * 2^-23 of the result (exp, add, divide and two multiplies at no more than 2 ulp
-  each); a change of the gate by d moves silu by at most 1.1 d;
+* silu and its product in FP32: (10 + |gate|) * 2^-23 of the result (exp, add, reciprocal and multiplies at no more
+  than 2 ulp each; the exponent -|gate| log2(e), rounded to 2^-24 of itself by its product and by its constant, moves
+  exp by |gate| 2^-23 of it at most); a change of the gate by d moves silu by at most 1.1 d;
 * one BF16 rounding: half a step, at most 2^-8 of the value.
 """
 
@@ -24,7 +25,7 @@ from .quant import BLOCK
 
 E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
 SILU_SLOPE = 1.1
-GATE_ROUNDING = 10 * 2.0**-23
+GATE_ROUNDING = 2.0**-23
 
 
 def e2m1_value(code: int) -> float:
@@ -117,7 +118,7 @@ def product(w, w_scale, x, x_scale, gated=False):
     g, u, dg, du = exact[:, :half], exact[:, half:], slack[:, :half], slack[:, half:]
     silu = g / (1 + np.exp(-g))
     h = silu * u
-    return h, SILU_SLOPE * dg * (np.abs(u) + du) + np.abs(silu) * du + GATE_ROUNDING * np.abs(h)
+    return h, SILU_SLOPE * dg * (np.abs(u) + du) + np.abs(silu) * du + GATE_ROUNDING * (10 + np.abs(g)) * np.abs(h)
 
 
 def sort_pairs(ids, experts):

@@ -127,7 +127,7 @@ def test_product_workspace(mx):
 
 @pytest.mark.parametrize("wkw,kw,code", [(w, {}, c) for w, c in BAD_WEIGHTS] + [({}, kw, c) for kw, c in [
     (dict(weight=False), -1), (dict(f=0), -1), (dict(x=None), -1), (dict(xs=None), -1), (dict(out=None), -1),
-    (dict(offsets=None), -1), (dict(rows=0), -1), (dict(x_rows=0), -1), (dict(gather=-1), -1), (dict(scatter=2), -1),
+    (dict(offsets=None), -1), (dict(rows=0), -1), (dict(x_rows=0), -1), (dict(gather=-1), -1), (dict(gather=33), -1), (dict(scatter=2), -1),
     (dict(order=None), -1), (dict(order=None, gather=0, scatter=1, x_rows=6), -1), (dict(gather=0), -1),
     (dict(x=4104), -2), (dict(out=4104), -2), (dict(offsets=4098), -2), (dict(order=4098), -2),
     (dict(f=8, x_rows=1 << 24), -5),  # 2^24 rows of 256 bytes: 4 GiB

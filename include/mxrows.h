@@ -134,7 +134,8 @@ int mxrows_product(const mxrows_weight* w, int32_t x_format, const uint8_t* x,
 
 /* ---- a router's pairs by expert -------------------------------------------- */
 
-/* Bytes of workspace mxmoe_sort needs; 0 on bad sizes. It needs no arming. */
+/* Bytes of workspace mxmoe_sort needs: 0 for at most 4096 pairs, and on bad
+ * sizes. It needs no arming. */
 size_t mxmoe_sort_workspace_bytes(int32_t tokens, int32_t top_k, int32_t experts);
 
 /* The pairs p = t * top_k + j of a router's choices by expert, an expert's in
@@ -146,7 +147,7 @@ size_t mxmoe_sort_workspace_bytes(int32_t tokens, int32_t top_k, int32_t experts
  *             MXG_ROWS_MAX pairs
  *   experts   1..MXG_MOE_MAX_EXPERTS
  *   workspace device, at least mxmoe_sort_workspace_bytes(), 16-B aligned; one
- *             call at a time per workspace
+ *             call at a time per workspace. NULL where that is 0
  *   order     device, [tokens * top_k] int32
  *   offsets   device, [experts + 1] int32
  * Errors: MXG_EINVAL, MXG_EALIGN, MXG_EWORKSPACE, MXG_EHIP. */

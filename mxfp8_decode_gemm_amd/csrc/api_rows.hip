@@ -162,8 +162,8 @@ int mxmoe_sort(const int32_t* ids, int32_t tokens, int32_t top_k, int32_t expert
                void* stream) {
   if (!ids || !order || !offsets || !pairs_ok(tokens, top_k, experts)) return MXG_EINVAL;
   if (!aligned(ids, 4) || !aligned(order, 4) || !aligned(offsets, 4)) return MXG_EALIGN;
-  if (!workspace || workspace_bytes < mxmoe_sort_workspace_bytes(tokens, top_k, experts))
-    return MXG_EWORKSPACE;
+  const size_t needed = mxmoe_sort_workspace_bytes(tokens, top_k, experts);
+  if (needed && (!workspace || workspace_bytes < needed)) return MXG_EWORKSPACE;
   if (!aligned(workspace, 16)) return MXG_EALIGN;
   return hip_code(launch_sort(ids, tokens * top_k, experts, workspace, order, offsets,
                               static_cast<hipStream_t>(stream)));

@@ -11,16 +11,18 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight consecutive values of a row as FP32.
+// Eight consecutive values of a row as FP32 (not kept in the caches: 16384 rows of 8192
+// BF16, quantized and back, 103 us; 137 kept).
 template <int TYPE>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) {
   if constexpr (TYPE == MXG_F32) {
-    const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + 4);
+    const v4f* q = reinterpret_cast<const v4f*>(static_cast<const float*>(p) + at);
+    const v4f a = __builtin_nontemporal_load(q), b = __builtin_nontemporal_load(q + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    const v4u a = __builtin_nontemporal_load(
+        reinterpret_cast<const v4u*>(static_cast<const uint16_t*>(p) + at));
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(kThreads)
 
 unsigned blocks_for(int64_t threads) {
   const int64_t b = (threads + kThreads - 1) / kThreads;
-  return (unsigned)(b < 4096 ? b : 4096);
+  return (unsigned)(b < (1 << 20) ? b : 1 << 20);
 }
 
 }  // namespace

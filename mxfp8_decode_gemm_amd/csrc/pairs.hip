@@ -181,50 +181,53 @@ void sort_shape(int64_t pairs, int experts, int* chunk, int* groups, int* stride
 //
 // Bound by the read of y. One thread per 8 columns of a token; a token's ids and
 // weights are the same for the whole workgroup (scalar loads), eight rows' loads in
-// flight.
+// flight. Neighbouring workgroups take a token's columns: its rows lie together.
 
 constexpr int kCombineThreads = 128;
 
 __global__ void __launch_bounds__(kCombineThreads)
-    combine_pairs_kernel(const uint4* y, const int32_t* ids, const float* weights, int top_k,
-                         int experts, int cols, uint4* out) {
-  const int c = blockIdx.y * kCombineThreads + threadIdx.x;
-  const int64_t t = blockIdx.x;
+    combine_pairs_kernel(const v4u* y, const int32_t* ids, const float* weights, int top_k,
+                         int experts, int cols, int tokens, v4u* out) {
+  const int c = blockIdx.x * kCombineThreads + threadIdx.x;
   if (c >= cols) return;
-  float s[8] = {};
-  constexpr int B = 8;
-  const int64_t p0 = t * top_k;
-  for (int j0 = 0; j0 < top_k; j0 += B) {
-    // A pair without an expert takes the row of the first one that has one: every load
-    // is issued, without a branch, and none of a row that is not asked for.
-    int any = 0;
-    float w[B];
-    bool there[B];
+  for (int64_t t = blockIdx.y; t < tokens; t += gridDim.y) {
+    float s[8] = {};
+    constexpr int B = 8;
+    const int64_t p0 = t * top_k;
+    for (int j0 = 0; j0 < top_k; j0 += B) {
+      // A pair without an expert takes the row of the first one that has one: every load
+      // is issued, without a branch, and none of a row that is not asked for.
+      int any = 0;
+      float w[B];
+      bool there[B];
 #pragma unroll
-    for (int j = B - 1; j >= 0; --j) {
-      const int at = min(j0 + j, top_k - 1), e = ids[p0 + at];
-      w[j] = weights[p0 + at];
-      there[j] = j0 + j < top_k && (unsigned)e < (unsigned)experts;
-      any = there[j] ? j + 1 : any;
-    }
-    if (any == 0) continue;
-    uint4 v[B];
+      for (int j = B - 1; j >= 0; --j) {
+        const int at = min(j0 + j, top_k - 1), e = ids[p0 + at];
+        w[j] = weights[p0 + at];
+        there[j] = j0 + j < top_k && (unsigned)e < (unsigned)experts;
+        any = there[j] ? j + 1 : any;
+      }
+      if (any == 0) continue;
+      v4u v[B];
 #pragma unroll
-    for (int j = 0; j < B; ++j) v[j] = y[(p0 + j0 + (there[j] ? j : any - 1)) * cols + c];
+      for (int j = 0; j < B; ++j)
+        v[j] = __builtin_nontemporal_load(y + (p0 + j0 + (there[j] ? j : any - 1)) * cols + c);
 #pragma unroll
-    for (int j = 0; j < B; ++j) {
-      const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+      for (int j = 0; j < B; ++j) {
+        const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = fmaf(w[j], __uint_as_float(u[i] << 16), s[2 * i]);
-        const float b = fmaf(w[j], __uint_as_float(u[i] & 0xFFFF0000u), s[2 * i + 1]);
-        s[2 * i] = there[j] ? a : s[2 * i];
-        s[2 * i + 1] = there[j] ? b : s[2 * i + 1];
+        for (int i = 0; i < 4; ++i) {
+          const float a = fmaf(w[j], __uint_as_float(u[i] << 16), s[2 * i]);
+          const float b = fmaf(w[j], __uint_as_float(u[i] & 0xFFFF0000u), s[2 * i + 1]);
+          s[2 * i] = there[j] ? a : s[2 * i];
+          s[2 * i + 1] = there[j] ? b : s[2 * i + 1];
+        }
       }
     }
+    const v4u r = {bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]), bf16_pair(s[4], s[5]),
+                   bf16_pair(s[6], s[7])};
+    __builtin_nontemporal_store(r, out + t * cols + c);
   }
-  out[t * cols + c] = uint4{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3]), bf16_pair(s[4], s[5]),
-                            bf16_pair(s[6], s[7])};
 }
 
 }  // namespace
@@ -232,6 +235,7 @@ __global__ void __launch_bounds__(kCombineThreads)
 size_t sort_workspace(int64_t pairs, int experts) {
   int chunk, groups, stride;
   sort_shape(pairs, experts, &chunk, &groups, &stride);
+  if (groups == 1) return 0;
   return ((size_t)groups * stride * 4 + 15) / 16 * 16;
 }
 
@@ -258,10 +262,11 @@ hipError_t launch_sort(const int32_t* ids, int pairs, int experts, void* workspa
 hipError_t launch_combine(const uint16_t* y, const int32_t* ids, const float* weights, int tokens,
                           int top_k, int experts, int hidden, uint16_t* out, hipStream_t s) {
   const int cols = hidden / 8;
-  const dim3 grid((unsigned)tokens, (unsigned)((cols + kCombineThreads - 1) / kCombineThreads));
+  const dim3 grid((unsigned)((cols + kCombineThreads - 1) / kCombineThreads),
+                  (unsigned)(tokens < 65535 ? tokens : 65535));
   hipLaunchKernelGGL(combine_pairs_kernel, grid, dim3(kCombineThreads), 0, s,
-                     reinterpret_cast<const uint4*>(y), ids, weights, top_k, experts, cols,
-                     reinterpret_cast<uint4*>(out));
+                     reinterpret_cast<const v4u*>(y), ids, weights, top_k, experts, cols, tokens,
+                     reinterpret_cast<v4u*>(out));
   return hipGetLastError();
 }
 

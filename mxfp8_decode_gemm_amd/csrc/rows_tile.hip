@@ -369,6 +369,15 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
       constexpr int kWidth = (kTwo ? 16 : 32) * RW;  // columns of the wave
       constexpr int kLanes = kWidth / 8;             // of 16 bytes, for a row
       const int col = ct * (kTwo ? 16 : 32) * T::kNW + ww * kWidth + 8 * (lane % kLanes);
+      constexpr int kTimes = 32 * kLanes / 64;  // stores of a lane for 32 rows
+      int to[NX][kTimes];                       // all rows' targets in one round trip
+#pragma unroll
+      for (int t = 0; t < NX; ++t)
+#pragma unroll
+        for (int u = 0; u < kTimes; ++u) {
+          const int row = tile.r0 + 32 * (t * WX + wx) + lane / kLanes + u * (64 / kLanes);
+          to[t][u] = row < tile.r1 ? target_row(a, row) : -1;
+        }
 #pragma unroll
       for (int t = 0; t < NX; ++t) {
         auto lay = [&](const v16f& v, int block) __attribute__((always_inline)) {
@@ -385,21 +394,15 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
           for (int i = 0; i < RW; ++i) lay(acc[i][t], i);
         }
         __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
-        constexpr int kTimes = 32 * kLanes / 64;
-        const int row0 = tile.r0 + 32 * (t * WX + wx) + lane / kLanes;
-        int to[kTimes];
         uint4 v[kTimes];
 #pragma unroll
-        for (int u = 0; u < kTimes; ++u) {
-          const int row = row0 + u * (64 / kLanes);
-          to[u] = row < tile.r1 ? target_row(a, row) : -1;
+        for (int u = 0; u < kTimes; ++u)
           v[u] = *reinterpret_cast<const uint4*>(
               mine + (lane / kLanes + u * (64 / kLanes)) * T::kOutRow + 16 * (lane % kLanes));
-        }
 #pragma unroll
         for (int u = 0; u < kTimes; ++u)
-          if (to[u] >= 0 && col < a.out_n)
-            *reinterpret_cast<uint4*>(a.out + (int64_t)to[u] * a.out_n + col) = v[u];
+          if (to[t][u] >= 0 && col < a.out_n)
+            *reinterpret_cast<uint4*>(a.out + (int64_t)to[t][u] * a.out_n + col) = v[u];
         __builtin_amdgcn_wave_barrier();
       }
     };

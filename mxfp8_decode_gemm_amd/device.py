@@ -687,9 +687,9 @@ def sort_pairs(ids: torch.Tensor, experts: int, order: torch.Tensor = None,
     else:
         _address(offsets, "offsets", torch.int32, (experts + 1,), dev)
     nbytes = _lib.mxmoe_sort_workspace_bytes(tokens, top_k, experts)
-    workspace = _fresh(ids, (nbytes,), torch.uint8, stream)
-    code = _lib.mxmoe_sort(pi, tokens, top_k, experts, workspace.data_ptr(), nbytes,
-                           order.data_ptr(), offsets.data_ptr(), handle)
+    workspace = _fresh(ids, (nbytes,), torch.uint8, stream) if nbytes else None
+    code = _lib.mxmoe_sort(pi, tokens, top_k, experts, workspace.data_ptr() if nbytes else None,
+                           nbytes, order.data_ptr(), offsets.data_ptr(), handle)
     if code:
         mx._check(code, "mxmoe_sort")
     if stream is not None:

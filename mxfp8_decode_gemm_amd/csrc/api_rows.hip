@@ -85,7 +85,7 @@ int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const 
   a.scatter = scatter;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (!by_tiles(a)) return hip_code(launch_rows_stream(a, w->format, x_format, s));
-  const size_t needed = rows_tile_workspace(a);
+  const size_t needed = rows_tile_workspace(a, x_format);
   if (needed) {
     if (!workspace || workspace_bytes < needed) return MXG_EWORKSPACE;
     if (!aligned(workspace, 16)) return MXG_EALIGN;
@@ -141,7 +141,7 @@ int mxrows_pack_weight(int32_t format, const uint8_t* w, const uint8_t* w_scale,
 size_t mxrows_workspace_bytes(const mxrows_weight* w, int32_t x_format, int32_t rows) {
   if (!weight_shape_ok(w) || w->experts != 1 || !format_ok(x_format) || !rows_ok(rows)) return 0;
   const RowsArgs a = rows_args(w, rows, nullptr);
-  return by_tiles(a) ? rows_tile_workspace(a) : 0;
+  return by_tiles(a) ? rows_tile_workspace(a, x_format) : 0;
 }
 
 int mxrows_product(const mxrows_weight* w, int32_t x_format, const uint8_t* x,

@@ -57,10 +57,12 @@ struct Tile {
   static constexpr int kLds = kScales + 2 * kPair;
   static constexpr int kCopyW = kNW / kWaves;  // blocks that a wave copies
   static constexpr bool kSplits = RW == 2;     // K may be divided among workgroups
+  // Workgroups of a CU (by registers and LDS).
+  static constexpr int kResident = RW * RX > 8 ? 1 : 2;
   // What the epilogue lays out at once: 32 rows of a wave's columns, a row's 16 bytes
   // longer than they are, so that eight rows meet no bank twice.
   static constexpr int kOutRow = 64 * RW + 16;
-  static_assert(kNW % kWaves == 0 && RW % 2 == 0 && kLds <= 160 * 1024, "");
+  static_assert(kNW % kWaves == 0 && RW % 2 == 0 && kResident * kLds <= 160 * 1024, "");
   static_assert(kWaves * 32 * kOutRow <= kScales, "");
 };
 
@@ -83,7 +85,8 @@ __device__ __forceinline__ void wait_loads() {
 }
 
 template <int FW, int FX, int RW, int RX, int WW, int WX>
-__global__ void __launch_bounds__(64 * WW * WX) __attribute__((amdgpu_waves_per_eu(1)))
+__global__ void __launch_bounds__(64 * WW * WX)
+__attribute__((amdgpu_waves_per_eu(Tile<FW, FX, RW, RX, WW, WX>::kResident)))
 rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
   using T = Tile<FW, FX, RW, RX, WW, WX>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
@@ -411,13 +414,13 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
     else
       emit(Int<0>());
   };
-  static_assert(RX == 4, "");
   const int n = (tile.r1 - tile.r0 + 32 * WX - 1) / (32 * WX);
-  if (n == 4)
-    run(Int<4>());
-  else if (n == 3)
-    run(Int<3>());
-  else if (n == 2)
+  if constexpr (RX == 4) {
+    if (n == 4) return run(Int<4>());
+    if (n == 3) return run(Int<3>());
+  }
+  static_assert(RX == 2 || RX == 4, "");
+  if (n == 2)
     run(Int<2>());
   else
     run(Int<1>());
@@ -478,35 +481,58 @@ __global__ void __launch_bounds__(64) join_kernel(RowsArgs a, int row_tiles, int
     *reinterpret_cast<uint4*>(a.out + (int64_t)(row + r32) * a.out_n + c) = u;
 }
 
-// What a launch is cut into.
+// What a launch is cut into: tiles of `side` rows of W and of x, K in `split` parts.
 struct Shape {
-  bool wide;      // 256 rows of W a tile, or 128
+  int side;
   int64_t row_tiles, col_tiles;
   int split;
 };
 
-constexpr int kTileRows = 256;  // rows of x
+int64_t row_tiles(const RowsArgs& a, int side) {
+  if (!a.offsets) return (a.rows + side - 1) / side;
+  return a.rows / side + (a.experts < a.rows ? a.experts : a.rows);
+}
 
-Shape shape_of(const RowsArgs& a) {
-  Shape s;
-  const int64_t most = a.rows / kTileRows + (a.experts < a.rows ? a.experts : a.rows);
-  s.row_tiles = a.offsets ? most : (a.rows + kTileRows - 1) / kTileRows;
-  s.col_tiles = (a.nb + 7) / 8;
-  s.wide = s.row_tiles * s.col_tiles >= 192;
-  if (!s.wide) s.col_tiles = (a.nb + 3) / 4;
-  s.split = 1;
-  if (!a.offsets && !s.wide) {
-    while (s.split < 16 && s.row_tiles * s.col_tiles * s.split * 2 <= 256 &&
-           a.kp >= 8 * s.split)
-      s.split *= 2;
+// The times that choose between them, in us as measured on one MI355X (K in pairs of
+// kb, MXFP4 x; MXFP8 x takes twice the time per pair): 256 tiles of 256 one to a CU take
+// 9 + 1.7 a pair; tiles of 128 take 4 + 0.65 a pair with one on a CU, twice that a pair
+// with two. 4096 x 4096 x 4096: 39 with 256, 51 with 128; 1024 x 7168 x 4096: 36 and 26.
+// A divided K adds a launch and its FP32 sums, written and read at 4 TB/s: 203 x 4096 x
+// 16384 in MXFP4 41 with one part; 512 x 7168 x 8192 28 with one, 42 with two.
+double side_time(int64_t tiles, int side, double pairs) {
+  if (side == 256) return (double)((tiles + 255) / 256) * (9 + 1.7 * pairs);
+  if (tiles <= 256) return 4 + 0.65 * pairs;
+  return (double)((tiles + 511) / 512) * (4 + 1.3 * pairs);
+}
+
+Shape shape_of(const RowsArgs& a, int x_format) {
+  const Shape big = {256, row_tiles(a, 256), (a.nb + 7) / 8, 1};
+  Shape s = {128, row_tiles(a, 128), (a.nb + 3) / 4, 1};
+  if (a.offsets) {
+    // Groups end in tiles that are half empty on average; only many rows a group, and
+    // more tiles than CUs, make up for the larger tile's.
+    const int64_t groups = a.experts < a.rows ? a.experts : a.rows;
+    const int64_t tiles = (a.rows / 256 + groups / 2) * big.col_tiles;
+    return a.rows / groups >= 256 && tiles >= 256 ? big : s;
   }
-  return s;
+  const double pairs = a.kp * (x_format == MXG_MXFP4 ? 1.0 : 2.0);
+  const int64_t tiles = s.row_tiles * s.col_tiles;
+  double best = side_time(tiles, 128, pairs);
+  for (int split = 2; split <= 16 && tiles * split <= 256 && a.kp >= 2 * split; split *= 2) {
+    const double t = side_time(tiles, 128, pairs / split) + 4 +
+                     split * (double)a.rows * a.n * 8 / 4e6;
+    if (t < best) {
+      best = t;
+      s.split = split;
+    }
+  }
+  return side_time(big.row_tiles * big.col_tiles, 256, pairs) < best ? big : s;
 }
 
 template <int FW, int FX, int RW, int RX, int WW, int WX>
 hipError_t launch(const RowsArgs& a, const Shape& h, hipStream_t s) {
   using T = Tile<FW, FX, RW, RX, WW, WX>;
-  static_assert(T::kRows == kTileRows, "");
+  static_assert(T::kRows == 32 * T::kNW, "");
   const int64_t grid = (h.row_tiles * h.col_tiles * h.split + 255) / 256 * 256;
   if (grid * T::kThreads > UINT32_MAX) return hipErrorInvalidValue;
   hipLaunchKernelGGL((rows_tile_kernel<FW, FX, RW, RX, WW, WX>), dim3((unsigned)grid),
@@ -526,15 +552,15 @@ hipError_t launch(const RowsArgs& a, const Shape& h, hipStream_t s) {
 
 template <int FW, int FX>
 hipError_t by_size(const RowsArgs& a, hipStream_t s) {
-  const Shape h = shape_of(a);
-  return h.wide ? launch<FW, FX, 4, 4, 2, 2>(a, h, s) : launch<FW, FX, 2, 4, 2, 2>(a, h, s);
+  const Shape h = shape_of(a, FX);
+  return h.side == 256 ? launch<FW, FX, 4, 4, 2, 2>(a, h, s) : launch<FW, FX, 2, 2, 2, 2>(a, h, s);
 }
 
 }  // namespace
 
-size_t rows_tile_workspace(const RowsArgs& a) {
-  const Shape h = shape_of(a);
-  return h.split > 1 ? (size_t)(h.row_tiles * h.col_tiles) * h.split * 4 * 128 * kTileRows : 0;
+size_t rows_tile_workspace(const RowsArgs& a, int x_format) {
+  const Shape h = shape_of(a, x_format);
+  return h.split > 1 ? (size_t)(h.row_tiles * h.col_tiles) * h.split * 4 * h.side * h.side : 0;
 }
 
 hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, hipStream_t s) {

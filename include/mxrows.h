@@ -101,7 +101,7 @@ typedef struct mxrows_weight {
 
 /* Bytes of workspace mxrows_product needs for `rows` rows of this weight (its
  * pointers are not looked at): 0 where K is not divided among workgroups, at most
- * 32 MiB, and 0 on bad sizes. It needs no arming. */
+ * 16 MiB, and 0 on bad sizes. It needs no arming. */
 size_t mxrows_workspace_bytes(const mxrows_weight* w, int32_t x_format, int32_t rows);
 
 /* out[t] = W x[t] for t in 0..rows-1, rounded once to BF16; gated:

@@ -54,10 +54,24 @@ RowsArgs rows_args(const mxrows_weight* w, int32_t rows, const int32_t* offsets)
   return a;
 }
 
-// Whether a call runs by tiles of many rows or streams W for few.
+// Whether a call runs by tiles of many rows (rows_tile.hip) or streams W for few
+// (rows_stream.hip). Streaming reads x for every 32 rows of W, and W for every 32 rows
+// of x; tiles have a start of their own. us, streamed and by tiles:
+//   one weight, by 32-row chunks times n k: 32 x 7168 x 8192 12.0 and 12.3, 24 x 7168 x
+//   8192 10.7 and 12.4, 32 x 4096 x 16384 22 and 13, 64 x 4096 x 4096 7.6 and 10, 64 x
+//   2048 x 8192 11.8 and 11.2, 96 x 2048 x 2048 5.0 and 7.3, 96 x 4096 x 4096 13.1 and
+//   12.6;
+//   64 experts of 4096 x k gated, by rows of an expert: k 512, 1 row 25 and 15; k 2048, 1
+//   and 4 rows 36 and 34, 53 and 49 (MXFP8 54 and 63, 80 and 93), 8 rows 61 and 52; k 4096,
+//   8 and 16 rows 100 and 107, 138 and 105.
 bool by_tiles(const RowsArgs& a) {
-  const int32_t groups = a.offsets ? (a.experts < a.rows ? a.experts : a.rows) : 1;
-  return a.rows / groups > 32;
+  if (a.offsets) {
+    const int32_t mean = a.rows / (a.experts < a.rows ? a.experts : a.rows);
+    return !((mean <= 4 && a.kp >= 8) || (mean <= 8 && a.kp >= 16));
+  }
+  const int64_t chunks = (a.rows + 31) / 32, size = (int64_t)a.n * a.k;
+  if (chunks == 1) return a.rows > 4 && size >= (1 << 26);
+  return chunks * size > (1 << 25);
 }
 
 int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const uint8_t* x_scale,

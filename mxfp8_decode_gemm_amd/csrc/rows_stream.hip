@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads) rows_stream_kernel(RowsArgs a) {
       Piece<FW> wp[RW][2];
 #pragma unroll
       for (int t = 0; t < RX; ++t) {
-        sx[t] = *reinterpret_cast<const uint32_t*>(xsr[t] + 4 * kb) >> (8 * g);
+        sx[t] = *reinterpret_cast<const uint32_t*>(xsr[t] + 4 * kb);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if constexpr (FX == MXG_MXFP4) {
@@ -107,9 +107,10 @@ __global__ void __launch_bounds__(kThreads) rows_stream_kernel(RowsArgs a) {
       for (int i = 0; i < RW; ++i)
 #pragma unroll
         for (int t = 0; t < RX; ++t) {
-          const uint32_t s = h ? sw[i] >> 16 : sw[i];
-          acc[i][t] = product<FW, FX, 0, 0>(wp[i][0], s, xp[t][0], sx[t], acc[i][t]);
-          acc[i][t] = product<FW, FX, 1, 2>(wp[i][1], s, xp[t][1], sx[t], acc[i][t]);
+          // (Shifted here, after the loads have been issued.)
+          const uint32_t s = h ? sw[i] >> 16 : sw[i], x = sx[t] >> (8 * g);
+          acc[i][t] = product<FW, FX, 0, 0>(wp[i][0], s, xp[t][0], x, acc[i][t]);
+          acc[i][t] = product<FW, FX, 1, 2>(wp[i][1], s, xp[t][1], x, acc[i][t]);
         }
     }
   }

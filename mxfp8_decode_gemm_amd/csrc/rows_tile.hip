@@ -56,7 +56,7 @@ struct Tile {
   static constexpr int kScales = kRing * kSlot, kPair = (kNW + kNX) * 256;
   static constexpr int kLds = kScales + 2 * kPair;
   static constexpr int kCopyW = kNW / kWaves;  // blocks that a wave copies
-  static constexpr bool kSplits = RW == 2;     // K may be divided among workgroups
+  static constexpr bool kSplits = RX == 2;     // K may be divided among workgroups
   // Workgroups of a CU (by registers and LDS).
   static constexpr int kResident = RW * RX > 8 ? 1 : 2;
   // What the epilogue lays out at once: 32 rows of a wave's columns, a row's 16 bytes
@@ -105,7 +105,10 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
   const int part = split > 1 ? at / tiles : 0, number = at - part * tiles;
   int ct, rt;
   tile_at(number, row_tiles, col_tiles, &ct, &rt);
-  RowTile tile{0, rt * T::kRows, min(rt * T::kRows + T::kRows, a.rows)};
+  // Rows in blocks of 32, shared evenly among the tiles.
+  const int64_t blocks = (a.rows + 31) / 32;
+  RowTile tile{0, (int)(32 * (rt * blocks / row_tiles)),
+               min((int)(32 * ((rt + 1) * blocks / row_tiles)), a.rows)};
   if (a.offsets) {
     tile = find_tile<T::kRows>(a.offsets, a.experts, a.rows, rt, lane);
     if (tile.expert < 0) return;
@@ -397,15 +400,16 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
           for (int i = 0; i < RW; ++i) lay(acc[i][t], i);
         }
         __builtin_amdgcn_wave_barrier();  // LDS is in order within the wave
-        uint4 v[kTimes];
+        v4u v[kTimes];
 #pragma unroll
         for (int u = 0; u < kTimes; ++u)
-          v[u] = *reinterpret_cast<const uint4*>(
+          v[u] = *reinterpret_cast<const v4u*>(
               mine + (lane / kLanes + u * (64 / kLanes)) * T::kOutRow + 16 * (lane % kLanes));
 #pragma unroll
         for (int u = 0; u < kTimes; ++u)
           if (to[t][u] >= 0 && col < a.out_n)
-            *reinterpret_cast<uint4*>(a.out + (int64_t)to[t][u] * a.out_n + col) = v[u];
+            __builtin_nontemporal_store(
+                v[u], reinterpret_cast<v4u*>(a.out + (int64_t)to[t][u] * a.out_n + col));
         __builtin_amdgcn_wave_barrier();
       }
     };
@@ -415,11 +419,15 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
       emit(Int<0>());
   };
   const int n = (tile.r1 - tile.r0 + 32 * WX - 1) / (32 * WX);
-  if constexpr (RX == 4) {
+  if constexpr (RX == 8) {
+    if (n == 8) return run(Int<8>());
+    if (n == 7) return run(Int<7>());
+    if (n == 6) return run(Int<6>());
+    if (n == 5) return run(Int<5>());
     if (n == 4) return run(Int<4>());
     if (n == 3) return run(Int<3>());
   }
-  static_assert(RX == 2 || RX == 4, "");
+  static_assert(RX == 2 || RX == 8, "");
   if (n == 2)
     run(Int<2>());
   else
@@ -432,7 +440,7 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
 template <int RW, int RX, int WW, int WX, bool GATED>
 __global__ void __launch_bounds__(64) join_kernel(RowsArgs a, int row_tiles, int col_tiles,
                                                   int split) {
-  constexpr int kWaves = WW * WX, kNW = WW * RW, kTileRows = 32 * WX * RX;
+  constexpr int kWaves = WW * WX, kNW = WW * RW;
   constexpr int kN = GATED ? 2 : 1;
   const int lane = threadIdx.x, r32 = lane & 31, g = lane >> 5;
   const int t = blockIdx.x % RX, wave = blockIdx.x / RX % kWaves;
@@ -441,8 +449,9 @@ __global__ void __launch_bounds__(64) join_kernel(RowsArgs a, int row_tiles, int
   const int ww = wave % WW, wx = wave / WW;
   int ct, rt;
   tile_at(number, row_tiles, col_tiles, &ct, &rt);
-  const int row = rt * kTileRows + 32 * (t * WX + wx);
-  if (row >= a.rows) return;
+  const int64_t blocks = (a.rows + 31) / 32;
+  const int row = (int)(32 * (rt * blocks / row_tiles)) + 32 * (t * WX + wx);
+  if (row >= min((int)(32 * ((rt + 1) * blocks / row_tiles)), a.rows)) return;
   const float4* from = reinterpret_cast<const float4*>(a.partial) +
                        ((int64_t)number * split * kWaves + wave) * (RW * RX * 256) +
                        (t * RW + block * kN) * 256 + 128 * half + lane;
@@ -526,7 +535,13 @@ Shape shape_of(const RowsArgs& a, int x_format) {
       s.split = split;
     }
   }
-  return side_time(big.row_tiles * big.col_tiles, 256, pairs) < best ? big : s;
+  if (side_time(big.row_tiles * big.col_tiles, 256, pairs) >= best) return s;
+  // As many row tiles as the last round of workgroups has room for: lower ones.
+  Shape t = big;
+  const int64_t rounds = (t.row_tiles * t.col_tiles + 255) / 256;
+  const int64_t fit = rounds * 256 / t.col_tiles;
+  if (fit > t.row_tiles && fit <= (a.rows + 31) / 32) t.row_tiles = fit;
+  return t;
 }
 
 template <int FW, int FX, int RW, int RX, int WW, int WX>
@@ -553,7 +568,7 @@ hipError_t launch(const RowsArgs& a, const Shape& h, hipStream_t s) {
 template <int FW, int FX>
 hipError_t by_size(const RowsArgs& a, hipStream_t s) {
   const Shape h = shape_of(a, FX);
-  return h.side == 256 ? launch<FW, FX, 4, 4, 2, 2>(a, h, s) : launch<FW, FX, 2, 2, 2, 2>(a, h, s);
+  return h.side == 256 ? launch<FW, FX, 2, 8, 4, 1>(a, h, s) : launch<FW, FX, 2, 2, 2, 2>(a, h, s);
 }
 
 }  // namespace

@@ -30,8 +30,8 @@ __device__ __forceinline__ void copy_kib(uint32_t to, const uint8_t* base, uint3
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
                  "global_load_lds_dwordx4 %1, %2 offset:1024\n\t"
                  "global_load_lds_dwordx4 %1, %2 offset:2048\n\t"
-                 "global_load_lds_dwordx4 %1, %2 offset:3072"
-                 ::"s"(to), "v"(off), "s"(base) : "memory");
+                 "global_load_lds_dwordx4 %1, %2 offset:%3"
+                 ::"s"(to), "v"(off), "s"(base), "n"(3 * 1024) : "memory");
 }
 // 256 bytes, 4 a lane.
 __device__ __forceinline__ void copy_words(uint32_t to, const uint8_t* base, uint32_t off) {
@@ -52,13 +52,36 @@ struct Tile {
   static constexpr int kWBlock = kStepW * kPer, kXBlock = 2048;
   static constexpr int kNW = WW * RW, kNX = WX * RX;  // blocks of 32 rows
   static constexpr int kRows = 32 * kNX;
-  static constexpr int kX = kNW * kWBlock, kSlot = kX + kNX * kXBlock, kRing = 4;
+  static constexpr int kX = kNW * kWBlock, kSlot = kX + kNX * kXBlock;
+  // Slots, and stages copied ahead. Four slots against three: 4096 rows of 7168 x 8192 in
+  // MXFP4 125 us and 128. Ahead by four, a small tile keeps more bytes in flight (203 rows
+  // of 4096 x 16384 31.4 us by four, 33.9 by three, W and x past the caches); a large one
+  // is level and starts later (4096 rows of 7168 x 4096 69.0 by four, 68.3 by three).
+  static constexpr int kRing = 4, kAhead = RX == 8 ? 3 : 4;
   static constexpr int kScales = kRing * kSlot, kPair = (kNW + kNX) * 256;
   static constexpr int kLds = kScales + 2 * kPair;
   static constexpr int kCopyW = kNW / kWaves;  // blocks that a wave copies
   static constexpr bool kSplits = RX == 2;     // K may be divided among workgroups
   // Workgroups of a CU (by registers and LDS).
-  static constexpr int kResident = RW * RX > 8 ? 1 : 2;
+  static constexpr int kResident = RX == 8 ? 1 : 2;
+  // Instructions of a wave's copies of the stages from..to-1 with `copy_x` blocks of x
+  // each; a pair's scales go with its first stage. And of the first 1 / kPer of a
+  // stage's copies.
+  static constexpr int scales(int stage, int copy_x) {
+    return stage % kStages == 0 ? kCopyW + copy_x : 0;
+  }
+  static constexpr int loads(int from, int to, int copy_x) {
+    int n = 0;
+    for (int q = from; q < to; ++q)
+      n += kCopyW * (kWBlock / 1024) + 2 * copy_x + scales(q, copy_x);
+    return n;
+  }
+  static constexpr int first_half(int stage, int copy_x) {
+    const int all = kCopyW + 2 * copy_x + scales(stage, copy_x);
+    int n = 0;
+    for (int c = 0; c < all / kPer; ++c) n += c < kCopyW ? kWBlock / 1024 : 1;
+    return n;
+  }
   // What the epilogue lays out at once: 32 rows of a wave's columns, a row's 16 bytes
   // longer than they are, so that eight rows meet no bank twice.
   static constexpr int kOutRow = 64 * RW + 16;
@@ -145,13 +168,8 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
     constexpr int NX = decltype(blocks)::value;
     constexpr int kBlocks = WX * NX;
     constexpr int kCopyX = (kBlocks + T::kWaves - 1) / T::kWaves;
-    // Instructions of a wave's copies of a stage and of a pair's scales, which go with
-    // the pair's first stage.
     constexpr int kWLoads = T::kWBlock / 1024;
     constexpr int kCopies = T::kCopyW + 2 * kCopyX;
-    constexpr auto loads = [](int stage) constexpr {
-      return T::kCopyW * kWLoads + 2 * kCopyX + (stage % T::kStages == 0 ? T::kCopyW + kCopyX : 0);
-    };
 
     // Rows of x: a wave instruction takes 64 bytes of 16 rows, lane l the piece (l ^ l /
     // 8) % 4 of row l / 4, so that row r holds piece p at p ^ (r / 2) % 4 and the lanes of
@@ -203,11 +221,12 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
       for (int n = part * all / parts; n < (part + 1) * all / parts; ++n) copy(n, stage);
     };
 
-    // The first four stages (with two steps a stage, the last one's second half comes in
-    // the first step).
+    // The first kAhead stages (with two steps a stage, the last one's second half comes
+    // in the first step).
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (j < T::kStages || kp > 1) copy_part(j, j % T::kStages == 0, 0, j == 3 ? T::kPer : 1);
+    for (int j = 0; j < T::kAhead; ++j)
+      if (j < T::kStages || kp > 1)
+        copy_part(j, j % T::kStages == 0, 0, j == T::kAhead - 1 ? T::kPer : 1);
 
     v16f acc[RW][NX];
 #pragma unroll
@@ -266,7 +285,7 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
     // One step of a pair: its products, between them the next step's operands and
     // copies. LEFT: the pairs there are after this one (2: or more). Before a stage's
     // last step its operands are in registers in every wave that has passed the barrier,
-    // so its slot takes the stage four on; there the next stage has to have landed,
+    // so its slot is free for another stage; there the next stage has to have landed,
     // younger loads may still fly.
     auto step = [&](auto number, auto left, int pair) __attribute__((always_inline)) {
       constexpr int S = decltype(number)::value, kLeft = decltype(left)::value;
@@ -279,9 +298,8 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
       constexpr int kThere = kLeft == 2 ? 99 : (kLeft + 1) * T::kStages;
       uint32_t nw[RW], nx[NX];
       if constexpr (kEdge && kNext) {
-        constexpr int kYounger = (J + 2 < kThere ? loads(J + 2) : 0) +
-                                 (J + 3 < kThere ? loads(J + 3) : 0);
-        wait_loads<kYounger>();
+        constexpr int kEnd = J + T::kAhead < kThere ? J + T::kAhead : kThere;
+        wait_loads<T::loads(J + 2, kEnd, kCopyX)>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if constexpr (S == 3) fetch_scales(nw, nx, pair + 1);
@@ -310,8 +328,8 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
               fetch(RW + n, Int<(S + 1) % 4>(), then);
           }
         }
-        // Stage J + 4: with two steps a stage, half in its last one, half in the next.
-        constexpr int kTo = kEdge ? J + 4 : J + 3;
+        // Stage J + kAhead: with two steps a stage, half in its last one, half in the next.
+        constexpr int kTo = kEdge ? J + T::kAhead : J + T::kAhead - 1;
         if constexpr (kTo < kThere)
           copy_part(first + kTo, kTo % T::kStages == 0, P == 1 || kEdge ? m : kM + m, kM * P);
         __builtin_amdgcn_sched_barrier(0);
@@ -332,16 +350,10 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
 
     // The first stage is there; of the others as many instructions may be in flight as
     // were issued.
-    constexpr int kRest3 = [] {  // of the part of stage 3
-      int n = 0;
-      const int all = kCopies + (3 % T::kStages == 0 ? T::kCopyW + kCopyX : 0);
-      for (int c = 0; c < all / T::kPer; ++c) n += c < T::kCopyW ? kWLoads : 1;
-      return n;
-    }();
-    if (kp > 1 || T::kStages == 4)
-      wait_loads<loads(1) + loads(2) + kRest3>();
+    if (kp > 1 || T::kStages >= T::kAhead)
+      wait_loads<T::loads(1, T::kAhead - 1, kCopyX) + T::first_half(T::kAhead - 1, kCopyX)>();
     else
-      wait_loads<loads(1)>();
+      wait_loads<T::loads(1, T::kStages, kCopyX)>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     fetch_scales(sw, sx, 0);

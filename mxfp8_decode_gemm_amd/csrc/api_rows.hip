@@ -55,23 +55,28 @@ RowsArgs rows_args(const mxrows_weight* w, int32_t rows, const int32_t* offsets)
 }
 
 // Whether a call runs by tiles of many rows (rows_tile.hip) or streams W for few
-// (rows_stream.hip). Streaming reads x for every 32 rows of W, and W for every 32 rows
-// of x; tiles have a start of their own. us, streamed and by tiles:
-//   one weight, by 32-row chunks times n k: 32 x 7168 x 8192 12.0 and 12.3, 24 x 7168 x
-//   8192 10.7 and 12.4, 32 x 4096 x 16384 22 and 13, 64 x 4096 x 4096 7.6 and 10, 64 x
-//   2048 x 8192 11.8 and 11.2, 96 x 2048 x 2048 5.0 and 7.3, 96 x 4096 x 4096 13.1 and
-//   12.6;
-//   64 experts of 4096 x k gated, by rows of an expert: k 512, 1 row 25 and 15; k 2048, 1
-//   and 4 rows 36 and 34, 53 and 49 (MXFP8 54 and 63, 80 and 93), 8 rows 61 and 52; k 4096,
-//   8 and 16 rows 100 and 107, 138 and 105.
-bool by_tiles(const RowsArgs& a) {
+// (rows_stream.hip), by the measured times of both, in us.
+// One weight: a round of 256 workgroups, each of 32 rows of W and 32 of x, streams 4096 x
+// 2048 4.9 and 6.7 (MXFP4 and MXFP8), 4096 x 4096 7.6 and 10.9, 4096 x 16384 25 and 39; with
+// 16 rows 3.4 and 4.7, 5.5 and 7.5, 15 and 27; with 8 at most 13 and 24. Either side of the
+// border, streamed and by tiles: 64 rows of 4096 x 4096 in MXFP4 7.6 and 10.2, 96 13.1 and
+// 12.4; 32 of 7168 x 8192 12.6 and 12.8, 64 23 and 13, in MXFP8 16 15.8 and 16.1, 32 20.7
+// and 16.3; 128 of 2048 x 2048 4.3 and 7.5, 256 8.6 and 7.6.
+// Experts, 64 of 4096 x k gated, by rows of each: k 512, 1 row 25 and 15; k 2048, 1 and 4
+// rows 36 and 34, 53 and 49 (MXFP8 54 and 63, 80 and 93), 8 rows 61 and 52; k 4096, 8 and 16
+// rows 100 and 107, 138 and 105.
+bool by_tiles(const RowsArgs& a, int x_format) {
   if (a.offsets) {
     const int32_t mean = a.rows / (a.experts < a.rows ? a.experts : a.rows);
     return !((mean <= 4 && a.kp >= 8) || (mean <= 8 && a.kp >= 16));
   }
-  const int64_t chunks = (a.rows + 31) / 32, size = (int64_t)a.n * a.k;
-  if (chunks == 1) return a.rows > 4 && size >= (1 << 26);
-  return chunks * size > (1 << 25);
+  const bool fp4 = x_format == MXG_MXFP4;
+  const int64_t chunks = (a.rows + 31) / 32;
+  const double pair = a.rows <= 8    ? (fp4 ? 0.18 : 0.35)
+                      : a.rows <= 16 ? (fp4 ? 0.22 : 0.39)
+                                     : (fp4 ? 0.36 : 0.57);
+  const double streamed = (double)((a.nb * chunks + 255) / 256) * (1.5 + a.kp * pair);
+  return rows_tile_us(a, x_format) < streamed;
 }
 
 int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const uint8_t* x_scale,
@@ -98,7 +103,7 @@ int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const 
   a.gather_inv = gather > 1 ? (uint32_t)(((uint64_t)1 << 32) / gather + 1) : 0;
   a.scatter = scatter;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (!by_tiles(a)) return hip_code(launch_rows_stream(a, w->format, x_format, s));
+  if (!by_tiles(a, x_format)) return hip_code(launch_rows_stream(a, w->format, x_format, s));
   const size_t needed = rows_tile_workspace(a, x_format);
   if (needed) {
     if (!workspace || workspace_bytes < needed) return MXG_EWORKSPACE;
@@ -155,7 +160,7 @@ int mxrows_pack_weight(int32_t format, const uint8_t* w, const uint8_t* w_scale,
 size_t mxrows_workspace_bytes(const mxrows_weight* w, int32_t x_format, int32_t rows) {
   if (!weight_shape_ok(w) || w->experts != 1 || !format_ok(x_format) || !rows_ok(rows)) return 0;
   const RowsArgs a = rows_args(w, rows, nullptr);
-  return by_tiles(a) ? rows_tile_workspace(a, x_format) : 0;
+  return by_tiles(a, x_format) ? rows_tile_workspace(a, x_format) : 0;
 }
 
 int mxrows_product(const mxrows_weight* w, int32_t x_format, const uint8_t* x,

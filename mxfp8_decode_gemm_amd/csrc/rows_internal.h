@@ -42,6 +42,7 @@ struct RowsArgs {
 hipError_t launch_rows_stream(const RowsArgs& a, int w_format, int x_format, hipStream_t s);
 // Bytes of a.partial that launch_rows_tile wants for these sizes (0: none).
 size_t rows_tile_workspace(const RowsArgs& a, int x_format);
+double rows_tile_us(const RowsArgs& a, int x_format);  // about its time
 hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, hipStream_t s);
 
 hipError_t launch_rows_pack(int format, const uint8_t* w, const uint8_t* ws, int experts, int n,

@@ -1,8 +1,36 @@
 // Products of many rows (gfx950): mxrows_product and mxmoe_grouped of
 // include/mxrows.h where the matrix cores bound them.
+//
+//   y[r][n] = sum over blocks b of 32 of 2^(sw[n][b] + sx[r][b] - 254) sum of w[n][.] x[r][.]
+//
+// on v_mfma_scale_f32_32x32x64_f8f6f4, W's rows as its A, x's as its B, so that a lane
+// holds neighbouring columns of a row of y. W lies in global memory as the instruction's
+// lanes take it (rows_internal.h) and goes to LDS by whole KiB; x goes there by rows,
+// swizzled. Both are copied without registers in between, stages ahead of the products,
+// behind counted waits and one barrier a stage; operands come to registers one step
+// ahead; sums stay in the accumulators. FP32 sums, rounded once, at the end.
+//
+// A tile is 256 rows of W by up to 256 of x, one workgroup with all of a CU's registers,
+// where there are enough of them (4096 rows of 7168 x 8192 in MXFP4 124 us, 3.9 PFLOP/s;
+// 4096 tokens x 8 of 64 experts of 4096 x 7168 gated 620 us, 3.1 PFLOP/s with the ends of
+// groups counted as work done for nothing). That is bound by power: random MXFP4 operands
+// let the matrix cores run at 7.4 PFLOP/s at 1.80 GHz with nothing else; here the products
+// alone take 44 us of 56 (4096 x 4096 x 8192), 47 with the operand reads, 52 with the
+// copies instead, and the clock falls to 1.5 GHz (without products 37 us at 2.15 GHz). Per
+// workgroup 3.5 us before the first product (5.8 with an order) and 5 to 6 us of results.
+//
+// Else a tile is 128 by 128, on a CU alone or by two, K divided where too few (203 rows of
+// 4096 x 16384 in MXFP4 by MXFP8 20 us and 4 to add up; 512 of 7168 x 8192 26 us in MXFP4,
+// 44 in MXFP8). Those are bound by copies out of L2, 32 KiB for 128 x 128 x 256 products
+// in MXFP4, and by their starts and ends.
+//
+// Left out: 128-row tiles for large problems (shape_of), tiles of 128 x 256 with a divided
+// K (level), copies past the caches (52 -> 60 us), XCD runs of 16 or 64 tiles and groups
+// of 4 or 16 row tiles (within 2 %).
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <type_traits>
 
 #include "rows_device.h"
@@ -18,6 +46,7 @@ using Int = std::integral_constant<int, N>;
 // loads: their end is waited for with s_waitcnt vmcnt.
 template <int COUNT>
 __device__ __forceinline__ void copy_kib(uint32_t to, const uint8_t* base, uint32_t off) {
+  to = __builtin_amdgcn_readfirstlane(to);
   static_assert(COUNT == 1 || COUNT == 2 || COUNT == 4, "");
   if constexpr (COUNT == 1)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
@@ -39,31 +68,44 @@ __device__ __forceinline__ void copy_words(uint32_t to, const uint8_t* base, uin
                ::"s"(to), "v"(off), "s"(base) : "memory");
 }
 
-// A tile's geometry. A stage is 64 bytes of each row of x (128 values in MXFP4: two
-// MFMA steps, 64 in MXFP8: one) with the same K of W; a ring of four of them lies in
-// LDS. Scales come by pairs of kb (four steps), two pairs.
+// A tile's geometry. A stage is kLine bytes of each row of x (of 64: 128 values in MXFP4,
+// two MFMA steps, 64 in MXFP8, one) with the same K of W; a ring of them lies in LDS.
+// Scales come by pairs of kb (four steps).
 // RX: the most 32-row blocks of x of a wave; a tile of fewer rows runs with fewer.
-template <int FW, int FX, int RW, int RX, int WW, int WX>
+template <int FW, int FX, int RW, int RX, int WW, int WX, bool DEEP>
 struct Tile {
   static constexpr int kWaves = WW * WX, kThreads = 64 * kWaves;
-  static constexpr int kPer = FX == MXG_MXFP4 ? 2 : 1;  // steps of a stage
+  // Bytes of a row of x in a stage. A CU copies whole lines of 128 bytes out of L2 at 125
+  // bytes a ns, halves at 72: that bounds a small tile (203 rows of 4096 x 16384 in MXFP4
+  // by MXFP8 27 us with whole lines, 31 with halves). A large one reads less of x for its
+  // products and is as fast with halves, of which a ring holds more stages.
+  static constexpr int kLine = RX == 2 ? 128 : 64;
+  static constexpr int kPer = kLine / (FX == MXG_MXFP4 ? 32 : 64);  // steps of a stage
   static constexpr int kStages = 4 / kPer;              // of a pair
   static constexpr int kStepW = FW == MXG_MXFP4 ? 1024 : 2048;
-  static constexpr int kWBlock = kStepW * kPer, kXBlock = 2048;
+  static constexpr int kWBlock = kStepW * kPer, kXBlock = 32 * kLine;
   static constexpr int kNW = WW * RW, kNX = WX * RX;  // blocks of 32 rows
   static constexpr int kRows = 32 * kNX;
   static constexpr int kX = kNW * kWBlock, kSlot = kX + kNX * kXBlock;
-  // Slots, and stages copied ahead. Four slots against three: 4096 rows of 7168 x 8192 in
-  // MXFP4 125 us and 128. Ahead by four, a small tile keeps more bytes in flight (203 rows
-  // of 4096 x 16384 31.4 us by four, 33.9 by three, W and x past the caches); a large one
-  // is level and starts later (4096 rows of 7168 x 4096 69.0 by four, 68.3 by three).
-  static constexpr int kRing = 4, kAhead = RX == 8 ? 3 : 4;
+  // Slots, and stages copied ahead. A large tile: four slots against three 125 us and 128
+  // (4096 rows of 7168 x 8192 in MXFP4); ahead by three, since by four is level and starts
+  // later (4096 rows of 7168 x 4096 68.3 and 69.0). Small ones share a CU's LDS by two, or
+  // where there is one for each CU have it alone, twice as deep (512 rows of 7168 x 8192
+  // 44 us in MXFP8 and 26 in MXFP4, 62 and 36 with half the ring; two on a CU by half
+  // rings of whole lines against four slots of half lines 392 us and 418, 64 experts of
+  // 4096 x 7168 in MXFP8 gated with 64 rows each).
+  static constexpr int kRing = RX == 8 ? 4 : (FW == FX ? 2 : 3) * (DEEP ? 2 : 1);
+  static constexpr int kAhead = RX == 8 ? 3 : kRing;
+  // Pairs that the stages ahead reach into; the ring of scales holds theirs.
+  static constexpr int kLefts = (kAhead + kStages - 1) / kStages;
+  static constexpr int kScaleRing = kLefts <= 2 ? 2 : 4;
+  static constexpr int kXLoads = kLine / 32;  // instructions for a block of x
   static constexpr int kScales = kRing * kSlot, kPair = (kNW + kNX) * 256;
-  static constexpr int kLds = kScales + 2 * kPair;
+  static constexpr int kLds = kScales + kScaleRing * kPair;
   static constexpr int kCopyW = kNW / kWaves;  // blocks that a wave copies
   static constexpr bool kSplits = RX == 2;     // K may be divided among workgroups
   // Workgroups of a CU (by registers and LDS).
-  static constexpr int kResident = RX == 8 ? 1 : 2;
+  static constexpr int kResident = RX == 8 || DEEP ? 1 : 2;
   // Instructions of a wave's copies of the stages from..to-1 with `copy_x` blocks of x
   // each; a pair's scales go with its first stage. And of the first 1 / kPer of a
   // stage's copies.
@@ -73,11 +115,11 @@ struct Tile {
   static constexpr int loads(int from, int to, int copy_x) {
     int n = 0;
     for (int q = from; q < to; ++q)
-      n += kCopyW * (kWBlock / 1024) + 2 * copy_x + scales(q, copy_x);
+      n += kCopyW * (kWBlock / 1024) + kXLoads * copy_x + scales(q, copy_x);
     return n;
   }
   static constexpr int first_half(int stage, int copy_x) {
-    const int all = kCopyW + 2 * copy_x + scales(stage, copy_x);
+    const int all = kCopyW + kXLoads * copy_x + scales(stage, copy_x);
     int n = 0;
     for (int c = 0; c < all / kPer; ++c) n += c < kCopyW ? kWBlock / 1024 : 1;
     return n;
@@ -101,27 +143,30 @@ __device__ __forceinline__ void tile_at(int number, int row_tiles, int col_tiles
   *rt = group * kGroup + (in - *ct * high);
 }
 
+constexpr int kRun = 32;  // tiles side by side on one XCD
+
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   static_assert(N < 64, "");
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-template <int FW, int FX, int RW, int RX, int WW, int WX>
+template <int FW, int FX, int RW, int RX, int WW, int WX, bool DEEP>
 __global__ void __launch_bounds__(64 * WW * WX)
-__attribute__((amdgpu_waves_per_eu(Tile<FW, FX, RW, RX, WW, WX>::kResident)))
+__attribute__((amdgpu_waves_per_eu(Tile<FW, FX, RW, RX, WW, WX, DEEP>::kResident)))
 rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
-  using T = Tile<FW, FX, RW, RX, WW, WX>;
+  using T = Tile<FW, FX, RW, RX, WW, WX, DEEP>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ww = wave % WW, wx = wave / WW;
   const int r32 = lane & 31, g = lane >> 5;
 
-  // Workgroups go to the XCDs in turn: runs of 32 tiles stay on one.
-  constexpr int kRun = 32;
-  const int bid = blockIdx.x;
-  const int at = bid / (8 * kRun) * (8 * kRun) + (bid & 7) * kRun + (bid >> 3) % kRun;
+  // Workgroups go to the XCDs in turn: runs of 32 tiles stay on one, of fewer where
+  // there are not 256.
+  const int run_of = min((int)gridDim.x / 8, kRun), bid = blockIdx.x;
+  const int round = bid / (8 * kRun) * (8 * kRun);
+  const int at = round + (bid & 7) * run_of + ((bid - round) >> 3);
   if (at >= row_tiles * col_tiles * split) return;
   // The tiles of one part of K after the other: those of a run share its rows of x.
   const int tiles = row_tiles * col_tiles;
@@ -157,10 +202,10 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
   }
   const int x_row = FX == MXG_MXFP4 ? a.k >> 1 : a.k;
   const int64_t base_row = a.gather ? 0 : tile.r0;
-  const uint8_t* xb = a.x + base_row * x_row + (int64_t)pair0 * (256 / T::kPer);
+  const uint8_t* xb = a.x + base_row * x_row + (int64_t)pair0 * (T::kStages * T::kLine);
   const uint8_t* xsb = a.xs + base_row * (a.k >> 5) + (int64_t)pair0 * 8;
   const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  const int last = kbs * (2 / T::kPer) - 1;  // the last stage that x has
+  const int last = (kbs * 2 + T::kPer - 1) / T::kPer - 1;  // the last stage that x has
 
   // The tile with NX blocks of 32 rows of x for each wave: block t of wave column wx
   // is the tile's block t * WX + wx, so that a tile of few rows is shared evenly.
@@ -169,22 +214,26 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
     constexpr int kBlocks = WX * NX;
     constexpr int kCopyX = (kBlocks + T::kWaves - 1) / T::kWaves;
     constexpr int kWLoads = T::kWBlock / 1024;
-    constexpr int kCopies = T::kCopyW + 2 * kCopyX;
+    constexpr int kCopies = T::kCopyW + T::kXLoads * kCopyX;
 
     // Rows of x: a wave instruction takes 64 bytes of 16 rows, lane l the piece (l ^ l /
-    // 8) % 4 of row l / 4, so that row r holds piece p at p ^ (r / 2) % 4 and the lanes of
-    // an operand read meet no bank twice. Rows past the end: the last one again. (Where
-    // the blocks do not go round, two waves copy the same one.)
-    uint32_t xo[kCopyX][2], xso[kCopyX];
+    // 8) % 4 of row l / 4, so that row r holds piece p at p ^ (r / 2) % 4 (or 128 of 8,
+    // piece (l ^ l / 8) % 8 of row l / 8, at p ^ r % 8), and the lanes of an operand read
+    // meet no bank twice. Rows past the end: the last one again. (Where the blocks do not
+    // go round, two waves copy the same one.)
+    constexpr int kPieces = T::kLine / 16;
+    const uint32_t half = 64 * ((lane ^ (lane >> 3)) >> 2 & 1);
+    uint32_t xo[kCopyX][T::kXLoads], xso[kCopyX];
     int xblock[kCopyX];
 #pragma unroll
     for (int i = 0; i < kCopyX; ++i) {
       const int b = xblock[i] = (wave + i * T::kWaves) % kBlocks;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = min(tile.r0 + 32 * b + 16 * j + (lane >> 2), tile.r1 - 1);
+      for (int j = 0; j < T::kXLoads; ++j) {
+        const int row =
+            min(tile.r0 + 32 * b + (32 / T::kXLoads) * j + lane / kPieces, tile.r1 - 1);
         xo[i][j] = (uint32_t)(source_row(a, row) - base_row) * (uint32_t)x_row +
-                   16 * ((lane ^ (lane >> 3)) & 3);
+                   16 * ((lane ^ (lane >> 3)) & (kPieces - 1));
       }
       const int row = min(tile.r0 + 32 * b + r32, tile.r1 - 1);
       xso[i] = (uint32_t)(source_row(a, row) - base_row) * (uint32_t)(a.k >> 5) + 4 * g;
@@ -192,18 +241,21 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
 
     // Copy n of a stage: W's blocks, x's (two each), with a pair's first stage its
     // scales. Where K ends with a pair's first half, W is zero in the second, and x's
-    // codes and scales before it are taken again.
+    // codes (by `half`, where a stage is a whole pair) and scales before it are taken
+    // again.
     auto copy = [&](int n, int stage) __attribute__((always_inline)) {
-      const uint32_t to = base + (stage & 3) * T::kSlot;
+      const uint32_t to = base + (uint32_t)stage % T::kRing * T::kSlot;
       const int pair = stage / T::kStages;
-      const uint32_t sto = base + T::kScales + (pair & 1) * T::kPair;
+      const uint32_t sto = base + T::kScales + (pair & (T::kScaleRing - 1)) * T::kPair;
       if (n < T::kCopyW) {
         copy_kib<kWLoads>(to + (wave + n * T::kWaves) * T::kWBlock,
                           wb[n] + (int64_t)stage * T::kWBlock, 16 * lane);
       } else if (n < kCopies) {
-        const int i = (n - T::kCopyW) >> 1, j = (n - T::kCopyW) & 1;
+        const int i = (n - T::kCopyW) / T::kXLoads, j = (n - T::kCopyW) % T::kXLoads;
+        uint32_t from = xo[i][j];
+        if (T::kPer == 4 && stage == last && kbs & 1) from -= half;
         copy_kib<1>(to + T::kX + xblock[i] * T::kXBlock + 1024 * j,
-                    xb + (int64_t)min(stage, last) * 64, xo[i][j]);
+                    xb + (int64_t)min(stage, last) * T::kLine, from);
       } else if (n < kCopies + T::kCopyW) {
         const int i = n - kCopies;
         copy_words(sto + (wave + i * T::kWaves) * 256, wsb[i] + (int64_t)pair * 256, 4 * lane);
@@ -225,7 +277,7 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
     // in the first step).
 #pragma unroll
     for (int j = 0; j < T::kAhead; ++j)
-      if (j < T::kStages || kp > 1)
+      if (j < T::kStages * kp)
         copy_part(j, j % T::kStages == 0, 0, j == T::kAhead - 1 ? T::kPer : 1);
 
     v16f acc[RW][NX];
@@ -246,7 +298,8 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
     uint32_t sw[RW], sx[NX];
 
     const uint32_t w_at = ww * RW * T::kWBlock + 16 * lane;
-    const uint32_t x_at = T::kX + wx * T::kXBlock + 64 * r32 + 16 * (g ^ ((r32 >> 1) & 3));
+    const uint32_t x_at = T::kX + wx * T::kXBlock + T::kLine * r32 +
+                          16 * (g ^ (T::kLine == 64 ? r32 >> 1 & 3 : r32 & 7));
     auto lds16 = [&](uint32_t at) __attribute__((always_inline)) {
       return *reinterpret_cast<const v4u*>(lds + at);
     };
@@ -255,7 +308,7 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
       constexpr int S = decltype(step)::value;
       Piece<FW>* const w = opw[S % kSetsW];
       Piece<FX>* const x = opx[S & 1];
-      const uint32_t slot = ((first + S / T::kPer) & 3) * T::kSlot;
+      const uint32_t slot = (uint32_t)(first + S / T::kPer) % T::kRing * T::kSlot;
       if (n < RW) {
         const uint32_t p = slot + w_at + n * T::kWBlock + (S % T::kPer) * T::kStepW;
         w[n].lo = lds16(p);
@@ -263,14 +316,15 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
       } else {
         const int t = n - RW;
         const uint32_t p = slot + t * WX * T::kXBlock;
-        x[t].lo = lds16(p + (x_at ^ (32 * (S % T::kPer))));
-        if constexpr (FX == MXG_MXFP8) x[t].hi = lds16(p + (x_at ^ 32));
+        const uint32_t at = x_at ^ (T::kLine / T::kPer * (S % T::kPer));
+        x[t].lo = lds16(p + at);
+        if constexpr (FX == MXG_MXFP8) x[t].hi = lds16(p + (at ^ 32));
       }
     };
     // A pair's scales, byte S of a word that of step S.
     auto fetch_scales = [&](uint32_t (&w)[RW], uint32_t (&x)[NX], int pair)
                             __attribute__((always_inline)) {
-      const uint8_t* p = lds + T::kScales + (pair & 1) * T::kPair;
+      const uint8_t* p = lds + T::kScales + (pair & (T::kScaleRing - 1)) * T::kPair;
 #pragma unroll
       for (int i = 0; i < RW; ++i)
         w[i] = *reinterpret_cast<const uint32_t*>(p + (ww * RW + i) * 256 + 4 * lane);
@@ -290,12 +344,12 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
     auto step = [&](auto number, auto left, int pair) __attribute__((always_inline)) {
       constexpr int S = decltype(number)::value, kLeft = decltype(left)::value;
       constexpr int kM = RW * NX, P = T::kPer;
-      constexpr bool kEdge = P == 1 || S % 2 == 1;  // a stage's last step
+      constexpr bool kEdge = S % P == P - 1;  // a stage's last step
       constexpr bool kNext = S < 3 || kLeft > 0;
       constexpr int J = S / P;                      // its stage of the pair
       const int first = pair * T::kStages;
       // Whether stage q, counted from this pair's first one, exists: q < kThere.
-      constexpr int kThere = kLeft == 2 ? 99 : (kLeft + 1) * T::kStages;
+      constexpr int kThere = kLeft == T::kLefts ? 99 : (kLeft + 1) * T::kStages;
       uint32_t nw[RW], nx[NX];
       if constexpr (kEdge && kNext) {
         constexpr int kEnd = J + T::kAhead < kThere ? J + T::kAhead : kThere;
@@ -331,7 +385,7 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
         // Stage J + kAhead: with two steps a stage, half in its last one, half in the next.
         constexpr int kTo = kEdge ? J + T::kAhead : J + T::kAhead - 1;
         if constexpr (kTo < kThere)
-          copy_part(first + kTo, kTo % T::kStages == 0, P == 1 || kEdge ? m : kM + m, kM * P);
+          copy_part(first + kTo, kTo % T::kStages == 0, kEdge ? m : kM * (S % P + 1) + m, kM * P);
         __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (S == 3 && kNext) {
@@ -350,18 +404,23 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
 
     // The first stage is there; of the others as many instructions may be in flight as
     // were issued.
-    if (kp > 1 || T::kStages >= T::kAhead)
+    if (T::kStages * kp >= T::kAhead)
       wait_loads<T::loads(1, T::kAhead - 1, kCopyX) + T::first_half(T::kAhead - 1, kCopyX)>();
     else
-      wait_loads<T::loads(1, T::kStages, kCopyX)>();
+      wait_loads<0>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     fetch_scales(sw, sx, 0);
 #pragma unroll
     for (int n = 0; n < RW + NX; ++n) fetch(n, Int<0>(), 0);
     int pair = 0;
-    for (; pair + 2 < kp; ++pair) whole(Int<2>(), pair);
-    if (pair + 1 < kp) whole(Int<1>(), pair++);
+    for (; pair + T::kLefts < kp; ++pair) whole(Int<T::kLefts>(), pair);
+    if constexpr (T::kLefts > 3)
+      if (pair + 3 < kp) whole(Int<3>(), pair++);
+    if constexpr (T::kLefts > 2)
+      if (pair + 2 < kp) whole(Int<2>(), pair++);
+    if constexpr (T::kLefts > 1)
+      if (pair + 1 < kp) whole(Int<1>(), pair++);
     whole(Int<0>(), pair);
 
     // ---- epilogue
@@ -507,6 +566,7 @@ struct Shape {
   int side;
   int64_t row_tiles, col_tiles;
   int split;
+  double us;  // (of one weight)
 };
 
 int64_t row_tiles(const RowsArgs& a, int side) {
@@ -514,21 +574,31 @@ int64_t row_tiles(const RowsArgs& a, int side) {
   return a.rows / side + (a.experts < a.rows ? a.experts : a.rows);
 }
 
-// The times that choose between them, in us as measured on one MI355X (K in pairs of
-// kb, MXFP4 x; MXFP8 x takes twice the time per pair): 256 tiles of 256 one to a CU take
-// 9 + 1.7 a pair; tiles of 128 take 4 + 0.65 a pair with one on a CU, twice that a pair
-// with two. 4096 x 4096 x 4096: 39 with 256, 51 with 128; 1024 x 7168 x 4096: 36 and 26.
-// A divided K adds a launch and its FP32 sums, written and read at 4 TB/s: 203 x 4096 x
-// 16384 in MXFP4 41 with one part; 512 x 7168 x 8192 28 with one, 42 with two.
-double side_time(int64_t tiles, int side, double pairs) {
-  if (side == 256) return (double)((tiles + 255) / 256) * (9 + 1.7 * pairs);
-  if (tiles <= 256) return 4 + 0.65 * pairs;
-  return (double)((tiles + 511) / 512) * (4 + 1.3 * pairs);
+// The times that choose between them, in us, fitted to one MI355X's with W and x past the
+// caches (k in pairs of kb; MXFP4 and MXFP8 x). Tiles of 128, 256 or fewer: 4096 x 2048 6.3
+// and 9.4, 4096 x 4096 12 and 17, 4096 x 16384 33 and 50. Two on a CU: 1536 rows of 4096 x
+// 4096 24 and 34, 1024 of 7168 x 8192 43 and 63.
+double small_time(int64_t tiles, double kp, bool fp4) {
+  if (tiles <= 256) return 3 + kp * (fp4 ? 0.5 : 0.75);
+  return (double)((tiles + 511) / 512) * (4 + kp * (fp4 ? 1.17 : 1.95));
+}
+// Tiles of 256 with `h` blocks of 32 rows of x: 7168 x 8192 by 2 31 and 52, by 4 40 and 64,
+// by 8 62 and 94; 2048 rows of 4096 x 4096 (by 4) 24 and 35.
+double wide_time(int64_t tiles, double h, double kp, bool fp4) {
+  const double pair = fp4 ? 0.55 + 0.14 * h : 1 + 0.23 * h;
+  return (double)((tiles + 255) / 256) * (4 + 0.9 * h + kp * pair);
+}
+// What a divided K adds: a launch, the parts and their FP32 sums, written and read. Rows of
+// 4096 x 16384 in MXFP4 with 1, 2 and 4 parts: 128 33, 23 and 18; 256 33, 24 and 23; 512 35
+// and 30; 512 of 4096 x 4096 13 and 20. 32 of 2048 x 8192 in MXFP8 16 with 16 parts, 64 12
+// with 8.
+double join_time(int split, double rows, double n) {
+  return 3 + 0.4 * split + split * rows * n * 8 / 3.5e6;
 }
 
 Shape shape_of(const RowsArgs& a, int x_format) {
-  const Shape big = {256, row_tiles(a, 256), (a.nb + 7) / 8, 1};
-  Shape s = {128, row_tiles(a, 128), (a.nb + 3) / 4, 1};
+  Shape big = {256, row_tiles(a, 256), (a.nb + 7) / 8, 1, 0};
+  Shape s = {128, row_tiles(a, 128), (a.nb + 3) / 4, 1, 0};
   if (a.offsets) {
     // Groups end in tiles that are half empty on average; only many rows a group, and
     // more tiles than CUs, make up for the larger tile's.
@@ -536,33 +606,38 @@ Shape shape_of(const RowsArgs& a, int x_format) {
     const int64_t tiles = (a.rows / 256 + groups / 2) * big.col_tiles;
     return a.rows / groups >= 256 && tiles >= 256 ? big : s;
   }
-  const double pairs = a.kp * (x_format == MXG_MXFP4 ? 1.0 : 2.0);
+  const bool fp4 = x_format == MXG_MXFP4;
   const int64_t tiles = s.row_tiles * s.col_tiles;
-  double best = side_time(tiles, 128, pairs);
+  const double read = 2.5 + (double)a.w_bytes / 6.2e6;  // W, once
+  s.us = fmax(small_time(tiles, a.kp, fp4), read);
   for (int split = 2; split <= 16 && tiles * split <= 256 && a.kp >= 2 * split; split *= 2) {
-    const double t = side_time(tiles, 128, pairs / split) + 4 +
-                     split * (double)a.rows * a.n * 8 / 4e6;
-    if (t < best) {
-      best = t;
+    const double t = fmax(small_time(tiles, (double)a.kp / split, fp4), read) +
+                     join_time(split, a.rows, a.n);
+    if (t < s.us) {
+      s.us = t;
       s.split = split;
     }
   }
-  if (side_time(big.row_tiles * big.col_tiles, 256, pairs) >= best) return s;
-  // As many row tiles as the last round of workgroups has room for: lower ones.
-  Shape t = big;
-  const int64_t rounds = (t.row_tiles * t.col_tiles + 255) / 256;
-  const int64_t fit = rounds * 256 / t.col_tiles;
-  if (fit > t.row_tiles && fit <= (a.rows + 31) / 32) t.row_tiles = fit;
-  return t;
+  // Of large tiles as many down the rows as the last round of workgroups has room for:
+  // lower ones.
+  const int64_t blocks = (a.rows + 31) / 32;
+  const int64_t rounds = (big.row_tiles * big.col_tiles + 255) / 256;
+  const int64_t fit = rounds * 256 / big.col_tiles;
+  if (fit > big.row_tiles) big.row_tiles = fit < blocks ? fit : blocks;
+  const double h = (double)((blocks + big.row_tiles - 1) / big.row_tiles);
+  big.us = wide_time(big.row_tiles * big.col_tiles, h, a.kp, fp4);
+  return big.us < s.us ? big : s;
 }
 
-template <int FW, int FX, int RW, int RX, int WW, int WX>
+template <int FW, int FX, int RW, int RX, int WW, int WX, bool DEEP>
 hipError_t launch(const RowsArgs& a, const Shape& h, hipStream_t s) {
-  using T = Tile<FW, FX, RW, RX, WW, WX>;
+  using T = Tile<FW, FX, RW, RX, WW, WX, DEEP>;
   static_assert(T::kRows == 32 * T::kNW, "");
-  const int64_t grid = (h.row_tiles * h.col_tiles * h.split + 255) / 256 * 256;
+  const int64_t tiles = h.row_tiles * h.col_tiles * h.split;
+  const int64_t unit = tiles < 8 * kRun ? 8 : 8 * kRun;
+  const int64_t grid = (tiles + unit - 1) / unit * unit;
   if (grid * T::kThreads > UINT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((rows_tile_kernel<FW, FX, RW, RX, WW, WX>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((rows_tile_kernel<FW, FX, RW, RX, WW, WX, DEEP>), dim3((unsigned)grid),
                      dim3(T::kThreads), 0, s, a, (int)h.row_tiles, (int)h.col_tiles, h.split);
   if constexpr (T::kSplits)
     if (h.split > 1) {
@@ -580,7 +655,9 @@ hipError_t launch(const RowsArgs& a, const Shape& h, hipStream_t s) {
 template <int FW, int FX>
 hipError_t by_size(const RowsArgs& a, hipStream_t s) {
   const Shape h = shape_of(a, FX);
-  return h.side == 256 ? launch<FW, FX, 2, 8, 4, 1>(a, h, s) : launch<FW, FX, 2, 2, 2, 2>(a, h, s);
+  if (h.side == 256) return launch<FW, FX, 2, 8, 4, 1, false>(a, h, s);
+  return h.row_tiles * h.col_tiles * h.split <= 256 ? launch<FW, FX, 2, 2, 2, 2, true>(a, h, s)
+                                                    : launch<FW, FX, 2, 2, 2, 2, false>(a, h, s);
 }
 
 }  // namespace
@@ -589,6 +666,8 @@ size_t rows_tile_workspace(const RowsArgs& a, int x_format) {
   const Shape h = shape_of(a, x_format);
   return h.split > 1 ? (size_t)(h.row_tiles * h.col_tiles) * h.split * 4 * h.side * h.side : 0;
 }
+
+double rows_tile_us(const RowsArgs& a, int x_format) { return shape_of(a, x_format).us; }
 
 hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, hipStream_t s) {
   if (x_format == MXG_MXFP4) return by_size<MXG_MXFP4, MXG_MXFP4>(a, s);

@@ -78,7 +78,8 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t* scale)
 }
 
 // One lane per 8 values ("chunk"), kFlight chunks of a lane in flight. Bound by HBM: 2
-// or 4 bytes read, 17/32 written per value. Rows without a gap are one long row
+// or 4 bytes read, 17/32 written per value (16384 rows of 8192 BF16 and back 103 us, 6.6
+// TB/s; 111 with eight chunks in flight). Rows without a gap are one long row
 // (rows == 1); otherwise blockIdx.y counts the rows.
 constexpr int kFlight = 4;
 template <int TYPE>

@@ -12,8 +12,8 @@ namespace {
 // ---- sort --------------------------------------------------------------------
 //
 // A counting sort that keeps the order of equal keys (the only atomics add whole
-// numbers in LDS). Workgroups
-// take contiguous chunks of the pairs, waves contiguous parts of a chunk. Bucket e
+// numbers in LDS). Workgroups take contiguous chunks of the pairs, waves contiguous
+// parts of a chunk. Bucket e
 // < experts holds expert e's pairs, bucket `experts` those without one. A pair's
 // place is the sum of what lies before its bucket, of its bucket in earlier
 // workgroups, in earlier waves and in earlier pairs of its wave; the last comes
@@ -22,6 +22,9 @@ namespace {
 // One workgroup does it in one launch. More of them count first, in a launch of
 // their own (a row of the workspace each), and each then sums the rows itself:
 // with at most kMostGroups of them that costs less than a third launch.
+//
+// Bound by latency: 64 pairs 3.1 us, 131072 pairs of 256 experts 10.8 (12.7 and 15.3 by
+// chunks of 2048 and 4096).
 
 constexpr int kSortWaves = 16;
 constexpr int kSortThreads = 64 * kSortWaves;
@@ -181,7 +184,9 @@ void sort_shape(int64_t pairs, int experts, int* chunk, int* groups, int* stride
 //
 // Bound by the read of y. One thread per 8 columns of a token; a token's ids and
 // weights are the same for the whole workgroup (scalar loads), eight rows' loads in
-// flight. Neighbouring workgroups take a token's columns: its rows lie together.
+// flight. Neighbouring workgroups take a token's columns: its rows lie together (4096
+// tokens of 8 x 7168 81 us, 6.4 TB/s; 106 with neighbours along the tokens, level with
+// 256 threads).
 
 constexpr int kCombineThreads = 128;
 

@@ -107,6 +107,9 @@ __global__ void __launch_bounds__(kThreads) rows_stream_kernel(RowsArgs a) {
     }
   }
 
+  // The sums are read no sooner than the last products have ended.
+#pragma unroll
+  for (int i = 0; i < RW; ++i) asm volatile("s_nop 15\n\ts_nop 15" : "+v"(acc[i]));
 #pragma unroll
   for (int i = 0; i < RW; ++i)
 #pragma unroll

@@ -39,6 +39,7 @@ extern "C" {
 #define MXG_F16 2
 #define MXG_MXFP4 4
 #define MXG_MXFP8 8
+#define MXG_MXFP8_FAST 9 /* as x_format: MXFP8 rows, sums of fewer bits (mxrows_product) */
 
 #define MXG_ROWS_MAX 16777216  /* rows of a call (2^24) */
 #define MXG_ROWS_MAX_N 1048576 /* rows of a weight */
@@ -108,19 +109,21 @@ size_t mxrows_workspace_bytes(const mxrows_weight* w, int32_t x_format, int32_t 
  * silu(Wg x[t]) * (Wu x[t]), formed in FP32 before the rounding. A row is out_n =
  * n (gated: n/2) values.
  *
- * The matrix instructions take codes and scales as they are and accumulate in
- * FP32. They sum the products of eight aligned values of K at a time, and of
- * those eight lose what lies below 2^-13 of the largest (toward zero). MXFP4 by
- * MXFP4 has no such product: its sums of eight are exact. With MXFP8 on either side
- * that is at most 7 * 2^-13 of the group's largest product, below the rounding of
- * the BF16 result unless the sum cancels to less than its products; where that
- * matters for up to 8 rows, mxgemm contracts MXFP8 in BF16. Products and sums
- * below 2^-149 are lost, a result or partial sum beyond the FP32 range is
- * infinite or NaN, and a scale byte 255 or an e4m3fn NaN makes NaN of what it
- * enters.
+ * Sums are FP32 and keep what FP32 keeps. MXFP4 by MXFP4 goes through the matrix
+ * instructions as codes and scales lie, eight aligned products of K at a time, whose sum
+ * is exact. With MXFP8 rows the operands are taken to BF16 with their scales, which is
+ * exact for scale bytes 3..246 (mxgemm's contraction). Where a nonzero code has another
+ * scale byte, the 64 values of K around it go by the scaled instruction instead, for at
+ * most 64 rows of W and of x together; that loses, of each eight aligned products, what
+ * lies below 2^-13 of the largest (toward zero). Rows of MXG_MXFP8_FAST all go by it, up
+ * to twice as fast for many rows: each eight products may be off by 7 * 2^-13 of the
+ * largest of them, so that a result is as good as its BF16 rounding unless its sum
+ * cancels to less than its products. Products and sums below 2^-149 are lost, a result or partial sum beyond the
+ * FP32 range is infinite or NaN, and a scale byte 255 or an e4m3fn NaN makes NaN of what
+ * it enters.
  *
  *   w         with experts == 1
- *   x_format  MXG_MXFP4 (with an MXFP4 weight) or MXG_MXFP8
+ *   x_format  MXG_MXFP4 (with an MXFP4 weight), MXG_MXFP8 or MXG_MXFP8_FAST
  *   x, x_scale  device, [rows, k] codes (16-B aligned), [rows, k/32] (4-B)
  *   rows      1..MXG_ROWS_MAX
  *   workspace device, at least mxrows_workspace_bytes(), 16-B aligned; one call at

@@ -56,7 +56,7 @@ MOE_MAX_PAIRS = 1024
 LORA_MAX_RANK = 128
 
 F16 = 2
-MXFP4, MXFP8 = 4, 8
+MXFP4, MXFP8, MXFP8_FAST = 4, 8, 9
 ROWS_MAX = 1 << 24
 ROWS_MAX_N = 1 << 20
 ROWS_MAX_K = 65536

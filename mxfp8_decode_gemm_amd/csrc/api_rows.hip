@@ -17,6 +17,7 @@ int hip_code(hipError_t e) { return e == hipSuccess ? MXG_OK : MXG_EHIP; }
 
 bool type_ok(int32_t t) { return t == MXG_F32 || t == MXG_BF16 || t == MXG_F16; }
 bool format_ok(int32_t f) { return f == MXG_MXFP4 || f == MXG_MXFP8; }
+bool x_format_ok(int32_t f) { return format_ok(f) || f == MXG_MXFP8_FAST; }
 bool rows_ok(int64_t rows) { return rows >= 1 && rows <= MXG_ROWS_MAX; }
 bool weight_ok(int32_t format, int32_t experts, int32_t n, int32_t k) {
   return format_ok(format) && experts >= 1 && experts <= MXG_MOE_MAX_EXPERTS && n >= 8 &&
@@ -38,7 +39,8 @@ bool weight_shape_ok(const mxrows_weight* w) {
 }
 
 // Sizes of a call (the pointers are the caller's to set).
-RowsArgs rows_args(const mxrows_weight* w, int32_t rows, const int32_t* offsets) {
+RowsArgs rows_args(const mxrows_weight* w, int32_t x_format, int32_t rows,
+                   const int32_t* offsets) {
   RowsArgs a = {};
   a.offsets = offsets;
   a.w_bytes = packed_expert_bytes(w->format, w->n, w->k);
@@ -48,6 +50,7 @@ RowsArgs rows_args(const mxrows_weight* w, int32_t rows, const int32_t* offsets)
   a.k = w->k;
   a.gated = w->gated;
   a.rows = rows;
+  a.fast = x_format == MXG_MXFP8_FAST;
   a.out_n = w->gated ? w->n / 2 : w->n;
   a.nb = (int32_t)row_blocks(w->n);
   a.kp = (int32_t)kb_pairs(w->k);
@@ -65,17 +68,37 @@ RowsArgs rows_args(const mxrows_weight* w, int32_t rows, const int32_t* offsets)
 // Experts, 64 of 4096 x k gated, by rows of each: k 512, 1 row 25 and 15; k 2048, 1 and 4
 // rows 36 and 34, 53 and 49 (MXFP8 54 and 63, 80 and 93), 8 rows 61 and 52; k 4096, 8 and 16
 // rows 100 and 107, 138 and 105.
-bool by_tiles(const RowsArgs& a, int x_format) {
+//
+// MXFP8 rows in BF16, W in MXFP4 and in MXFP8. One weight: 4096 x 2048 3.7 and 4.4 with 8
+// rows, 4.3 and 4.9 with 16, 5.2 and 6.2 with 32, 4096 x 16384 16 and 19, 17 and 23, 26 and
+// 36. Either side of the border, streamed and by tiles: 32 rows of 7168 x 8192 14 and 19
+// (MXFP8 20 and 23), 64 27 and 20 (36 and 24); 128 of 1024 x 8192 14.5 and 14.9 (19.3 and
+// 14.9), of 4096 x 4096 15.6 and 17.1 (20.4 and 17.2), 256 28.9 and 22.4 (39 and 22).
+// Experts, 64 of 4096 x 2048 gated: 8 rows 69 and 113 (99 and 132), 16 105 and 117 (143 and
+// 135), 32 128 and 129 (177 and 147); of 2048 x 2048 8 rows 42 and 57 (58 and 67), 16 63 and
+// 57 (91 and 70); 8 of 2048 x 2048 with 16 rows 8.1 and 14 (11 and 15), with 32 16 and 15 (20
+// and 15).
+bool by_tiles(const RowsArgs& a, int w_format, int x_format) {
+  const bool bf16 = x_format == MXG_MXFP8 && !a.fast;
   if (a.offsets) {
-    const int32_t mean = a.rows / (a.experts < a.rows ? a.experts : a.rows);
+    const int32_t groups = a.experts < a.rows ? a.experts : a.rows, mean = a.rows / groups;
+    const int64_t columns = (int64_t)groups * (a.gated ? a.nb / 2 : a.nb);
+    if (bf16) return mean > (columns <= 1024 ? 16 : 8);
     return !((mean <= 4 && a.kp >= 8) || (mean <= 8 && a.kp >= 16));
   }
-  const bool fp4 = x_format == MXG_MXFP4;
+  const bool fp4 = bf16 ? w_format == MXG_MXFP4 : x_format == MXG_MXFP4;
   const int64_t chunks = (a.rows + 31) / 32;
-  const double pair = a.rows <= 8    ? (fp4 ? 0.18 : 0.35)
-                      : a.rows <= 16 ? (fp4 ? 0.22 : 0.39)
-                                     : (fp4 ? 0.36 : 0.57);
-  const double streamed = (double)((a.nb * chunks + 255) / 256) * (1.5 + a.kp * pair);
+  double pair;
+  if (bf16)
+    pair = a.rows <= 8    ? (fp4 ? 0.22 : 0.27)
+           : a.rows <= 16 ? (fp4 ? 0.24 : 0.32)
+                          : (fp4 ? 0.37 : 0.55);
+  else
+    pair = a.rows <= 8    ? (fp4 ? 0.18 : 0.35)
+           : a.rows <= 16 ? (fp4 ? 0.22 : 0.39)
+                          : (fp4 ? 0.36 : 0.57);
+  const double streamed = (double)((a.nb * chunks + 255) / 256) * ((bf16 ? 2 : 1.5) + a.kp * pair) +
+                          (bf16 ? 0.3 * (double)(chunks - 1) : 0);
   return rows_tile_us(a, x_format) < streamed;
 }
 
@@ -84,14 +107,14 @@ int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const 
               const int32_t* offsets, int32_t rows, void* workspace, size_t workspace_bytes,
               uint16_t* out, void* stream) {
   if (!w || !w->w || !w->scale || !x || !x_scale || !out) return MXG_EINVAL;
-  if (!weight_shape_ok(w) || !format_ok(x_format) || !rows_ok(rows)) return MXG_EINVAL;
+  if (!weight_shape_ok(w) || !x_format_ok(x_format) || !rows_ok(rows)) return MXG_EINVAL;
   if (!aligned(w->w, 16) || !aligned(w->scale, 16) || !aligned(x, 16) || !aligned(x_scale, 4) ||
       !aligned(out, 16))
     return MXG_EALIGN;
   if (w->format == MXG_MXFP8 && x_format == MXG_MXFP4) return MXG_EUNSUPPORTED;
   const int64_t x_row = x_format == MXG_MXFP4 ? w->k / 2 : w->k;
   if (gather && (int64_t)x_rows * x_row >= ((int64_t)1 << 32)) return MXG_EUNSUPPORTED;
-  RowsArgs a = rows_args(w, rows, offsets);
+  RowsArgs a = rows_args(w, x_format, rows, offsets);
   a.w = w->w;
   a.ws = w->scale;
   a.x = x;
@@ -103,7 +126,8 @@ int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const 
   a.gather_inv = gather > 1 ? (uint32_t)(((uint64_t)1 << 32) / gather + 1) : 0;
   a.scatter = scatter;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (!by_tiles(a, x_format)) return hip_code(launch_rows_stream(a, w->format, x_format, s));
+  if (!by_tiles(a, w->format, x_format))
+    return hip_code(launch_rows_stream(a, w->format, x_format, s));
   const size_t needed = rows_tile_workspace(a, x_format);
   if (needed) {
     if (!workspace || workspace_bytes < needed) return MXG_EWORKSPACE;
@@ -158,9 +182,10 @@ int mxrows_pack_weight(int32_t format, const uint8_t* w, const uint8_t* w_scale,
 }
 
 size_t mxrows_workspace_bytes(const mxrows_weight* w, int32_t x_format, int32_t rows) {
-  if (!weight_shape_ok(w) || w->experts != 1 || !format_ok(x_format) || !rows_ok(rows)) return 0;
-  const RowsArgs a = rows_args(w, rows, nullptr);
-  return by_tiles(a, x_format) ? rows_tile_workspace(a, x_format) : 0;
+  if (!weight_shape_ok(w) || w->experts != 1 || !x_format_ok(x_format) || !rows_ok(rows))
+    return 0;
+  const RowsArgs a = rows_args(w, x_format, rows, nullptr);
+  return by_tiles(a, w->format, x_format) ? rows_tile_workspace(a, x_format) : 0;
 }
 
 int mxrows_product(const mxrows_weight* w, int32_t x_format, const uint8_t* x,

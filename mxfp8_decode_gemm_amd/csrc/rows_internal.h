@@ -32,6 +32,7 @@ struct RowsArgs {
   const int32_t* order;   // or null
   int64_t w_bytes, ws_bytes;  // of one expert
   int32_t experts, n, k, gated, rows, x_rows, gather, scatter;
+  int32_t fast;           // MXG_MXFP8_FAST
   int32_t out_n, nb, kp;  // columns of out; row blocks of a weight, pairs of kb
   // floor(2^32 / gather) + 1: o / gather is the high word of its product with o, for o
   // below 2^24 and gather from 2 to 32 (the product's excess is below o 2^-32).
@@ -44,6 +45,9 @@ hipError_t launch_rows_stream(const RowsArgs& a, int w_format, int x_format, hip
 size_t rows_tile_workspace(const RowsArgs& a, int x_format);
 double rows_tile_us(const RowsArgs& a, int x_format);  // about its time
 hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, hipStream_t s);
+// Its tiles for MXFP8 rows that are not to be `fast` (rows_bf16.hip).
+hipError_t launch_rows_bf16(const RowsArgs& a, int w_format, int row_tiles, int col_tiles,
+                            int split, hipStream_t s);
 
 hipError_t launch_rows_pack(int format, const uint8_t* w, const uint8_t* ws, int experts, int n,
                             int k, uint8_t* wp, uint8_t* wsp, hipStream_t s);

@@ -9,9 +9,11 @@
 // L2) into registers and feeds both to the scaled MFMA as they are; the partial
 // tiles meet in LDS and are summed in ascending K order.
 //
-// One row of 7168 x 8192 in MXFP4 7.7 us (31 MB, 4.1 TB/s: less than a round trip to
-// memory for each CU), 8 in MXFP8 14.8 us (4.1 TB/s); 8 tokens x 8 of 64 experts of
-// 4096 x 7168 gated, MXFP4 by MXFP8, 108 us (656 MB, 6.1 TB/s). Left out: units in a
+// MXFP8 rows go through BF16 (BF; rows_device.h) unless they are to be fast.
+//
+// One row of 7168 x 8192 in MXFP4 7.7 us (31 MB, 4.1 TB/s; a wave asks for the next 256 of K
+// when it has multiplied the last), 8 in MXFP8 13.0 us (4.7 TB/s; fast 14.4); 8 tokens x 8 of
+// 64 experts of 4096 x 7168 gated, MXFP4 by MXFP8, 106 us (656 MB, 6.2 TB/s; fast 101). Left out: units in a
 // register ring of 2 to 6 (experts slower, one weight level), 16 waves, 64 rows of x.
 
 #include <hip/hip_runtime.h>
@@ -24,8 +26,9 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
 
-template <int FW, int FX, bool GATED>
-__global__ void __launch_bounds__(kThreads) rows_stream_kernel(RowsArgs a) {
+// BF: MXFP8 contracted in BF16 (rows_device.h).
+template <int FW, int FX, bool GATED, bool BF>
+__global__ void __launch_bounds__(kThreads, 4) rows_stream_kernel(RowsArgs a) {
   constexpr int RW = GATED ? 2 : 1;
   constexpr int kTile = 32;
   __shared__ float red[kWaves][RW][16][64];
@@ -61,6 +64,7 @@ __global__ void __launch_bounds__(kThreads) rows_stream_kernel(RowsArgs a) {
 #pragma unroll
     for (int q = 0; q < 16; ++q) acc[i][q] = 0.f;
 
+  uint32_t again = 0;  // (BF) not 0 where BF16 did not hold a value
   const int kbs = a.k >> 7;
   const int p0 = wave * a.kp / kWaves, p1 = (wave + 1) * a.kp / kWaves;
   for (int p = p0; p < p1; ++p) {
@@ -97,13 +101,56 @@ __global__ void __launch_bounds__(kThreads) rows_stream_kernel(RowsArgs a) {
           }
         }
       }
+      if constexpr (BF) {
+        uint32_t z = well_inside(sx);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          const uint32_t inside = well_inside(sw[i]);
+          z &= h ? inside | 0x8080u : inside | 0x80800000u;
+        }
+        const bool check = !__all(all_inside(z));
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const BlockScales xs = {sx >> (16 * s) & 0xFFu, sx >> (16 * s + 8) & 0xFFu};
+          if (check) again |= leaves_bf16(xp[s], xs);
+          const Bf16Piece xb = to_bf16(xp[s], xs);
+#pragma unroll
+          for (int i = 0; i < RW; ++i) {
+            const auto both = __builtin_amdgcn_permlane32_swap(sw[i], sw[i], false, false);
+            const int shift = 8 * (2 * h + s);
+            const BlockScales w = {both[0] >> shift & 0xFFu, both[1] >> shift & 0xFFu};
+            const Piece<FW> p = by_blocks(wp[i][s]);
+            if (check) again |= leaves_bf16(p, w);
+            acc[i] = product(to_bf16(p, w), xb, acc[i]);
+            // (One operand of W after the other: two workgroups' registers on a CU.)
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          // (Shifted here, after the loads have been issued.)
+          const uint32_t s = h ? sw[i] >> 16 : sw[i], x = sx >> (8 * g);
+          acc[i] = product<FW, FX, 0, 0>(wp[i][0], s, xp[0], x, acc[i]);
+          acc[i] = product<FW, FX, 1, 2>(wp[i][1], s, xp[1], x, acc[i]);
+        }
+      }
+    }
+  }
+
+  if constexpr (BF) {
+    if (__any(again != 0)) {
+      const uint8_t *wu[RW], *xu[1] = {xr}, *xsu[1] = {xsr};
+      const uint32_t* wsu[RW];
+      v16f sums[RW][1];
 #pragma unroll
       for (int i = 0; i < RW; ++i) {
-        // (Shifted here, after the loads have been issued.)
-        const uint32_t s = h ? sw[i] >> 16 : sw[i], x = sx >> (8 * g);
-        acc[i] = product<FW, FX, 0, 0>(wp[i][0], s, xp[0], x, acc[i]);
-        acc[i] = product<FW, FX, 1, 2>(wp[i][1], s, xp[1], x, acc[i]);
+        wu[i] = w[i] - 16 * lane;
+        wsu[i] = ws[i] - lane;
       }
+      contract_again<FW>(wu, wsu, xu, xsu, 2 * p0, 2 * p1, kbs, 0, 2, sums);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) acc[i] = sums[i][0];
     }
   }
 
@@ -139,24 +186,27 @@ __global__ void __launch_bounds__(kThreads) rows_stream_kernel(RowsArgs a) {
   }
 }
 
-template <int FW, int FX>
+template <int FW, int FX, bool BF>
 hipError_t launch(const RowsArgs& a, hipStream_t s) {
   const int64_t most = a.rows / 32 + (a.experts < a.rows ? a.experts : a.rows);
   const dim3 grid((unsigned)(a.offsets ? most : (a.rows + 31) / 32),
                   (unsigned)(a.gated ? a.nb / 2 : a.nb));
   if (a.gated)
-    hipLaunchKernelGGL((rows_stream_kernel<FW, FX, true>), grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((rows_stream_kernel<FW, FX, true, BF>), grid, dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((rows_stream_kernel<FW, FX, false>), grid, dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((rows_stream_kernel<FW, FX, false, BF>), grid, dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_rows_stream(const RowsArgs& a, int w_format, int x_format, hipStream_t s) {
-  if (x_format == MXG_MXFP4) return launch<MXG_MXFP4, MXG_MXFP4>(a, s);
-  if (w_format == MXG_MXFP4) return launch<MXG_MXFP4, MXG_MXFP8>(a, s);
-  return launch<MXG_MXFP8, MXG_MXFP8>(a, s);
+  if (x_format == MXG_MXFP4) return launch<MXG_MXFP4, MXG_MXFP4, false>(a, s);
+  if (w_format == MXG_MXFP4)
+    return a.fast ? launch<MXG_MXFP4, MXG_MXFP8, false>(a, s)
+                  : launch<MXG_MXFP4, MXG_MXFP8, true>(a, s);
+  return a.fast ? launch<MXG_MXFP8, MXG_MXFP8, false>(a, s)
+                : launch<MXG_MXFP8, MXG_MXFP8, true>(a, s);
 }
 
 }  // namespace mxg

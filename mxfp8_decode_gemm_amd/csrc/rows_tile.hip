@@ -1,5 +1,6 @@
 // Products of many rows (gfx950): mxrows_product and mxmoe_grouped of
-// include/mxrows.h where the matrix cores bound them.
+// include/mxrows.h where the matrix cores bound them, of MXFP4 rows and of MXFP8 rows that are
+// to be fast (rows_bf16.hip takes the others).
 //
 //   y[r][n] = sum over blocks b of 32 of 2^(sw[n][b] + sx[r][b] - 254) sum of w[n][.] x[r][.]
 //
@@ -33,40 +34,13 @@
 #include <cmath>
 #include <type_traits>
 
-#include "rows_device.h"
+#include "tile_device.h"
 
 namespace mxg {
 namespace {
 
 template <int N>
 using Int = std::integral_constant<int, N>;
-
-// 1024 bytes from base + off (a lane's 16) to LDS at `to` (wave-uniform), and
-// COUNT - 1 times the next 1024 to the next 1024. The compiler does not see these
-// loads: their end is waited for with s_waitcnt vmcnt.
-template <int COUNT>
-__device__ __forceinline__ void copy_kib(uint32_t to, const uint8_t* base, uint32_t off) {
-  to = __builtin_amdgcn_readfirstlane(to);
-  static_assert(COUNT == 1 || COUNT == 2 || COUNT == 4, "");
-  if constexpr (COUNT == 1)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 ::"s"(to), "v"(off), "s"(base) : "memory");
-  else if constexpr (COUNT == 2)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
-                 "global_load_lds_dwordx4 %1, %2 offset:1024"
-                 ::"s"(to), "v"(off), "s"(base) : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
-                 "global_load_lds_dwordx4 %1, %2 offset:1024\n\t"
-                 "global_load_lds_dwordx4 %1, %2 offset:2048\n\t"
-                 "global_load_lds_dwordx4 %1, %2 offset:%3"
-                 ::"s"(to), "v"(off), "s"(base), "n"(3 * 1024) : "memory");
-}
-// 256 bytes, 4 a lane.
-__device__ __forceinline__ void copy_words(uint32_t to, const uint8_t* base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-               ::"s"(to), "v"(off), "s"(base) : "memory");
-}
 
 // A tile's geometry. A stage is kLine bytes of each row of x (of 64: 128 values in MXFP4,
 // two MFMA steps, 64 in MXFP8, one) with the same K of W; a ring of them lies in LDS.
@@ -131,26 +105,6 @@ struct Tile {
   static_assert(kWaves * 32 * kOutRow <= kScales, "");
 };
 
-// Tile `number` of a launch: eight row tiles side by side down the columns, so that
-// neighbours share W and x.
-__device__ __forceinline__ void tile_at(int number, int row_tiles, int col_tiles, int* ct,
-                                        int* rt) {
-  constexpr int kGroup = 8;
-  const int group = row_tiles <= kGroup ? 0 : number / (kGroup * col_tiles);
-  const int high = min(kGroup, row_tiles - group * kGroup);
-  const int in = number - group * kGroup * col_tiles;
-  *ct = high == kGroup ? in / kGroup : in / high;
-  *rt = group * kGroup + (in - *ct * high);
-}
-
-constexpr int kRun = 32;  // tiles side by side on one XCD
-
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  static_assert(N < 64, "");
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
-
 template <int FW, int FX, int RW, int RX, int WW, int WX, bool DEEP>
 __global__ void __launch_bounds__(64 * WW * WX)
 __attribute__((amdgpu_waves_per_eu(Tile<FW, FX, RW, RX, WW, WX, DEEP>::kResident)))
@@ -162,11 +116,7 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
   const int ww = wave % WW, wx = wave / WW;
   const int r32 = lane & 31, g = lane >> 5;
 
-  // Workgroups go to the XCDs in turn: runs of 32 tiles stay on one, of fewer where
-  // there are not 256.
-  const int run_of = min((int)gridDim.x / 8, kRun), bid = blockIdx.x;
-  const int round = bid / (8 * kRun) * (8 * kRun);
-  const int at = round + (bid & 7) * run_of + ((bid - round) >> 3);
+  const int at = tile_of_workgroup();
   if (at >= row_tiles * col_tiles * split) return;
   // The tiles of one part of K after the other: those of a run share its rows of x.
   const int tiles = row_tiles * col_tiles;
@@ -607,31 +557,50 @@ double join_time(int split, double rows, double n) {
   return 3 + 0.4 * split + split * rows * n * 8 / 3.5e6;
 }
 
+// Tiles of 128 in BF16 (rows_bf16.hip) with up to 64 rows of x and with up to 128: 2048 x
+// 2048 13.6 and 18.3, 4096 x 4096 22.6 and 31, 1024 x 8192 41 and 56; 224 of 8192 59 (MXFP4)
+// and 65. With 2, 4 and 8 parts of 64 rows 128 rows of 1024 x 8192 25.8, 17.3 and 14.9, of 4096
+// x 4096 18.5 and 17.1 with 2 and 4; 203 of 4096 x 16384 40.6 with 4 by 128, 47 with 2 by 64.
+double bf16_time(int64_t tiles, int64_t rows, double kp) {
+  return (double)((tiles + 255) / 256) * (rows <= 64 ? 4.4 + 1.15 * kp : 5.5 + 1.58 * kp);
+}
+double bf16_join_time(int split, double rows, double n) {
+  return 2 + 0.2 * split + split * rows * n * 8 / 3.5e6;
+}
+
 Shape shape_of(const RowsArgs& a, int x_format) {
   Shape big = {256, row_tiles(a, 256), (a.nb + 7) / 8, 1, 0};
   Shape s = {128, row_tiles(a, 128), (a.nb + 3) / 4, 1, 0};
+  const bool bf16 = x_format == MXG_MXFP8 && !a.fast;
   if (a.offsets) {
     // Groups end in tiles that are half empty on average; only many rows a group, and
     // more tiles than CUs, make up for the larger tile's.
     const int64_t groups = a.experts < a.rows ? a.experts : a.rows;
     const int64_t tiles = (a.rows / 256 + groups / 2) * big.col_tiles;
-    return a.rows / groups >= 256 && tiles >= 256 ? big : s;
+    return !bf16 && a.rows / groups >= 256 && tiles >= 256 ? big : s;
   }
   const bool fp4 = x_format == MXG_MXFP4;
-  const int64_t tiles = s.row_tiles * s.col_tiles;
+  const int64_t blocks = (a.rows + 31) / 32;
   const double read = 2.5 + (double)a.w_bytes / 6.2e6;  // W, once
-  s.us = fmax(small_time(tiles, a.kp, fp4), read);
-  for (int split = 2; split <= 16 && tiles * split <= 256 && a.kp >= 2 * split; split *= 2) {
-    const double t = fmax(small_time(tiles, (double)a.kp / split, fp4), read) +
-                     join_time(split, a.rows, a.n);
-    if (t < s.us) {
-      s.us = t;
-      s.split = split;
+  // Tiles of 128 rows of x, and in BF16 of 64 too, with K whole and divided.
+  s.us = INFINITY;
+  const int64_t col_tiles = s.col_tiles, most = s.row_tiles;
+  for (int64_t row_tiles : {most, bf16 ? (blocks + 1) / 2 : most}) {
+    const int64_t tiles = row_tiles * col_tiles, rows = (blocks + row_tiles - 1) / row_tiles * 32;
+    for (int split = 1; split <= 16; split *= 2) {
+      if (split > 1 && (tiles * split > 256 || a.kp < 2 * split)) break;
+      const double kp = (double)a.kp / split;
+      const double join = split == 1 ? 0
+                          : bf16     ? bf16_join_time(split, a.rows, a.n)
+                                     : join_time(split, a.rows, a.n);
+      const double t =
+          fmax(bf16 ? bf16_time(tiles, rows, kp) : small_time(tiles, kp, fp4), read) + join;
+      if (t < s.us) s = Shape{128, row_tiles, col_tiles, split, t};
     }
   }
+  if (bf16) return s;
   // Of large tiles as many down the rows as the last round of workgroups has room for:
   // lower ones.
-  const int64_t blocks = (a.rows + 31) / 32;
   const int64_t rounds = (big.row_tiles * big.col_tiles + 255) / 256;
   const int64_t fit = rounds * 256 / big.col_tiles;
   if (fit > big.row_tiles) big.row_tiles = fit < blocks ? fit : blocks;
@@ -644,28 +613,27 @@ template <int FW, int FX, int RW, int RX, int WW, int WX, bool DEEP>
 hipError_t launch(const RowsArgs& a, const Shape& h, hipStream_t s) {
   using T = Tile<FW, FX, RW, RX, WW, WX, DEEP>;
   static_assert(T::kRows == 32 * T::kNW, "");
-  const int64_t tiles = h.row_tiles * h.col_tiles * h.split;
-  const int64_t unit = tiles < 8 * kRun ? 8 : 8 * kRun;
-  const int64_t grid = (tiles + unit - 1) / unit * unit;
-  if (grid * T::kThreads > UINT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((rows_tile_kernel<FW, FX, RW, RX, WW, WX, DEEP>), dim3((unsigned)grid),
+  const unsigned grid = tile_grid(h.row_tiles * h.col_tiles * h.split, T::kThreads);
+  if (grid == 0) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((rows_tile_kernel<FW, FX, RW, RX, WW, WX, DEEP>), dim3(grid),
                      dim3(T::kThreads), 0, s, a, (int)h.row_tiles, (int)h.col_tiles, h.split);
-  if constexpr (T::kSplits)
-    if (h.split > 1) {
-      const dim3 joins((unsigned)(h.row_tiles * h.col_tiles * T::kWaves * RX), a.gated ? RW : 2 * RW);
-      if (a.gated)
-        hipLaunchKernelGGL((join_kernel<RW, RX, WW, WX, true>), joins, dim3(64), 0, s, a,
-                           (int)h.row_tiles, (int)h.col_tiles, h.split);
-      else
-        hipLaunchKernelGGL((join_kernel<RW, RX, WW, WX, false>), joins, dim3(64), 0, s, a,
-                           (int)h.row_tiles, (int)h.col_tiles, h.split);
-    }
+  return hipGetLastError();
+}
+
+// (of tiles of 128 by 128)
+hipError_t launch_join(const RowsArgs& a, const Shape& h, hipStream_t s) {
+  const dim3 joins((unsigned)(h.row_tiles * h.col_tiles * 8), a.gated ? 2 : 4);
+  if (a.gated)
+    hipLaunchKernelGGL((join_kernel<2, 2, 2, 2, true>), joins, dim3(64), 0, s, a,
+                       (int)h.row_tiles, (int)h.col_tiles, h.split);
+  else
+    hipLaunchKernelGGL((join_kernel<2, 2, 2, 2, false>), joins, dim3(64), 0, s, a,
+                       (int)h.row_tiles, (int)h.col_tiles, h.split);
   return hipGetLastError();
 }
 
 template <int FW, int FX>
-hipError_t by_size(const RowsArgs& a, hipStream_t s) {
-  const Shape h = shape_of(a, FX);
+hipError_t by_size(const RowsArgs& a, const Shape& h, hipStream_t s) {
   if (h.side == 256) return launch<FW, FX, 2, 8, 4, 1, false>(a, h, s);
   return h.row_tiles * h.col_tiles * h.split <= 256 ? launch<FW, FX, 2, 2, 2, 2, true>(a, h, s)
                                                     : launch<FW, FX, 2, 2, 2, 2, false>(a, h, s);
@@ -681,9 +649,17 @@ size_t rows_tile_workspace(const RowsArgs& a, int x_format) {
 double rows_tile_us(const RowsArgs& a, int x_format) { return shape_of(a, x_format).us; }
 
 hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, hipStream_t s) {
-  if (x_format == MXG_MXFP4) return by_size<MXG_MXFP4, MXG_MXFP4>(a, s);
-  if (w_format == MXG_MXFP4) return by_size<MXG_MXFP4, MXG_MXFP8>(a, s);
-  return by_size<MXG_MXFP8, MXG_MXFP8>(a, s);
+  const Shape h = shape_of(a, x_format);
+  hipError_t e;
+  if (x_format == MXG_MXFP4)
+    e = by_size<MXG_MXFP4, MXG_MXFP4>(a, h, s);
+  else if (!a.fast)
+    e = launch_rows_bf16(a, w_format, (int)h.row_tiles, (int)h.col_tiles, h.split, s);
+  else if (w_format == MXG_MXFP4)
+    e = by_size<MXG_MXFP4, MXG_MXFP8>(a, h, s);
+  else
+    e = by_size<MXG_MXFP8, MXG_MXFP8>(a, h, s);
+  return e == hipSuccess && h.split > 1 ? launch_join(a, h, s) : e;
 }
 
 }  // namespace mxg

@@ -590,7 +590,7 @@ class _RowsWeight:
     w = property(lambda self: self._packed[0])
     w_scale = property(lambda self: self._packed[1])
 
-    def _pack(self, w, w_scale, gated, activation, stream) -> None:
+    def _pack(self, w, w_scale, gated, activation, fast, stream) -> None:
         _refuse(w, "w", torch.uint8, (None, None, None), None)
         e, n, width = w.shape
         dev = self.device = w.device
@@ -609,6 +609,7 @@ class _RowsWeight:
         if (self.format, self.activation) == (mx.MXFP8, mx.MXFP4):
             raise ValueError("activation: an MXFP8 weight takes MXFP8 activations")
         self.gated, self.out_n = bool(gated), n // 2 if gated else n
+        self._mxfp8 = mx.MXFP8_FAST if fast else mx.MXFP8  # MXFP8 rows, to the library
         handle = _on(dev, stream)
         wp = _fresh(w, (nbytes,), torch.uint8, stream)
         wsp = _fresh(w, (mx.mxrows_packed_scale_bytes(self.format, e, n, self.k),), torch.uint8,
@@ -626,8 +627,9 @@ class _RowsWeight:
         if x_scale is None:
             _address(x, "x", torch.bfloat16, (rows, k), dev)
             x, x_scale = _QUANTIZE[self.activation](x, stream=stream)
-            return self.activation, x, x_scale, x.data_ptr(), x_scale.data_ptr()
-        kind = mx.MXFP4 if 2 * x.shape[1] == k else mx.MXFP8
+            kind = mx.MXFP4 if self.activation == mx.MXFP4 else self._mxfp8
+            return kind, x, x_scale, x.data_ptr(), x_scale.data_ptr()
+        kind = mx.MXFP4 if 2 * x.shape[1] == k else self._mxfp8
         px = _address(x, "x", torch.uint8, (rows, k // 2 if kind == mx.MXFP4 else k), dev)
         return kind, x, x_scale, px, _address(x_scale, "x_scale", torch.uint8, (rows, k // 32), dev)
 
@@ -636,14 +638,16 @@ class Linear(_RowsWeight):
     """A projection [n, k] in MXFP4 or MXFP8, packed once, for any number of rows
     (``Operands`` and ``publish`` are the projection of at most 8). gated: the rows are
     [gate; up], and a result is silu(gate) * up of them. activation ("mxfp4" or "mxfp8",
-    by default the weight's format): what BF16 rows are quantized to."""
+    by default the weight's format): what BF16 rows are quantized to. fast: products of MXFP8
+    rows may lose what lies 2^-13 below the largest of eight (mxrows.h says when that
+    matters); many rows then take about half the time."""
 
     def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, gated: bool = False,
-                 activation: str = None, stream=None) -> None:
+                 activation: str = None, stream=None, fast: bool = False) -> None:
         _refuse(w, "w", torch.uint8, (None, None), None)
         if not isinstance(w_scale, torch.Tensor) or w_scale.dim() != 2:
             raise ValueError("w_scale: a device tensor [n, k/32] is needed")
-        self._pack(w.unsqueeze(0), w_scale.unsqueeze(0), gated, activation, stream)
+        self._pack(w.unsqueeze(0), w_scale.unsqueeze(0), gated, activation, fast, stream)
 
     def __call__(self, x: torch.Tensor, x_scale: torch.Tensor = None, out: torch.Tensor = None,
                  stream=None) -> torch.Tensor:
@@ -700,11 +704,11 @@ def sort_pairs(ids: torch.Tensor, experts: int, order: torch.Tensor = None,
 class GroupedLinear(_RowsWeight):
     """Every expert's projection in MXFP4 or MXFP8 (uint8 codes [experts, n, k/2] or
     [experts, n, k], scale bytes [experts, n, k/32]), packed once, on the rows of its
-    pairs. gated and activation: as ``Linear``."""
+    pairs. gated, activation and fast: as ``Linear``."""
 
     def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, gated: bool = False,
-                 activation: str = None, stream=None) -> None:
-        self._pack(w, w_scale, gated, activation, stream)
+                 activation: str = None, stream=None, fast: bool = False) -> None:
+        self._pack(w, w_scale, gated, activation, fast, stream)
 
     def __call__(self, x: torch.Tensor, x_scale, offsets: torch.Tensor,
                  order: torch.Tensor = None, gather: int = 0, scatter: bool = False,
@@ -765,12 +769,15 @@ class PromptExperts:
     """The experts of one layer on a prompt's rows, where ``Experts`` takes a decode step's
     (at most 1024 pairs): w13 [experts, 2 inter, hidden] (gate rows, then up rows) and w2
     [experts, hidden, inter] in MXFP4 or MXFP8, packed once. activation ("mxfp4" or "mxfp8",
-    by default each weight's format): what the rows of both products are quantized to."""
+    by default each weight's format): what the rows of both products are quantized to. fast:
+    as ``Linear``."""
 
     def __init__(self, w13: torch.Tensor, w13_scale: torch.Tensor, w2: torch.Tensor,
-                 w2_scale: torch.Tensor, activation: str = None, stream=None) -> None:
-        self.up = GroupedLinear(w13, w13_scale, gated=True, activation=activation, stream=stream)
-        self.down = GroupedLinear(w2, w2_scale, activation=activation, stream=stream)
+                 w2_scale: torch.Tensor, activation: str = None, stream=None,
+                 fast: bool = False) -> None:
+        self.up = GroupedLinear(w13, w13_scale, gated=True, activation=activation, stream=stream,
+                                fast=fast)
+        self.down = GroupedLinear(w2, w2_scale, activation=activation, stream=stream, fast=fast)
         self.experts, self.hidden, self.inter = self.up.experts, self.up.k, self.up.out_n
         if (self.down.experts, self.down.n, self.down.k) != (self.experts, self.hidden, self.inter):
             raise ValueError("w2: [experts, hidden, inter] of w13 is needed")

@@ -6,8 +6,9 @@ return how far a result may be off before its rounding to BF16; ``bf16_bound`` a
 
 * an FP32 sum of K products, taken eight at a time: at most K/8 additions, and 16 more where partial sums of
   waves meet, each off by no more than 2^-23 of the sum of magnitudes;
-* with MXFP8 on either side the matrix instruction drops, of eight products at aligned K, what lies below 2^-13 of
-  the largest: at most 7 * 2^-13 of it. The largest magnitudes of the eight of W and of x bound that product;
+* with MXFP8 rows that are to be fast, or that BF16 does not hold with their scales (a scale byte outside 3..246 beside
+  a nonzero code, in W or x), the matrix instruction drops, of eight products at aligned K, what lies below 2^-13 of the
+  largest: at most 7 * 2^-13 of it. The largest magnitudes of the eight of W and of x bound that product;
 * silu and its product in FP32: (10 + |gate|) * 2^-23 of the result (exp, add, reciprocal and multiplies at no more
   than 2 ulp each; the exponent -|gate| log2(e), rounded to 2^-24 of itself by its product and by its constant, moves
   exp by |gate| 2^-23 of it at most); a change of the gate by d moves silu by at most 1.1 d;
@@ -103,13 +104,19 @@ def is_mxfp8(codes: np.ndarray, scales: np.ndarray) -> bool:
     return codes.shape[-1] == 32 * scales.shape[-1]
 
 
-def product(w, w_scale, x, x_scale, gated=False):
+def leaves_bf16(v, scales):
+    """Whether values, given with their scale bytes, hold a nonzero one whose scale byte is outside 3..246."""
+    outside = np.repeat((scales < 3) | (scales > 246), BLOCK, axis=-1)
+    return bool((outside & (v != 0)).any())
+
+
+def product(w, w_scale, x, x_scale, gated=False, fast=False):
     """(exact, slack) [rows, n]: W x of every row; gated: silu(gate) * up, [rows, n/2]."""
     wv, xv = values(w, w_scale), values(x, x_scale)
     k = wv.shape[1]
     exact = xv @ wv.T
     slack = (k / 8 + 16) * 2.0**-23 * (np.abs(xv) @ np.abs(wv).T)
-    if is_mxfp8(w, w_scale) or is_mxfp8(x, x_scale):
+    if is_mxfp8(x, x_scale) and (fast or leaves_bf16(wv, w_scale) or leaves_bf16(xv, x_scale)):
         largest = lambda v: np.abs(v).reshape(len(v), -1, 8).max(-1)  # noqa: E731
         slack += 7 * 2.0**-13 * (largest(xv) @ largest(wv).T)
     if not gated:
@@ -132,7 +139,8 @@ def sort_pairs(ids, experts):
     return np.array(order, dtype=np.int32), np.array(offsets, dtype=np.int32)
 
 
-def grouped(w, w_scale, x, x_scale, offsets, order=None, gather=0, scatter=False, gated=False, rows=None):
+def grouped(w, w_scale, x, x_scale, offsets, order=None, gather=0, scatter=False, gated=False, rows=None,
+            fast=False):
     """(exact, slack, written) [rows, ...]; written: which rows the experts' pairs lead to."""
     rows = len(x) if rows is None else rows
     width = w.shape[1] // 2 if gated else w.shape[1]
@@ -144,7 +152,7 @@ def grouped(w, w_scale, x, x_scale, offsets, order=None, gather=0, scatter=False
             continue
         src = order[at] // gather if gather else at
         dst = order[at] if scatter else at
-        exact[dst], slack[dst] = product(w[e], w_scale[e], x[src], x_scale[src], gated)
+        exact[dst], slack[dst] = product(w[e], w_scale[e], x[src], x_scale[src], gated, fast)
         written[dst] = True
     return exact, slack, written
 

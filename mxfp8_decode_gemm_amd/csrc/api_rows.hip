@@ -123,7 +123,7 @@ int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const 
   a.order = order;
   a.x_rows = x_rows;
   a.gather = gather;
-  a.gather_inv = gather > 1 ? (uint32_t)(((uint64_t)1 << 32) / gather + 1) : 0;
+  a.over = gather_quotient(gather);
   a.scatter = scatter;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (!by_tiles(a, w->format, x_format))

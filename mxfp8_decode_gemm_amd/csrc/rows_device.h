@@ -261,7 +261,7 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* offsets, int experts
 
 // The row of x that an entry of the order leads to.
 __device__ __forceinline__ int source_of(const RowsArgs& a, uint32_t o) {
-  const int r = (int)(a.gather == 1 ? o : __umulhi(o, a.gather_inv));
+  const int r = (int)(a.gather == 1 ? o : over_gather(o, a.over));
   return min(max(r, 0), a.x_rows - 1);
 }
 

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/mxrows.h"
+#include "gather_quotient.h"
 
 namespace mxg {
 
@@ -34,9 +35,7 @@ struct RowsArgs {
   int32_t experts, n, k, gated, rows, x_rows, gather, scatter;
   int32_t fast;           // MXG_MXFP8_FAST
   int32_t out_n, nb, kp;  // columns of out; row blocks of a weight, pairs of kb
-  // floor(2^32 / gather) + 1: o / gather is the high word of its product with o, for o
-  // below 2^24 and gather from 2 to 32 (the product's excess is below o 2^-32).
-  uint32_t gather_inv;
+  GatherQuotient over;    // of gather, from 2 on
   float* partial;         // workspace of a split K (one weight, all rows), or null
 };
 

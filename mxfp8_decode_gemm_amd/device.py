@@ -787,6 +787,8 @@ class PromptExperts:
         """BF16 x [tokens, hidden], ids and weights as ``route`` returns them; BF16 [tokens,
         hidden]: sort_pairs, both products with the rows quantized before each, combine."""
         tokens, top_k = _matrix(ids, "ids").shape
+        if _matrix(x, "x").shape[0] != tokens:
+            raise ValueError(f"x: {x.shape[0]} rows for the choices of {tokens} tokens")
         order, offsets = sort_pairs(ids, self.experts, stream=stream)
         h = self.up(x, None, offsets, order, gather=top_k, stream=stream)
         y = self.down(h, None, offsets, order, scatter=True, stream=stream)

@@ -496,12 +496,23 @@ class AdaptedLinear:
 
 _TYPES = {torch.float32: mx.F32, torch.bfloat16: mx.BF16, torch.float16: mx.F16}
 _FORMATS = {"mxfp4": mx.MXFP4, "mxfp8": mx.MXFP8}
+_MOST = (1 << 31) - 1
 
 
 def _matrix(t, name: str) -> torch.Tensor:
+    """A device tensor of two dimensions, each in the 32 bits that the library takes sizes in
+    (ctypes cuts a longer number without a word)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name}: a device tensor of two dimensions is needed")
+    rows, width = t.shape
+    if rows > _MOST or width > _MOST:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} is beyond 32 bits")
     return t
+
+
+def _count(value, name: str, most: int) -> None:
+    if not 0 <= value <= most:
+        raise ValueError(f"{name}: {value} is not within 0..{most}")
 
 
 def quantize4(x: torch.Tensor, codes: torch.Tensor = None, scales: torch.Tensor = None,
@@ -544,6 +555,7 @@ def dequantize4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16,
     """One mxfp4_dequantize call: the values of codes [rows, k/2] and scales [rows, k/32]
     as float32, bfloat16 or float16 [rows, k]."""
     rows, half = _matrix(codes, "codes").shape
+    _count(half, "half a row", _MOST // 2)
     dev = codes.device
     handle = _on(dev, stream)
     pc = _address(codes, "codes", torch.uint8, (rows, half), dev)
@@ -597,6 +609,7 @@ class _RowsWeight:
         blocks = w_scale.shape[-1] if isinstance(w_scale, torch.Tensor) and w_scale.dim() else 0
         self.format = mx.MXFP4 if width == 16 * blocks else mx.MXFP8
         self.experts, self.n, self.k = e, n, 32 * blocks
+        _count(max(e, n, self.k), "w's sizes", _MOST)
         if width not in (16 * blocks, 32 * blocks):
             raise ValueError("w: 16 (MXFP4) or 32 (MXFP8) bytes for each scale byte are needed")
         _refuse(w_scale, "w_scale", torch.uint8, (e, n, blocks), dev)
@@ -679,6 +692,7 @@ def sort_pairs(ids: torch.Tensor, experts: int, order: torch.Tensor = None,
     """One mxmoe_sort call on a router's ids [tokens, top_k]: (order int32 [tokens *
     top_k], offsets int32 [experts + 1])."""
     tokens, top_k = _matrix(ids, "ids").shape
+    _count(experts, "experts", mx.MOE_MAX_EXPERTS)
     dev = ids.device
     handle = _on(dev, stream)
     pi = _address(ids, "ids", torch.int32, (tokens, top_k), dev)
@@ -687,7 +701,7 @@ def sort_pairs(ids: torch.Tensor, experts: int, order: torch.Tensor = None,
     else:
         _address(order, "order", torch.int32, (tokens * top_k,), dev)
     if offsets is None:
-        offsets = _fresh(ids, (max(experts, 0) + 1,), torch.int32, stream)
+        offsets = _fresh(ids, (experts + 1,), torch.int32, stream)
     else:
         _address(offsets, "offsets", torch.int32, (experts + 1,), dev)
     nbytes = _lib.mxmoe_sort_workspace_bytes(tokens, top_k, experts)
@@ -721,11 +735,13 @@ class GroupedLinear(_RowsWeight):
         dev = self.device
         handle = _on(dev, stream)
         x_rows = _matrix(x, "x").shape[0]
+        _count(gather, "gather", mx.ROUTE_MAX_TOP_K)
         rows = x_rows
         po = None
         if order is not None:
             rows = order.numel() if isinstance(order, torch.Tensor) else None
             po = _address(order, "order", torch.int32, (rows,), dev)
+            _count(rows, "order's length", mx.ROWS_MAX)
         poff = _address(offsets, "offsets", torch.int32, (self.experts + 1,), dev)
         kind, x, x_scale, px, ps = self._codes(x, x_scale, x_rows, stream)
         if out is None:
@@ -748,6 +764,7 @@ def combine(y: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, experts: 
     and weights as ``route`` returns them; BF16 [tokens, hidden]."""
     tokens, top_k = _matrix(ids, "ids").shape
     hidden = _matrix(y, "y").shape[1]
+    _count(experts, "experts", mx.MOE_MAX_EXPERTS)
     dev = y.device
     handle = _on(dev, stream)
     py = _address(y, "y", torch.bfloat16, (tokens * top_k, hidden), dev)

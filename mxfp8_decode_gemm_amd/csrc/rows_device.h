@@ -188,15 +188,18 @@ __device__ __forceinline__ void contract_again(const uint8_t* const (&w)[RW],
 }
 
 // silu(gate) * up. With E = exp(-|gate|), silu is gate / (1 + E) for a gate from zero
-// on and gate E / (1 + E) below: the reciprocal's argument lies in 1..2, and E as the
-// square of exp2(-|gate| log2(e) / 2) is right down to FP32's subnormals. E is off by
-// |gate| 2^-23 and a few 2^-24 of itself (the exponent's rounding), far below the
-// result's BF16 rounding; expf and a division took twice the time of a tile's
-// epilogue.
+// on and gate E / (1 + E) below: the reciprocal's argument lies in 1..2. E is q^3 of q =
+// exp2(-|gate| log2(e) / 3), and its factors join the product one by one: E and silu
+// leave FP32's normal range from gates of -87 and -91 on, their product with a large up
+// does not (q does at -262, where E is below 2^-377). No partial product overflows
+// where the whole does not: |gate| q / 2 / (1 + E) stays below 0.53, and 2 q follows. E is
+// off by |gate| 2^-23 and a few 2^-24 of itself (the exponent's rounding), far below the
+// result's BF16 rounding; expf and a division took twice the time of a tile's epilogue.
 __device__ __forceinline__ float gated(float gate, float up) {
-  const float q = __builtin_amdgcn_exp2f(fabsf(gate) * -0.72134752f);
-  const float e = q * q;
-  return gate * (gate < 0.f ? e : 1.f) * __builtin_amdgcn_rcpf(1.f + e) * up;
+  const float q = __builtin_amdgcn_exp2f(fabsf(gate) * -0.48089835f);
+  const float f = gate < 0.f ? q : 1.f;
+  const float s = gate * f * (0.5f * __builtin_amdgcn_rcpf(1.f + q * q * q));
+  return s * up * (2.f * f) * f;
 }
 
 // Eight neighbouring columns of lane l's row l % 32 in BF16, from the values that it

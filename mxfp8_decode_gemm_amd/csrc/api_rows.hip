@@ -57,49 +57,9 @@ RowsArgs rows_args(const mxrows_weight* w, int32_t x_format, int32_t rows,
   return a;
 }
 
-// Whether a call runs by tiles of many rows (rows_tile.hip) or streams W for few
-// (rows_stream.hip), by the measured times of both, in us.
-// One weight: a round of 256 workgroups, each of 32 rows of W and 32 of x, streams 4096 x
-// 2048 4.9 and 6.7 (MXFP4 and MXFP8), 4096 x 4096 7.6 and 10.9, 4096 x 16384 25 and 39; with
-// 16 rows 3.4 and 4.7, 5.5 and 7.5, 15 and 27; with 8 at most 13 and 24. Either side of the
-// border, streamed and by tiles: 64 rows of 4096 x 4096 in MXFP4 7.6 and 10.2, 96 13.1 and
-// 12.4; 32 of 7168 x 8192 12.6 and 12.8, 64 23 and 13, in MXFP8 16 15.8 and 16.1, 32 20.7
-// and 16.3; 128 of 2048 x 2048 4.3 and 7.5, 256 8.6 and 7.6.
-// Experts, 64 of 4096 x k gated, by rows of each: k 512, 1 row 25 and 15; k 2048, 1 and 4
-// rows 36 and 34, 53 and 49 (MXFP8 54 and 63, 80 and 93), 8 rows 61 and 52; k 4096, 8 and 16
-// rows 100 and 107, 138 and 105.
-//
-// MXFP8 rows in BF16, W in MXFP4 and in MXFP8. One weight: 4096 x 2048 3.7 and 4.4 with 8
-// rows, 4.3 and 4.9 with 16, 5.2 and 6.2 with 32, 4096 x 16384 16 and 19, 17 and 23, 26 and
-// 36. Either side of the border, streamed and by tiles: 32 rows of 7168 x 8192 14 and 19
-// (MXFP8 20 and 23), 64 27 and 20 (36 and 24); 128 of 1024 x 8192 14.5 and 14.9 (19.3 and
-// 14.9), of 4096 x 4096 15.6 and 17.1 (20.4 and 17.2), 256 28.9 and 22.4 (39 and 22).
-// Experts, 64 of 4096 x 2048 gated: 8 rows 69 and 113 (99 and 132), 16 105 and 117 (143 and
-// 135), 32 128 and 129 (177 and 147); of 2048 x 2048 8 rows 42 and 57 (58 and 67), 16 63 and
-// 57 (91 and 70); 8 of 2048 x 2048 with 16 rows 8.1 and 14 (11 and 15), with 32 16 and 15 (20
-// and 15).
-bool by_tiles(const RowsArgs& a, int w_format, int x_format) {
-  const bool bf16 = x_format == MXG_MXFP8 && !a.fast;
-  if (a.offsets) {
-    const int32_t groups = a.experts < a.rows ? a.experts : a.rows, mean = a.rows / groups;
-    const int64_t columns = (int64_t)groups * (a.gated ? a.nb / 2 : a.nb);
-    if (bf16) return mean > (columns <= 1024 ? 16 : 8);
-    return !((mean <= 4 && a.kp >= 8) || (mean <= 8 && a.kp >= 16));
-  }
-  const bool fp4 = bf16 ? w_format == MXG_MXFP4 : x_format == MXG_MXFP4;
-  const int64_t chunks = (a.rows + 31) / 32;
-  double pair;
-  if (bf16)
-    pair = a.rows <= 8    ? (fp4 ? 0.22 : 0.27)
-           : a.rows <= 16 ? (fp4 ? 0.24 : 0.32)
-                          : (fp4 ? 0.37 : 0.55);
-  else
-    pair = a.rows <= 8    ? (fp4 ? 0.18 : 0.35)
-           : a.rows <= 16 ? (fp4 ? 0.22 : 0.39)
-                          : (fp4 ? 0.36 : 0.57);
-  const double streamed = (double)((a.nb * chunks + 255) / 256) * ((bf16 ? 2 : 1.5) + a.kp * pair) +
-                          (bf16 ? 0.3 * (double)(chunks - 1) : 0);
-  return rows_tile_us(a, x_format) < streamed;
+RowsChoice choice_of(const mxrows_weight* w, int32_t x_format, int32_t rows, bool grouped) {
+  return rows_choice(
+      rows_problem(w->format, x_format, w->experts, w->n, w->k, w->gated != 0, rows, grouped));
 }
 
 int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const uint8_t* x_scale,
@@ -126,15 +86,15 @@ int rows_call(const mxrows_weight* w, int32_t x_format, const uint8_t* x, const 
   a.over = gather_quotient(gather);
   a.scatter = scatter;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (!by_tiles(a, w->format, x_format))
-    return hip_code(launch_rows_stream(a, w->format, x_format, s));
-  const size_t needed = rows_tile_workspace(a, x_format);
+  const RowsChoice c = choice_of(w, x_format, rows, offsets != nullptr);
+  if (c.side == 0) return hip_code(launch_rows_stream(a, w->format, x_format, s));
+  const size_t needed = choice_workspace(c);
   if (needed) {
     if (!workspace || workspace_bytes < needed) return MXG_EWORKSPACE;
     if (!aligned(workspace, 16)) return MXG_EALIGN;
     a.partial = static_cast<float*>(workspace);
   }
-  return hip_code(launch_rows_tile(a, w->format, x_format, s));
+  return hip_code(launch_rows_tile(a, w->format, x_format, c, s));
 }
 }  // namespace
 
@@ -184,8 +144,7 @@ int mxrows_pack_weight(int32_t format, const uint8_t* w, const uint8_t* w_scale,
 size_t mxrows_workspace_bytes(const mxrows_weight* w, int32_t x_format, int32_t rows) {
   if (!weight_shape_ok(w) || w->experts != 1 || !x_format_ok(x_format) || !rows_ok(rows))
     return 0;
-  const RowsArgs a = rows_args(w, x_format, rows, nullptr);
-  return by_tiles(a, w->format, x_format) ? rows_tile_workspace(a, x_format) : 0;
+  return choice_workspace(choice_of(w, x_format, rows, false));
 }
 
 int mxrows_product(const mxrows_weight* w, int32_t x_format, const uint8_t* x,

@@ -8,6 +8,7 @@
 
 #include "../../include/mxrows.h"
 #include "gather_quotient.h"
+#include "rows_choice.h"
 
 namespace mxg {
 
@@ -20,11 +21,7 @@ namespace mxg {
 // block 2 s + g either way: the instruction's own order of K. Units lie [row
 // block][kb], 2048 or 4096 bytes each; scales [row block][kb / 2][lane] as words,
 // byte 2 (kb % 2) + s. kb runs to an even number, rows to 32: zeros with scale
-// byte 127.
-inline int unit_bytes(int format) { return format == MXG_MXFP4 ? 2048 : 4096; }
-inline int64_t row_blocks(int64_t n) { return (n + 31) / 32; }
-inline int64_t kb_pairs(int64_t k) { return (k + 255) / 256; }
-
+// byte 127. (Sizes: rows_choice.h.)
 struct RowsArgs {
   const uint8_t *w, *ws;  // packed
   const uint8_t *x, *xs;  // row-major codes and scales
@@ -40,10 +37,9 @@ struct RowsArgs {
 };
 
 hipError_t launch_rows_stream(const RowsArgs& a, int w_format, int x_format, hipStream_t s);
-// Bytes of a.partial that launch_rows_tile wants for these sizes (0: none).
-size_t rows_tile_workspace(const RowsArgs& a, int x_format);
-double rows_tile_us(const RowsArgs& a, int x_format);  // about its time
-hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, hipStream_t s);
+// By tiles; choice_workspace(h) bytes of a.partial are used.
+hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, const RowsChoice& h,
+                            hipStream_t s);
 // Its tiles for MXFP8 rows that are not to be `fast` (rows_bf16.hip).
 hipError_t launch_rows_bf16(const RowsArgs& a, int w_format, int row_tiles, int col_tiles,
                             int split, hipStream_t s);

@@ -31,7 +31,6 @@
 
 #include <hip/hip_runtime.h>
 
-#include <cmath>
 #include <type_traits>
 
 #include "tile_device.h"
@@ -522,95 +521,8 @@ __global__ void __launch_bounds__(64) join_kernel(RowsArgs a, int row_tiles, int
     *reinterpret_cast<uint4*>(a.out + (int64_t)(row + r32) * a.out_n + c) = u;
 }
 
-// What a launch is cut into: tiles of `side` rows of W and of x, K in `split` parts.
-struct Shape {
-  int side;
-  int64_t row_tiles, col_tiles;
-  int split;
-  double us;  // (of one weight)
-};
-
-int64_t row_tiles(const RowsArgs& a, int side) {
-  if (!a.offsets) return (a.rows + side - 1) / side;
-  return a.rows / side + (a.experts < a.rows ? a.experts : a.rows);
-}
-
-// The times that choose between them, in us, fitted to one MI355X's with W and x past the
-// caches (k in pairs of kb; MXFP4 and MXFP8 x). Tiles of 128, 256 or fewer: 4096 x 2048 6.3
-// and 9.4, 4096 x 4096 12 and 17, 4096 x 16384 33 and 50. Two on a CU: 1536 rows of 4096 x
-// 4096 24 and 34, 1024 of 7168 x 8192 43 and 63.
-double small_time(int64_t tiles, double kp, bool fp4) {
-  if (tiles <= 256) return 3 + kp * (fp4 ? 0.5 : 0.75);
-  return (double)((tiles + 511) / 512) * (4 + kp * (fp4 ? 1.17 : 1.95));
-}
-// Tiles of 256 with `h` blocks of 32 rows of x: 7168 x 8192 by 2 31 and 52, by 4 40 and 64,
-// by 8 62 and 94; 2048 rows of 4096 x 4096 (by 4) 24 and 35.
-double wide_time(int64_t tiles, double h, double kp, bool fp4) {
-  const double pair = fp4 ? 0.55 + 0.14 * h : 1 + 0.23 * h;
-  return (double)((tiles + 255) / 256) * (4 + 0.9 * h + kp * pair);
-}
-// What a divided K adds: a launch, the parts and their FP32 sums, written and read. Rows of
-// 4096 x 16384 in MXFP4 with 1, 2 and 4 parts: 128 33, 23 and 18; 256 33, 24 and 23; 512 35
-// and 30; 512 of 4096 x 4096 13 and 20. 32 of 2048 x 8192 in MXFP8 16 with 16 parts, 64 12
-// with 8.
-double join_time(int split, double rows, double n) {
-  return 3 + 0.4 * split + split * rows * n * 8 / 3.5e6;
-}
-
-// Tiles of 128 in BF16 (rows_bf16.hip) with up to 64 rows of x and with up to 128: 2048 x
-// 2048 13.6 and 18.3, 4096 x 4096 22.6 and 31, 1024 x 8192 41 and 56; 224 of 8192 59 (MXFP4)
-// and 65. With 2, 4 and 8 parts of 64 rows 128 rows of 1024 x 8192 25.8, 17.3 and 14.9, of 4096
-// x 4096 18.5 and 17.1 with 2 and 4; 203 of 4096 x 16384 40.6 with 4 by 128, 47 with 2 by 64.
-double bf16_time(int64_t tiles, int64_t rows, double kp) {
-  return (double)((tiles + 255) / 256) * (rows <= 64 ? 4.4 + 1.15 * kp : 5.5 + 1.58 * kp);
-}
-double bf16_join_time(int split, double rows, double n) {
-  return 2 + 0.2 * split + split * rows * n * 8 / 3.5e6;
-}
-
-Shape shape_of(const RowsArgs& a, int x_format) {
-  Shape big = {256, row_tiles(a, 256), (a.nb + 7) / 8, 1, 0};
-  Shape s = {128, row_tiles(a, 128), (a.nb + 3) / 4, 1, 0};
-  const bool bf16 = x_format == MXG_MXFP8 && !a.fast;
-  if (a.offsets) {
-    // Groups end in tiles that are half empty on average; only many rows a group, and
-    // more tiles than CUs, make up for the larger tile's.
-    const int64_t groups = a.experts < a.rows ? a.experts : a.rows;
-    const int64_t tiles = (a.rows / 256 + groups / 2) * big.col_tiles;
-    return !bf16 && a.rows / groups >= 256 && tiles >= 256 ? big : s;
-  }
-  const bool fp4 = x_format == MXG_MXFP4;
-  const int64_t blocks = (a.rows + 31) / 32;
-  const double read = 2.5 + (double)a.w_bytes / 6.2e6;  // W, once
-  // Tiles of 128 rows of x, and in BF16 of 64 too, with K whole and divided.
-  s.us = INFINITY;
-  const int64_t col_tiles = s.col_tiles, most = s.row_tiles;
-  for (int64_t row_tiles : {most, bf16 ? (blocks + 1) / 2 : most}) {
-    const int64_t tiles = row_tiles * col_tiles, rows = (blocks + row_tiles - 1) / row_tiles * 32;
-    for (int split = 1; split <= 16; split *= 2) {
-      if (split > 1 && (tiles * split > 256 || a.kp < 2 * split)) break;
-      const double kp = (double)a.kp / split;
-      const double join = split == 1 ? 0
-                          : bf16     ? bf16_join_time(split, a.rows, a.n)
-                                     : join_time(split, a.rows, a.n);
-      const double t =
-          fmax(bf16 ? bf16_time(tiles, rows, kp) : small_time(tiles, kp, fp4), read) + join;
-      if (t < s.us) s = Shape{128, row_tiles, col_tiles, split, t};
-    }
-  }
-  if (bf16) return s;
-  // Of large tiles as many down the rows as the last round of workgroups has room for:
-  // lower ones.
-  const int64_t rounds = (big.row_tiles * big.col_tiles + 255) / 256;
-  const int64_t fit = rounds * 256 / big.col_tiles;
-  if (fit > big.row_tiles) big.row_tiles = fit < blocks ? fit : blocks;
-  const double h = (double)((blocks + big.row_tiles - 1) / big.row_tiles);
-  big.us = wide_time(big.row_tiles * big.col_tiles, h, a.kp, fp4);
-  return big.us < s.us ? big : s;
-}
-
 template <int FW, int FX, int RW, int RX, int WW, int WX, bool DEEP>
-hipError_t launch(const RowsArgs& a, const Shape& h, hipStream_t s) {
+hipError_t launch(const RowsArgs& a, const RowsChoice& h, hipStream_t s) {
   using T = Tile<FW, FX, RW, RX, WW, WX, DEEP>;
   static_assert(T::kRows == 32 * T::kNW, "");
   const unsigned grid = tile_grid(h.row_tiles * h.col_tiles * h.split, T::kThreads);
@@ -621,7 +533,7 @@ hipError_t launch(const RowsArgs& a, const Shape& h, hipStream_t s) {
 }
 
 // (of tiles of 128 by 128)
-hipError_t launch_join(const RowsArgs& a, const Shape& h, hipStream_t s) {
+hipError_t launch_join(const RowsArgs& a, const RowsChoice& h, hipStream_t s) {
   const dim3 joins((unsigned)(h.row_tiles * h.col_tiles * 8), a.gated ? 2 : 4);
   if (a.gated)
     hipLaunchKernelGGL((join_kernel<2, 2, 2, 2, true>), joins, dim3(64), 0, s, a,
@@ -633,7 +545,7 @@ hipError_t launch_join(const RowsArgs& a, const Shape& h, hipStream_t s) {
 }
 
 template <int FW, int FX>
-hipError_t by_size(const RowsArgs& a, const Shape& h, hipStream_t s) {
+hipError_t by_size(const RowsArgs& a, const RowsChoice& h, hipStream_t s) {
   if (h.side == 256) return launch<FW, FX, 2, 8, 4, 1, false>(a, h, s);
   return h.row_tiles * h.col_tiles * h.split <= 256 ? launch<FW, FX, 2, 2, 2, 2, true>(a, h, s)
                                                     : launch<FW, FX, 2, 2, 2, 2, false>(a, h, s);
@@ -641,19 +553,12 @@ hipError_t by_size(const RowsArgs& a, const Shape& h, hipStream_t s) {
 
 }  // namespace
 
-size_t rows_tile_workspace(const RowsArgs& a, int x_format) {
-  const Shape h = shape_of(a, x_format);
-  return h.split > 1 ? (size_t)(h.row_tiles * h.col_tiles) * h.split * 4 * h.side * h.side : 0;
-}
-
-double rows_tile_us(const RowsArgs& a, int x_format) { return shape_of(a, x_format).us; }
-
-hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, hipStream_t s) {
-  const Shape h = shape_of(a, x_format);
+hipError_t launch_rows_tile(const RowsArgs& a, int w_format, int x_format, const RowsChoice& h,
+                            hipStream_t s) {
   hipError_t e;
   if (x_format == MXG_MXFP4)
     e = by_size<MXG_MXFP4, MXG_MXFP4>(a, h, s);
-  else if (!a.fast)
+  else if (x_format == MXG_MXFP8)
     e = launch_rows_bf16(a, w_format, (int)h.row_tiles, (int)h.col_tiles, h.split, s);
   else if (w_format == MXG_MXFP4)
     e = by_size<MXG_MXFP4, MXG_MXFP8>(a, h, s);

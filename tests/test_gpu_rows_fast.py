@@ -25,8 +25,9 @@ def dv():
 
 
 # Streams, K divided, tiles of 128 alone on a CU and by two, tiles of 256.
-SIZES = [(1, 40, 128), (8, 96, 1024), (33, 136, 4096), (130, 520, 8320), (40, 264, 16384), (289, 1032, 128),
-         (289, 1032, 640), (289, 1032, 1408), (1100, 4104, 256), (1100, 4104, 640), (2060, 4104, 128), (2060, 4104, 1152)]
+SIZES = [(1, 40, 128), (8, 96, 1024), (33, 136, 4096), (130, 520, 8320), (40, 264, 16384), (200, 1088, 16512),
+         *((289, 1032, k) for k in (128, 256, 384, 512, 640, 768, 1024, 1152, 1408, 1664, 2176)),
+         *((1100, 4104, k) for k in (128, 256, 384, 640, 896, 1280)), *((2060, 4104, k) for k in (128, 384, 512, 1152))]
 
 
 @pytest.mark.parametrize("gated", [False, True])

@@ -11,7 +11,9 @@ namespace {
 
 // 1024 bytes from base + off (a lane's 16) to LDS at `to` (wave-uniform), and
 // COUNT - 1 times the next 1024 to the next 1024. The compiler does not see these
-// loads: their end is waited for with s_waitcnt vmcnt.
+// loads: their end is waited for with s_waitcnt vmcnt. (m0 is a reserved register: it
+// cannot be named as clobbered, and the compiler writes it itself right before an
+// instruction of its own that reads it, of which these kernels have none.)
 template <int COUNT>
 __device__ __forceinline__ void copy_kib(uint32_t to, const uint8_t* base, uint32_t off) {
   to = __builtin_amdgcn_readfirstlane(to);

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include "mx_device.h"
+#include "quant_device.h"
 #include "rows_internal.h"
 
 namespace mxg {
@@ -37,13 +38,6 @@ __device__ __forceinline__ void load8(const void* p, int64_t at, float (&v)[8]) 
   }
 }
 
-// Maximum over the 4 lanes of a quad; all lanes active.
-__device__ __forceinline__ uint32_t quad_max_u32(uint32_t a) {
-  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xF, 0xF, true));
-  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x4E, 0xF, 0xF, true));
-  return a;
-}
-
 // The scale byte of a block whose largest magnitude has these FP32 bits: with
 // amax = (1 + f) 2^(E - 127), amax <= 6 2^e = 1.5 2^(e + 2) holds first at e = E -
 // 129 where f <= 1/2 and at E - 128 otherwise; never below -127. Subnormal FP32
@@ -62,7 +56,7 @@ __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint32_t* scale)
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  const uint32_t sb = *scale = fp4_scale_byte(quad_max_u32(amax));
+  const uint32_t sb = *scale = fp4_scale_byte(quad_max(amax));
   uint32_t codes = 0;
   if (sb == 0xFFu) {
 #pragma unroll

@@ -13,18 +13,20 @@ namespace {
 //
 // A counting sort that keeps the order of equal keys (the only atomics add whole
 // numbers in LDS). Workgroups take contiguous chunks of the pairs, waves contiguous
-// parts of a chunk. Bucket e
-// < experts holds expert e's pairs, bucket `experts` those without one. A pair's
-// place is the sum of what lies before its bucket, of its bucket in earlier
-// workgroups, in earlier waves and in earlier pairs of its wave; the last comes
-// from matching the 64 keys of a round bit by bit.
+// parts of a chunk. Bucket e < experts holds expert e's pairs, bucket `experts` those
+// without one. A pair's place is the sum of what lies before its bucket, of its bucket
+// in earlier workgroups, in earlier waves and in earlier pairs of its wave; the last
+// comes from matching the 64 keys of a round bit by bit.
 //
 // One workgroup does it in one launch. More of them count first, in a launch of
 // their own (a row of the workspace each), and each then sums the rows itself:
-// with at most kMostGroups of them that costs less than a third launch.
+// with at most kMostGroups of them that costs less than a third launch. The second
+// launch reads and matches its keys again, to count before the workspace's rows and to
+// place behind them.
 //
-// Bound by latency: 64 pairs 3.1 us, 131072 pairs of 256 experts 10.8 (12.7 and 15.3 by
-// chunks of 2048 and 4096).
+// Bound by latency: 64 pairs 3.1 us, 1024 of 256 experts 4.1, 2048 5.6, 4096 8.4; by more
+// than one workgroup 4104 pairs 7.6 (no workspace up to there), 131072 10.8 (12.7 and 15.3
+// by chunks of 2048 and 4096), 300000 15.6.
 
 constexpr int kSortWaves = 16;
 constexpr int kSortThreads = 64 * kSortWaves;

@@ -8,8 +8,12 @@
 // holds neighbouring columns of a row of y. W lies in global memory as the instruction's
 // lanes take it (rows_internal.h) and goes to LDS by whole KiB; x goes there by rows,
 // swizzled. Both are copied without registers in between, stages ahead of the products,
-// behind counted waits and one barrier a stage; operands come to registers one step
-// ahead; sums stay in the accumulators. FP32 sums, rounded once, at the end.
+// behind one barrier and one wait a stage; operands come to registers one step ahead; sums
+// stay in the accumulators. FP32 sums, rounded once, at the end. The wait counts the loads
+// that may still fly, but small tiles by two with equal formats have a ring of two stages
+// and wait for all. In the tiles of 256, which hold every register of a SIMD, four words of
+// a lane's addresses lie in scratch; one comes back right behind the wait for the first
+// stage, and its own wait is for all the stages copied by then.
 //
 // A tile is 256 rows of W by up to 256 of x, one workgroup with all of a CU's registers,
 // where there are enough of them (4096 rows of 7168 x 8192 in MXFP4 124 us, 3.9 PFLOP/s;
@@ -18,14 +22,17 @@
 // let the matrix cores run at 7.4 PFLOP/s at 1.80 GHz with nothing else; here the products
 // alone take 44 us of 56 (4096 x 4096 x 8192), 47 with the operand reads, 52 with the
 // copies instead, and the clock falls to 1.5 GHz (without products 37 us at 2.15 GHz). Per
-// workgroup 3.5 us before the first product (5.8 with an order) and 5 to 6 us of results.
+// workgroup 3.5 us before the first product (5.8 with an order) and 5 to 6 us of results:
+// an order's entries are loaded one after the other, 3 to 6 of x's rows before the first
+// copy, and with results that go by it 16 or 32 of theirs behind the last product (4096 x 8
+// rows of 64 experts of 7168 x 2048 in MXFP4 403 us in place, 463 scattered).
 //
-// Else a tile is 128 by 128, on a CU alone or by two, K divided where too few (203 rows of
-// 4096 x 16384 in MXFP4 by MXFP8 20 us and 4 to add up; 512 of 7168 x 8192 26 us in MXFP4,
-// 44 in MXFP8). Those are bound by copies out of L2, 32 KiB for 128 x 128 x 256 products
-// in MXFP4, and by their starts and ends.
+// Else a tile is 128 by 128, on a CU alone or by two, K divided where too few (512 rows of
+// 7168 x 8192 26 us in MXFP4; fast, 203 of 4096 x 16384 in MXFP4 by MXFP8 20 us and 4 to add
+// up, 512 of 7168 x 8192 in MXFP8 44). Those are bound by copies out of L2, 32 KiB for 128 x
+// 128 x 256 products in MXFP4, and by their starts and ends.
 //
-// Left out: 128-row tiles for large problems (shape_of), tiles of 128 x 256 with a divided
+// Left out: 128-row tiles for large problems (rows_choice.h), tiles of 128 x 256 with a divided
 // K (level), copies past the caches (52 -> 60 us), XCD runs of 16 or 64 tiles and groups
 // of 4 or 16 row tiles (within 2 %).
 
@@ -50,7 +57,7 @@ struct Tile {
   static constexpr int kWaves = WW * WX, kThreads = 64 * kWaves;
   // Bytes of a row of x in a stage. A CU copies whole lines of 128 bytes out of L2 at 125
   // bytes a ns, halves at 72: that bounds a small tile (203 rows of 4096 x 16384 in MXFP4
-  // by MXFP8 27 us with whole lines, 31 with halves). A large one reads less of x for its
+  // by MXFP8, fast, 27 us with whole lines, 31 with halves). A large one reads less of x for its
   // products and is as fast with halves, of which a ring holds more stages.
   static constexpr int kLine = RX == 2 ? 128 : 64;
   static constexpr int kPer = kLine / (FX == MXG_MXFP4 ? 32 : 64);  // steps of a stage
@@ -371,9 +378,11 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
     if constexpr (T::kLefts > 1)
       if (pair + 1 < kp) whole(Int<1>(), pair++);
     whole(Int<0>(), pair);
-    // The sums are read no sooner than the last products have ended: 32 wait states. The
-    // compiler puts 19 behind an MXFP8 product of 64 cycles; in a form of this kernel with a
-    // wave more, the last product's last sum was then read without it.
+    // The sums are read no sooner than 32 wait states behind the last product: a guard. The
+    // compiler counts 19 behind an MXFP8 product of 64 cycles, which is that product's length;
+    // a form of this kernel with a wave more read the last product's last sum without it, and
+    // the cause is not shown. (Small tiles by two run two waves on a SIMD as well; they have
+    // not shown it.)
 #pragma unroll
     for (int t = 0; t < NX; ++t)
 #pragma unroll
@@ -407,7 +416,7 @@ rows_tile_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
       constexpr int kLanes = kWidth / 8;             // of 16 bytes, for a row
       const int col = ct * (kTwo ? 16 : 32) * T::kNW + ww * kWidth + 8 * (lane % kLanes);
       constexpr int kTimes = 32 * kLanes / 64;  // stores of a lane for 32 rows
-      int to[NX][kTimes];                       // all rows' targets in one round trip
+      int to[NX][kTimes];                       // (one round trip for each)
 #pragma unroll
       for (int t = 0; t < NX; ++t)
 #pragma unroll

@@ -1,4 +1,4 @@
-"""The sums of products with MXFP8 rows on an MI355X: FP32 keeps what lies 2^-14 below the largest product beside it, as
+"""The sums of products of any number of rows on an MI355X, of MXFP8 rows above all: FP32 keeps what lies 2^-14 below the largest product beside it, as
 mxgemm and mxmoe_experts do, for any number of rows and by every kernel. Inputs whose large products cancel leave results
 made of small ones alone; every partial sum of them is an FP32 value in any order, so that the results are the exact sums,
 rounded once to BF16."""
@@ -74,12 +74,13 @@ def test_experts(dv, w_form, groups, k, form):
     assert torch.equal(got[cuda(written)], _rounded(exact)[cuda(written)])
 
 
-@pytest.mark.parametrize("w_form", W_FORMS)
-@pytest.mark.parametrize("rows,n,k", [(2, 128, 2048), (70, 320, 4096), (300, 1088, 1152), (1100, 4160, 512)])
-def test_the_bound_of_the_decode_projection(dv, w_form, rows, n, k):
+@pytest.mark.parametrize("w_form,x_form", [("mxfp4", "mxfp8"), ("mxfp8", "mxfp8"), ("mxfp4", "mxfp4")])
+@pytest.mark.parametrize("rows,n,k", [(2, 128, 2048), (70, 320, 4096), (130, 576, 8320), (300, 1088, 1152),
+                                      (1100, 4160, 512), (2060, 4160, 1152)])
+def test_the_bound_of_the_decode_projection(dv, w_form, x_form, rows, n, k):
     """Random operands: within a BF16 step and 1e-6 of the sum of magnitudes (a gated row's gate and up each)."""
     rng = np.random.default_rng(rows * n + k)
-    w, x = weights(rng, w_form, n, k), weights(rng, "mxfp8", rows, k)
+    w, x = weights(rng, w_form, n, k), weights(rng, x_form, rows, k)
     w[1][...] += rng.integers(0, 3, w[1].shape, dtype=np.uint8)
     args = *map(cuda, w), *map(cuda, x)
     exact = oracle.product(*w, *x)[0]

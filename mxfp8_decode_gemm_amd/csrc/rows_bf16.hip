@@ -376,13 +376,13 @@ rows_bf16_kernel(RowsArgs a, int row_tiles, int col_tiles, int split) {
 
 hipError_t launch_rows_bf16(const RowsArgs& a, int w_format, int row_tiles, int col_tiles,
                             int split, hipStream_t s) {
-  const unsigned grid = tile_grid((int64_t)row_tiles * col_tiles * split, kThreads);
-  if (grid == 0) return hipErrorInvalidValue;
+  const TileGrid g = tile_grid((int64_t)row_tiles * col_tiles * split);
+  const dim3 grid(g.x, g.y);
   if (w_format == MXG_MXFP4)
-    hipLaunchKernelGGL((rows_bf16_kernel<MXG_MXFP4>), dim3(grid), dim3(kThreads), 0, s, a,
+    hipLaunchKernelGGL((rows_bf16_kernel<MXG_MXFP4>), grid, dim3(kThreads), 0, s, a,
                        row_tiles, col_tiles, split);
   else
-    hipLaunchKernelGGL((rows_bf16_kernel<MXG_MXFP8>), dim3(grid), dim3(kThreads), 0, s, a,
+    hipLaunchKernelGGL((rows_bf16_kernel<MXG_MXFP8>), grid, dim3(kThreads), 0, s, a,
                        row_tiles, col_tiles, split);
   return hipGetLastError();
 }

@@ -42,6 +42,20 @@ struct RowsChoice {
   double us;  // (of one weight)
 };
 
+constexpr int kRun = 32;  // tiles side by side on one XCD
+
+// The grid of a launch of so many tiles, a workgroup each: whole runs, in rows of 2^20 where
+// there are more (a row's threads have to be countable in 32 bits).
+struct TileGrid {
+  unsigned x, y;
+};
+inline TileGrid tile_grid(int64_t tiles) {
+  const int64_t unit = tiles < 8 * kRun ? 8 : 8 * kRun, most = 1 << 20;
+  const int64_t grid = (tiles + unit - 1) / unit * unit;
+  if (grid <= most) return {(unsigned)grid, 1};
+  return {(unsigned)most, (unsigned)((grid + most - 1) / most)};
+}
+
 // Bytes of the sums of a divided K.
 inline size_t choice_workspace(const RowsChoice& c) {
   return c.split > 1 ? (size_t)(c.row_tiles * c.col_tiles) * c.split * 4 * c.side * c.side : 0;

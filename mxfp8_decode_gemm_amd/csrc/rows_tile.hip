@@ -534,9 +534,8 @@ template <int FW, int FX, int RW, int RX, int WW, int WX, bool DEEP>
 hipError_t launch(const RowsArgs& a, const RowsChoice& h, hipStream_t s) {
   using T = Tile<FW, FX, RW, RX, WW, WX, DEEP>;
   static_assert(T::kRows == 32 * T::kNW, "");
-  const unsigned grid = tile_grid(h.row_tiles * h.col_tiles * h.split, T::kThreads);
-  if (grid == 0) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((rows_tile_kernel<FW, FX, RW, RX, WW, WX, DEEP>), dim3(grid),
+  const TileGrid g = tile_grid(h.row_tiles * h.col_tiles * h.split);
+  hipLaunchKernelGGL((rows_tile_kernel<FW, FX, RW, RX, WW, WX, DEEP>), dim3(g.x, g.y),
                      dim3(T::kThreads), 0, s, a, (int)h.row_tiles, (int)h.col_tiles, h.split);
   return hipGetLastError();
 }

@@ -50,8 +50,6 @@ __device__ __forceinline__ void tile_at(int number, int row_tiles, int col_tiles
   *rt = group * kGroup + (in - *ct * high);
 }
 
-constexpr int kRun = 32;  // tiles side by side on one XCD
-
 template <int N>
 __device__ __forceinline__ void wait_loads() {
   static_assert(N < 64, "");
@@ -61,17 +59,10 @@ __device__ __forceinline__ void wait_loads() {
 // Workgroups go to the XCDs in turn: runs of 32 tiles stay on one, of fewer where
 // there are not 256.
 __device__ __forceinline__ int tile_of_workgroup() {
-  const int run_of = min((int)gridDim.x / 8, kRun), bid = blockIdx.x;
+  const int run_of = min((int)gridDim.x / 8, kRun);
+  const int bid = (int)(blockIdx.y * gridDim.x + blockIdx.x);
   const int round = bid / (8 * kRun) * (8 * kRun);
   return round + (bid & 7) * run_of + ((bid - round) >> 3);
-}
-
-// Workgroups of a launch of so many tiles, whole runs of them; 0 where a grid cannot be
-// that large.
-inline unsigned tile_grid(int64_t tiles, int threads) {
-  const int64_t unit = tiles < 8 * kRun ? 8 : 8 * kRun;
-  const int64_t grid = (tiles + unit - 1) / unit * unit;
-  return grid * threads > UINT32_MAX ? 0 : (unsigned)grid;
 }
 
 }  // namespace

@@ -14,6 +14,13 @@ PROGRAM = """
 #include <cstdio>
 using namespace mxg;
 int main() {
+  // Grids: whole runs, at least the tiles, threads of a row in 32 bits.
+  for (int64_t t : {1, 7, 8, 255, 256, 257, 4096, 1 << 20, (1 << 20) + 1, 8978432, 1082130432}) {
+    const TileGrid g = tile_grid(t);
+    if ((int64_t)g.x * g.y < t || (uint64_t)g.x * 512 > 0xFFFFFFFFu || g.y > 65535 || g.x % 8 ||
+        (t >= 256 && g.x % 256) || (g.y > 1 && (int64_t)g.x * (g.y - 1) >= t))
+      return 1;
+  }
   int a[8];
   while (scanf("%d %d %d %d %d %d %d %d", a, a + 1, a + 2, a + 3, a + 4, a + 5, a + 6, a + 7) == 8) {
     const RowsChoice c = rows_choice(rows_problem(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7]));

@@ -165,3 +165,35 @@ def test_nan_codes_stay_in_their_rows_and_columns(dv, rows, w_form):
     got = dv.Linear(*map(cuda, w))(*map(cuda, x))
     want = torch.from_numpy(oracle.product(*w, *x)[0]).cuda()
     assert torch.equal(got.isnan(), want.isnan()) and got[1:3].isnan().all() and not got[3:, 10:70].isnan().any()
+
+
+@pytest.mark.parametrize("rows,n,k", [(7, 264, 2048), (130, 520, 8320), (300, 1032, 640)])
+@pytest.mark.parametrize("w_form", W_FORMS)
+def test_captured_with_values_that_come_to_leave_bf16(dv, w_form, rows, n, k):
+    """One graph, replayed on rows that BF16 holds, that it does not hold, and again that it holds, with eager work and a
+    call on another stream between: the eager results each time."""
+    rng = np.random.default_rng(rows)
+    lin = dv.Linear(*map(cuda, weights(rng, w_form, n, k)))
+    inputs = [weights(rng, "mxfp8", rows, k) for _ in range(3)]
+    inputs[1][1][::2, 3] = 1                              # (rows scaled by 2^-126 in one block)
+    inputs[1][1][1, 5] = 255
+    x, xs = map(cuda, inputs[0])
+    lin(x, xs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = lin(x, xs)
+    side = torch.cuda.Stream()
+    for i in (0, 1, 2, 1, 0):
+        x.copy_(cuda(inputs[i][0]))
+        xs.copy_(cuda(inputs[i][1]))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        want = lin(x, xs)
+        other = lin(x, xs, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+        assert torch.equal(other.view(torch.int16), want.view(torch.int16))
+        assert bool(want.isnan().any()) == (i == 1)

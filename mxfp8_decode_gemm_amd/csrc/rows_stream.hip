@@ -13,8 +13,9 @@
 //
 // One row of 7168 x 8192 in MXFP4 7.7 us (31 MB, 4.1 TB/s; a wave asks for the next 256 of K
 // when it has multiplied the last), 8 in MXFP8 13.0 us (4.7 TB/s; fast 14.4); 8 tokens x 8 of
-// 64 experts of 4096 x 7168 gated, MXFP4 by MXFP8, 106 us (656 MB, 6.2 TB/s; fast 101). Left out: units in a
-// register ring of 2 to 6 (experts slower, one weight level), 16 waves, 64 rows of x.
+// 64 experts of 4096 x 7168 gated, MXFP4 by MXFP8, 96 to 108 us (656 MB, 6.1 to 6.8 TB/s; fast
+// 101). Left out: units in a register ring of 2 to 6 (experts slower, one weight level), 16
+// waves, 64 rows of x.
 
 #include <hip/hip_runtime.h>
 
